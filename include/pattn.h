@@ -63,10 +63,25 @@ typedef enum {
 typedef enum {
   PATTN_KV_BF16 = 0,      /* K and V stored as bf16                          */
   PATTN_KV_FP8_E4M3 = 1,  /* K and V stored as e4m3 bytes, one fp32 scale each */
-  PATTN_KV_F16 = 2        /* K and V stored as f16; q and out are f16 too (the
+  PATTN_KV_F16 = 2,       /* K and V stored as f16; q and out are f16 too (the
                              FlashAttention backend supports float16 and
                              bfloat16 models)                                 */
+  PATTN_KV_FP8_E4M3_ROW = 3 /* K and V stored as e4m3 bytes with one fp32 scale
+                             per (token, KV head) row of K and of V, in a
+                             buffer of their own (see PATTN_ROW_SCALE_MIN)    */
 } pattn_kv_dtype_t;
+
+/*
+ * The scales of a PATTN_KV_FP8_E4M3_ROW cache: fp32 [num_blocks][block_size / 16]
+ * [num_kv_heads][2][16], on the device, 16-B aligned.  Slot i of block b stands
+ * for code * scale with scale = row_scales[b][i / 16][head][0 for K, 1 for V]
+ * [i % 16].  (So the scales that go with 16 slots of one head are one 128-byte
+ * line, and those of neighbouring heads follow it.)  Scales are within
+ * [PATTN_ROW_SCALE_MIN, PATTN_ROW_SCALE_MAX] = [2^-60, 2^60]; the writers below
+ * keep to it.
+ */
+#define PATTN_ROW_SCALE_MIN 8.673617379884035e-19f
+#define PATTN_ROW_SCALE_MAX 1.152921504606847e+18f
 
 /*
  * Host-side sizes and resources of one call.  Everything a device-pointer API
@@ -156,7 +171,9 @@ typedef struct {
  *                   q is scaled per row into f16 (the decode kernel likewise
  *                   per head)
  *   kv_scale        host float[2] {k_scale, v_scale}; required for e4m3, ignored
- *                   for bf16 (may be NULL)
+ *                   for bf16 (may be NULL).  For PATTN_KV_FP8_E4M3_ROW: the
+ *                   [device] row scales (layout at PATTN_ROW_SCALE_MIN), 16-B
+ *                   aligned; the scales of keys at or past seq_len are not used
  *   ext             host sizes, workspace and stream (see pattn_ext_t)
  *
  * Returns PATTN_OK once the work is enqueued.  Host-side checks return
@@ -343,6 +360,130 @@ pattn_status_t pattn_reshape_and_cache_diffkv(const void* key, const void* value
                                               int head_size_v, int block_size, int num_blocks,
                                               int kv_dtype, unsigned* device_status,
                                               void* stream);
+
+/*
+ * pattn_reshape_and_cache_rows -- pattn_reshape_and_cache for a
+ * PATTN_KV_FP8_E4M3_ROW cache: each (token, KV head) row of K and of V is
+ * stored with a scale of its own,
+ *   scale = max|x| / 448 clamped to [2^-60, 2^60] (NaN elements do not count),
+ *   code  = e4m3(x / scale), fp32 division, round to nearest even, saturated
+ *           at +-448, NaN stays NaN.
+ * An infinity (and a magnitude above 448 * 2^60) is stored as the largest code.
+ *
+ *   key, value      [device] bf16 [num_tokens, num_kv_heads, head_size]
+ *   kv_cache        [device] e4m3 bytes, the cache of pattn_varlen_fwd
+ *   row_scales      [device] the cache's scales, updated in place
+ *   head_size       a multiple of 16, at most 256
+ *   the rest        as for pattn_reshape_and_cache
+ */
+pattn_status_t pattn_reshape_and_cache_rows(const void* key, const void* value, void* kv_cache,
+                                            float* row_scales, const int64_t* slot_mapping,
+                                            int num_tokens, int num_kv_heads, int head_size,
+                                            int block_size, int num_blocks,
+                                            unsigned* device_status, void* stream);
+
+/*
+ * pattn_rope_and_cache -- rotary embedding of q and k and the cache write of k
+ * and v, in one kernel: what a layer does between its q/k/v projection and
+ * pattn_varlen_fwd.
+ *
+ * For token t: each q head and each k head is first normed if its weight is
+ * given, x <- x * w / sqrt(mean(x^2) + norm_eps); then its first rot_dim
+ * elements are rotated pair by pair,
+ *   (a, b) -> (a c - b s, b c + a s),  c = cos_sin[P][i],
+ *   s = cos_sin[P][rot_dim / 2 + i] for rotary pair i,
+ *   P = positions[axis of pair i][t].
+ * q goes to q_out, k and v to the cache slot slot_mapping[t], stored as kv_dtype
+ * says: PATTN_KV_BF16 / PATTN_KV_F16 rounded to that type (q, key and value are
+ * then of it too; they are bf16 with the e4m3 caches), PATTN_KV_FP8_E4M3 and
+ * PATTN_KV_FP8_E4M3_ROW quantised as pattn_reshape_and_cache and
+ * pattn_reshape_and_cache_rows do.  The norm, the rotation and the quantisation
+ * are fp32 with one rounding at the end.
+ *
+ * Either q (with q_out) or key (with value) may be NULL, and is then left out.
+ */
+typedef struct {
+  size_t struct_size;     /* sizeof(pattn_rope_t)                             */
+  const void* q;          /* [device] [num_tokens] rows of num_heads * head_size;
+                             token t's at q + t * q_stride elements           */
+  void* q_out;            /* [device] likewise with q_out_stride; may be q itself
+                             with the same stride, else must not overlap it   */
+  const void* key;        /* [device] rows of num_kv_heads * head_size        */
+  const void* value;      /* [device] likewise                                */
+  long long q_stride, q_out_stride, key_stride, value_stride;
+                          /* elements between tokens, multiples of 8 and at least
+                             a token's row (so q, key and value may be parts of
+                             one packed projection); all buffers 16-B aligned */
+  const float* cos_sin;   /* [device] fp32 [max_position][rot_dim]: the cosines of
+                             the rot_dim / 2 pairs, then their sines; 16-B aligned */
+  const int64_t* positions; /* [device] [num_axes] rows of num_tokens         */
+  long long positions_stride; /* elements between the axes' rows              */
+  const unsigned char* pair_axis; /* host [rot_dim / 2]: the axis whose position
+                             turns pair i; NULL with one axis                 */
+  const void* q_norm;     /* [device] [head_size] weight of the norm of q heads, of
+                             q's type, or NULL for no norm                    */
+  const void* k_norm;     /* [device] likewise for k heads                    */
+  void* kv_cache;         /* [device] the cache of pattn_varlen_fwd, updated  */
+  float* row_scales;      /* [device] PATTN_KV_FP8_E4M3_ROW: the row scales, updated */
+  const float* kv_scale;  /* PATTN_KV_FP8_E4M3: host float[2] {k_scale, v_scale} */
+  const int64_t* slot_mapping; /* [device] [num_tokens], as for
+                             pattn_reshape_and_cache: negative writes no key and
+                             value (q is still rotated)                       */
+  unsigned* device_status; /* [device] optional (may be NULL): a slot past the
+                             pool (its key and value are not written) and a
+                             position outside the table (nothing of the token is
+                             written) OR bit 1 into it                        */
+  void* stream;           /* cudaStream_t; NULL = the legacy default stream   */
+  float norm_eps;         /* finite, >= 0                                     */
+  int num_tokens;
+  int num_heads;
+  int num_kv_heads;
+  int head_size;          /* a multiple of 16, at most 256                    */
+  int rot_dim;            /* a multiple of 16, at most head_size              */
+  int interleaved;        /* 0: pair i is elements (i, i + rot_dim / 2);
+                             1: elements (2 i, 2 i + 1)                       */
+  int num_axes;           /* 0: no rotation; 1: one position per token; 2..4  */
+  int max_position;       /* rows of cos_sin.  A token whose first axis' position
+                             is negative is padding: nothing of it is written */
+  int kv_dtype;
+  int block_size;         /* a multiple of 16                                 */
+  int num_blocks;
+} pattn_rope_t;
+
+/* Returns PATTN_OK once enqueued; argument errors before any CUDA call;
+ * PATTN_ERR_CUDA if the launch fails.  Allocates nothing, never synchronises. */
+pattn_status_t pattn_rope_and_cache(const pattn_rope_t* args);
+
+/*
+ * pattn_gather_cache -- read ranges of the cache back into contiguous rows (to
+ * hand a prefix to another instance, or to a kernel that wants dense K and V).
+ *
+ * Request r's output rows are [out_start_loc[r], out_start_loc[r + 1]); row
+ * out_start_loc[r] + i holds its key key_starts[r] + i.  A code of an e4m3
+ * cache becomes code * scale (fp32), rounded once to bf16; 16-bit caches are
+ * copied.
+ *
+ *   kv_cache, block_table, kv_dtype, kv_scale   as for pattn_varlen_fwd
+ *   key_starts      [device] int32 [num_seqs], or NULL for 0
+ *   out_start_loc   [device] int32 [num_seqs + 1], non-decreasing
+ *   key_out, value_out   [device] [num_rows, num_kv_heads, head_size], bf16 (f16
+ *                   for PATTN_KV_F16), 16-B aligned; rows outside
+ *                   [out_start_loc[0], out_start_loc[num_seqs]) are left as they
+ *                   are, and no row at or past num_rows is written
+ *   head_size       a multiple of 8
+ *   device_status   [device] optional (may be NULL): a key outside its block-table
+ *                   row or a block id outside the pool zeroes the output row and
+ *                   ORs bit 1 into this word
+ *
+ * Returns PATTN_OK once enqueued; argument errors before any CUDA call;
+ * PATTN_ERR_CUDA if the launch fails.  Allocates nothing, never synchronises.
+ */
+pattn_status_t pattn_gather_cache(const void* kv_cache, const int32_t* block_table,
+                                  const int32_t* key_starts, const int32_t* out_start_loc,
+                                  void* key_out, void* value_out, int num_seqs, int num_rows,
+                                  int max_blocks_per_seq, int num_blocks, int num_kv_heads,
+                                  int head_size, int block_size, int kv_dtype,
+                                  const float* kv_scale, unsigned* device_status, void* stream);
 
 /* A static, human-readable name for a status code. */
 const char* pattn_status_string(int status);

@@ -19,6 +19,7 @@ from . import _build
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
 KV_F16 = 2  # f16 cache; q and out are f16 too
+KV_FP8_E4M3_ROW = 3  # e4m3 cache with one fp32 scale per (token, KV head) row
 MAX_SPLITS = 64
 
 STATUS = {0: "PATTN_OK", 1: "PATTN_ERR_INVALID_ARGUMENT", 2: "PATTN_ERR_UNSUPPORTED",
@@ -29,7 +30,8 @@ EXPORTS = ("pattn_varlen_fwd", "pattn_workspace_bytes", "pattn_decode_splits",
            "pattn_read_device_status", "pattn_status_string", "pattn_version",
            "pattn_decode_fwd_static", "pattn_reshape_and_cache",
            "pattn_reshape_and_cache_diffkv", "pattn_cascade_fwd",
-           "pattn_cascade_workspace_bytes")
+           "pattn_cascade_workspace_bytes", "pattn_reshape_and_cache_rows",
+           "pattn_rope_and_cache", "pattn_gather_cache")
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -49,6 +51,25 @@ class Ext(ctypes.Structure):
                 ("stream", ctypes.c_void_p),
                 ("timing_events", ctypes.POINTER(ctypes.c_void_p)),
                 ("sinks", ctypes.c_void_p), ("head_size_v", ctypes.c_int)]
+
+
+class RopeArgs(ctypes.Structure):
+    """pattn_rope_t"""
+    _fields_ = ([("struct_size", ctypes.c_size_t)] +
+                [(n, ctypes.c_void_p) for n in ("q", "q_out", "key", "value")] +
+                [(n, ctypes.c_longlong) for n in ("q_stride", "q_out_stride", "key_stride",
+                                                  "value_stride")] +
+                [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                 ("positions_stride", ctypes.c_longlong)] +
+                [(n, ctypes.c_void_p) for n in ("pair_axis", "q_norm", "k_norm", "kv_cache",
+                                                "row_scales", "kv_scale", "slot_mapping",
+                                                "device_status", "stream")] +
+                [("norm_eps", ctypes.c_float)] +
+                [(n, ctypes.c_int) for n in ("num_tokens", "num_heads", "num_kv_heads",
+                                             "head_size", "rot_dim", "interleaved", "num_axes",
+                                             "max_position", "kv_dtype", "block_size",
+                                             "num_blocks")])
+
 
 PHASES = ("plan", "prefill", "decode", "combine")
 
@@ -95,9 +116,40 @@ def load(path=None):
     lib.pattn_reshape_and_cache.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, vp, vp, vp]
     lib.pattn_reshape_and_cache_diffkv.restype = i
     lib.pattn_reshape_and_cache_diffkv.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp]
+    lib.pattn_reshape_and_cache_rows.restype = i
+    lib.pattn_reshape_and_cache_rows.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
+    lib.pattn_rope_and_cache.restype = i
+    lib.pattn_rope_and_cache.argtypes = [ctypes.POINTER(RopeArgs)]
+    lib.pattn_gather_cache.restype = i
+    lib.pattn_gather_cache.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp]
     if path is None:
         _lib = lib
     return lib
+
+
+def _scale_arg(kv_dtype, kv_scale):
+    """kv_scale as the C ABI takes it: host float[2], or for KV_FP8_E4M3_ROW the
+    device address of the row scales (a tensor or its address)."""
+    if kv_scale is None:
+        return None
+    if kv_dtype == KV_FP8_E4M3_ROW:
+        return kv_scale if isinstance(kv_scale, int) else kv_scale.data_ptr()
+    return (ctypes.c_float * 2)(float(kv_scale[0]), float(kv_scale[1]))
+
+
+def row_scales_shape(num_blocks, block_size, num_kv_heads):
+    """Shape of the fp32 row scales of a KV_FP8_E4M3_ROW cache: slot i of block b
+    is scaled by scales[b, i // 16, head, 0 (K) or 1 (V), i % 16]."""
+    return (num_blocks, block_size // 16, num_kv_heads, 2, 16)
+
+
+def _check_row_scales(scales, num_blocks, block_size, num_kv_heads, device):
+    import torch
+    if (not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32 or
+            scales.device != device or not scales.is_contiguous() or
+            scales.numel() != num_blocks * block_size * num_kv_heads * 2):
+        raise ValueError("kv_scale of a KV_FP8_E4M3_ROW cache must be a contiguous fp32 tensor of "
+                         "shape row_scales_shape(...) on the cache's device")
 
 
 def pattn_reshape_and_cache(key, value, kv_cache, slot_mapping, num_tokens, num_kv_heads,
@@ -106,9 +158,7 @@ def pattn_reshape_and_cache(key, value, kv_cache, slot_mapping, num_tokens, num_
     """Raw call of the KV-cache write with integer device pointers; returns
     the status code."""
     lib = lib or load()
-    ks = None
-    if kv_scale is not None:
-        ks = (ctypes.c_float * 2)(float(kv_scale[0]), float(kv_scale[1]))
+    ks = _scale_arg(kv_dtype, kv_scale)
     return lib.pattn_reshape_and_cache(key, value, kv_cache, slot_mapping, int(num_tokens),
                                        int(num_kv_heads), int(head_size), int(block_size),
                                        int(num_blocks), int(kv_dtype), ks,
@@ -120,10 +170,22 @@ def reshape_and_cache(key, value, kv_cache, slot_mapping, *, block_size, kv_dtyp
     """pattn_reshape_and_cache on torch tensors: key/value bf16 [T, Hkv, d],
     kv_cache [2, num_blocks, block_size, Hkv, d] (bf16, or uint8 e4m3 codes),
     slot_mapping int64 [T].  ``device_status``: optional int32/uint32 tensor of
-    one element that collects the out-of-pool bit.  Raises PattnError."""
+    one element that collects the out-of-pool bit.  With KV_FP8_E4M3_ROW
+    ``kv_scale`` is the cache's row-scale tensor, updated as well
+    (pattn_reshape_and_cache_rows).  Raises PattnError."""
     import torch
     if stream is None:
         stream = torch.cuda.current_stream(key.device)
+    if kv_dtype == KV_FP8_E4M3_ROW:
+        _check_row_scales(kv_scale, kv_cache.shape[1], block_size, key.shape[1], kv_cache.device)
+        st = load().pattn_reshape_and_cache_rows(
+            key.data_ptr(), value.data_ptr(), kv_cache.data_ptr(), kv_scale.data_ptr(),
+            slot_mapping.data_ptr(), key.shape[0], key.shape[1], key.shape[2], int(block_size),
+            kv_cache.shape[1], None if device_status is None else device_status.data_ptr(),
+            stream.cuda_stream)
+        if st != 0:
+            raise PattnError(st, "pattn_reshape_and_cache_rows")
+        return kv_cache
     st = pattn_reshape_and_cache(key.data_ptr(), value.data_ptr(), kv_cache.data_ptr(),
                                  slot_mapping.data_ptr(), key.shape[0], key.shape[1],
                                  key.shape[2], block_size, kv_cache.shape[1], kv_dtype, kv_scale,
@@ -150,6 +212,180 @@ def reshape_and_cache_diffkv(key, value, kv_cache, slot_mapping, *, block_size,
     if st != 0:
         raise PattnError(st, "pattn_reshape_and_cache_diffkv")
     return kv_cache
+
+
+def rope_pair_axis(sections, interleaved=False):
+    """The axis of each rotary pair, for rope_and_cache.  ``sections``: pairs per
+    axis, e.g. (16, 24, 24).  In order, or ``interleaved``: the axes take turns
+    (0, 1, 2, 0, 1, 2, ...) while each still has pairs left and pairs without a
+    partner go to the first axis."""
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    n_axes, total = len(sections), sum(sections)
+    out = [0] * total
+    for a in range(1, n_axes):
+        for p in list(range(a, total, n_axes))[:sections[a]]:
+            out[p] = a
+    if [out.count(a) for a in range(n_axes)] != list(sections):
+        raise ValueError("sections cannot take turns")
+    return out
+
+
+def _rows_of(x, name, dtype):
+    """(address, elements between tokens) of a [T, heads, head_size] tensor whose
+    token rows are contiguous."""
+    if x.dim() != 3 or x.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor [num_tokens, heads, head_size]")
+    T, H, D = x.shape
+    st, sh, sd = x.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return x.data_ptr(), (st if T > 1 else H * D)
+
+
+def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *, block_size,
+                   kv_dtype=KV_BF16, kv_scale=None, interleaved=False, pair_axis=None,
+                   q_norm=None, k_norm=None, norm_eps=1e-6, q_out=None, device_status=None,
+                   stream=None):
+    """pattn_rope_and_cache on torch tensors: rotates q and k, writes q to
+    ``q_out`` (default: a new tensor; ``q`` itself for in place) and k and v into
+    the cache.
+
+    q [T, H, d], key and value [T, Hkv, d], each with contiguous token rows at
+    any token stride (views of one packed projection); q or key with value may
+    be None.  kv_cache, ``kv_dtype``, ``kv_scale``: as for ``forward``
+    (KV_FP8_E4M3_ROW: the row scales, updated too).  positions: int64 [T], or
+    [axes, T] with ``pair_axis`` the axis of each rotary pair (see
+    ``rope_pair_axis``), or None for no rotation.  cos_sin: fp32
+    [max_position, rot_dim], cosines then sines.  ``q_norm``, ``k_norm``: [d]
+    weights of a root-mean-square norm per head.  ``device_status``: optional
+    int32/uint32 tensor of one element that collects bit 1 for slots past the
+    pool and positions outside the table.  Returns ``q_out``; raises PattnError
+    or ValueError."""
+    import torch
+    x = q if q is not None else key
+    if x is None:
+        raise ValueError("rope_and_cache needs q or key")
+    dt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
+    dev = x.device
+    a = RopeArgs()
+    a.struct_size = ctypes.sizeof(RopeArgs)
+    T, a.head_size = x.shape[0], x.shape[2]
+    a.num_tokens = T
+    if q is not None:
+        a.q, a.q_stride = _rows_of(q, "q", dt)
+        a.num_heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        elif q_out.shape != q.shape or q_out.device != dev:
+            raise ValueError("q_out must have q's shape and device")
+        a.q_out, a.q_out_stride = _rows_of(q_out, "q_out", dt)
+    if key is not None:
+        if (value is None or key.shape != value.shape or key.shape[0] != T or
+                key.shape[2] != a.head_size or key.device != dev or value.device != dev):
+            raise ValueError("key and value must be [num_tokens, num_kv_heads, head_size] like q")
+        a.key, a.key_stride = _rows_of(key, "key", dt)
+        a.value, a.value_stride = _rows_of(value, "value", dt)
+        Hkv, NB = key.shape[1], kv_cache.shape[1]
+        if (tuple(kv_cache.shape) != (2, NB, block_size, Hkv, a.head_size) or
+                not kv_cache.is_contiguous() or kv_cache.device != dev or
+                kv_cache.element_size() != (1 if kv_dtype in (KV_FP8_E4M3, KV_FP8_E4M3_ROW) else 2)):
+            raise ValueError("kv_cache must be a contiguous [2, num_blocks, block_size, "
+                             "num_kv_heads, head_size] tensor of the cache's type")
+        if (slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or
+                slot_mapping.device != dev or not slot_mapping.is_contiguous()):
+            raise ValueError("slot_mapping must be a contiguous int64 [num_tokens] tensor")
+        a.num_kv_heads, a.num_blocks = Hkv, NB
+        a.kv_cache, a.slot_mapping = kv_cache.data_ptr(), slot_mapping.data_ptr()
+        if kv_dtype == KV_FP8_E4M3_ROW:
+            _check_row_scales(kv_scale, NB, block_size, Hkv, dev)
+            a.row_scales = kv_scale.data_ptr()
+        elif kv_dtype == KV_FP8_E4M3 and kv_scale is not None:
+            scale = _scale_arg(kv_dtype, kv_scale)
+            a.kv_scale = ctypes.addressof(scale)
+    a.kv_dtype, a.block_size = int(kv_dtype), int(block_size)
+    if positions is not None:
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if (positions.dtype != torch.int64 or positions.shape[-1] != T or positions.dim() > 2 or
+                positions.device != dev or (T > 1 and positions.stride(-1) != 1)):
+            raise ValueError("positions must be int64 [num_tokens] or [axes, num_tokens]")
+        if (cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.device != dev or
+                not cos_sin.is_contiguous()):
+            raise ValueError("cos_sin must be a contiguous fp32 [max_position, rot_dim] tensor")
+        a.positions, a.num_axes = positions.data_ptr(), axes
+        a.positions_stride = positions.stride(0) if axes > 1 else T
+        a.cos_sin = cos_sin.data_ptr()
+        a.max_position, a.rot_dim = cos_sin.shape
+        if axes > 1:
+            if pair_axis is None or len(pair_axis) != a.rot_dim // 2:
+                raise ValueError("positions of several axes need pair_axis with rot_dim / 2 entries")
+            pairs = bytes(pair_axis)
+            a.pair_axis = ctypes.cast(ctypes.c_char_p(pairs), ctypes.c_void_p)
+    a.interleaved = int(interleaved)
+    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is not None:
+            if w.dtype != dt or w.shape != (a.head_size,) or w.device != dev or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dt} [head_size] tensor")
+            setattr(a, name, w.data_ptr())
+    a.norm_eps = norm_eps
+    if device_status is not None:
+        a.device_status = device_status.data_ptr()
+    if T == 0:  # (an empty tensor has no address)
+        return q_out
+    a.stream = (stream or torch.cuda.current_stream(dev)).cuda_stream
+    st = load().pattn_rope_and_cache(ctypes.byref(a))
+    if st != 0:
+        raise PattnError(st, "pattn_rope_and_cache")
+    return q_out
+
+
+def gather_cache(kv_cache, block_table, out_start_loc, *, num_rows, block_size, kv_dtype=KV_BF16,
+                 kv_scale=None, key_starts=None, key_out=None, value_out=None,
+                 device_status=None, stream=None):
+    """pattn_gather_cache on torch tensors: the keys and values of request r's
+    positions key_starts[r] (default 0), ... into rows out_start_loc[r] ...
+    out_start_loc[r + 1] of ``key_out`` and ``value_out`` [num_rows, Hkv, d]
+    (default: new tensors; bf16, f16 for KV_F16).  kv_cache, ``kv_dtype``,
+    ``kv_scale``: as for ``forward``.  Returns (key_out, value_out); raises
+    PattnError or ValueError."""
+    import torch
+    dev = kv_cache.device
+    NB, Hkv, D = kv_cache.shape[1], kv_cache.shape[3], kv_cache.shape[4]
+    if kv_cache.shape[2] != block_size or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be a contiguous [2, num_blocks, block_size, num_kv_heads, "
+                         "head_size] tensor")
+    if kv_cache.element_size() != (1 if kv_dtype in (KV_FP8_E4M3, KV_FP8_E4M3_ROW) else 2):
+        raise ValueError("kv_cache must be of the cache's type")
+    B = block_table.shape[0]
+    for name, x, shape in (("block_table", block_table, (B, block_table.shape[1])),
+                           ("out_start_loc", out_start_loc, (B + 1,)),
+                           ("key_starts", key_starts, (B,))):
+        if x is not None and (x.dtype != torch.int32 or x.shape != shape or x.device != dev or
+                              not x.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+    if kv_dtype == KV_FP8_E4M3_ROW:
+        _check_row_scales(kv_scale, NB, block_size, Hkv, dev)
+    dt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
+    shape = (num_rows, Hkv, D)
+    if key_out is None:
+        key_out = torch.empty(shape, dtype=dt, device=dev)
+    if value_out is None:
+        value_out = torch.empty(shape, dtype=dt, device=dev)
+    for x in (key_out, value_out):
+        if x.shape != shape or x.dtype != dt or x.device != dev or not x.is_contiguous():
+            raise ValueError(f"key_out and value_out must be contiguous {dt} tensors of shape {shape}")
+    if num_rows == 0 or B == 0:  # (an empty tensor has no address)
+        return key_out, value_out
+    st = load().pattn_gather_cache(
+        kv_cache.data_ptr(), block_table.data_ptr(),
+        None if key_starts is None else key_starts.data_ptr(), out_start_loc.data_ptr(),
+        key_out.data_ptr(), value_out.data_ptr(), B, int(num_rows), block_table.shape[1], NB, Hkv, D,
+        int(block_size), int(kv_dtype), _scale_arg(kv_dtype, kv_scale),
+        None if device_status is None else device_status.data_ptr(),
+        (stream or torch.cuda.current_stream(dev)).cuda_stream)
+    if st != 0:
+        raise PattnError(st, "pattn_gather_cache")
+    return key_out, value_out
 
 
 def pattn_cascade_workspace_bytes(ext, num_heads, num_kv_heads, head_size, block_size,
@@ -188,9 +424,7 @@ def cascade_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scal
     ws = (workspace or _default_ws).get(need, dev)
     ext.workspace = ws.data_ptr()
     ext.workspace_bytes = ws.numel()
-    ks = None
-    if kv_scale is not None:
-        ks = (ctypes.c_float * 2)(float(kv_scale[0]), float(kv_scale[1]))
+    ks = _scale_arg(kv_dtype, kv_scale)
     st = load().pattn_cascade_fwd(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
                                   seq_lens.data_ptr(), query_start_loc.data_ptr(), out.data_ptr(),
                                   float(scale), int(num_heads), int(num_kv_heads), int(head_size),
@@ -228,9 +462,7 @@ def pattn_varlen_fwd(q, kv_cache, block_table, seq_lens, query_start_loc, out, s
                      kv_dtype, kv_scale, ext, lib=None):
     """Raw call with integer device pointers; returns the status code."""
     lib = lib or load()
-    ks = None
-    if kv_scale is not None:
-        ks = (ctypes.c_float * 2)(float(kv_scale[0]), float(kv_scale[1]))
+    ks = _scale_arg(kv_dtype, kv_scale)
     return lib.pattn_varlen_fwd(q, kv_cache, block_table, seq_lens, query_start_loc, out,
                                 float(scale), int(num_heads), int(num_kv_heads),
                                 int(head_size), int(block_size), int(window), int(causal),
@@ -244,9 +476,7 @@ def pattn_decode_fwd_static(q, kv_cache, block_table, seq_lens, query_start_loc,
     """Raw call of the workspace-free decode entry point; returns the status.
     For callers that cannot allocate device memory (see include/pattn.h)."""
     lib = lib or load()
-    ks = None
-    if kv_scale is not None:
-        ks = (ctypes.c_float * 2)(float(kv_scale[0]), float(kv_scale[1]))
+    ks = _scale_arg(kv_dtype, kv_scale)
     return lib.pattn_decode_fwd_static(q, kv_cache, block_table, seq_lens, query_start_loc,
                                        out, float(scale), int(num_heads), int(num_kv_heads),
                                        int(head_size), int(block_size), int(window),

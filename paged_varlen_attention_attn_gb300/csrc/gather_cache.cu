@@ -1,0 +1,191 @@
+// gather_cache.cu -- reading ranges of the paged cache back into contiguous
+// 16-bit rows (sm_103a).
+//
+// Output row i belongs to request r with out_start_loc[r] <= i <
+// out_start_loc[r + 1] and holds key key_starts[r] + i - out_start_loc[r]:
+// codes of an e4m3 cache are multiplied by their scale in fp32 and rounded
+// once, 16-bit rows are copied.
+//
+// Bound by HBM (a row-scaled e4m3 row of 128 is 132 bytes read and 256
+// written).  A warp takes ROWS_PER_WARP output rows of K or of V: that many
+// lanes find their row's request (binary search) and block, the results go
+// round by shuffles, and the loads of all rows are independent.
+#include <cmath>
+
+#include "../../include/pattn.h"
+#include "common.cuh"
+#include "internal.h"
+
+namespace pattn {
+namespace {
+
+constexpr int GC_THREADS = 128;
+constexpr int ROWS_PER_WARP = 4;
+
+struct GatherParams {
+  const void* cache;
+  const float* row_scales;
+  const int* block_table;
+  const int* key_starts;
+  const int* osl;
+  void* out[2];
+  unsigned* status;
+  float scale[2];
+  int B, rows, mbps, NB, Hkv, D, bs;
+};
+
+// KIND: the cache (PATTN_KV_*); the 16-bit kinds copy bits.
+template <int KIND>
+__global__ void __launch_bounds__(GC_THREADS)
+    gather_cache_kernel(const __grid_constant__ GatherParams p) {
+  constexpr bool Q8 = KIND == PATTN_KV_FP8_E4M3 || KIND == PATTN_KV_FP8_E4M3_ROW;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (GC_THREADS / 32) + (threadIdx.x >> 5);
+  const int kv = static_cast<int>(unit & 1);
+  const int64_t first = (unit >> 1) * ROWS_PER_WARP;
+  if (first >= p.rows) return;
+  const int lane = threadIdx.x & 31;
+
+  // lane l < ROWS_PER_WARP: where output row first + l comes from
+  int64_t slot = -2;  // -2: leave the row, -1: zero it, else the cache slot
+  if (lane < ROWS_PER_WARP && first + lane < p.rows) {
+    const int row = static_cast<int>(first) + lane;
+    int lo = 0, hi = p.B;  // the last request that starts at or before the row
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.osl[mid] <= row) lo = mid;
+      else hi = mid;
+    }
+    const int at = p.osl[lo];
+    if (row >= at && row < p.osl[lo + 1]) {
+      const int64_t key = static_cast<int64_t>(p.key_starts ? p.key_starts[lo] : 0) + row - at;
+      int blk = -1;
+      if (key >= 0 && key < static_cast<int64_t>(p.mbps) * p.bs)
+        blk = p.block_table[static_cast<int64_t>(lo) * p.mbps + key / p.bs];
+      if (blk < 0 || blk >= p.NB) {
+        flag_status(p.status, PATTN_DEV_BAD_METADATA);
+        slot = -1;
+      } else {
+        slot = static_cast<int64_t>(blk) * p.bs + key % p.bs;
+      }
+    }
+  }
+  int64_t from[ROWS_PER_WARP];
+#pragma unroll
+  for (int r = 0; r < ROWS_PER_WARP; ++r) from[r] = __shfl_sync(0xffffffffu, slot, r);
+
+  const int row_elems = p.Hkv * p.D;
+  const int pieces = row_elems / 8;  // 8 elements each
+  uint16_t* out = static_cast<uint16_t*>(p.out[kv]) + first * row_elems;
+  const int64_t kv_base = static_cast<int64_t>(kv) * p.NB * p.bs;
+  for (int c = lane; c < pieces; c += 32) {
+    if constexpr (Q8) {
+      uint2 w[ROWS_PER_WARP];
+      float sc[ROWS_PER_WARP];
+      const int h = c * 8 / p.D;
+#pragma unroll
+      for (int r = 0; r < ROWS_PER_WARP; ++r) {
+        w[r] = make_uint2(0u, 0u);
+        sc[r] = p.scale[kv];
+        if (from[r] >= 0) {
+          w[r] = *reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(p.cache) +
+                                                 (kv_base + from[r]) * row_elems + c * 8);
+          if constexpr (KIND == PATTN_KV_FP8_E4M3_ROW)
+            // slot = block * bs + offset, so slot / 16 counts 16-slot groups
+            sc[r] = p.row_scales[((from[r] >> 4) * p.Hkv + h) * 32 + kv * 16 + (from[r] & 15)];
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < ROWS_PER_WARP; ++r) {
+        if (from[r] == -2) continue;
+        const unsigned u[4] = {w[r].x, w[r].x >> 16, w[r].y, w[r].y >> 16};
+        unsigned o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const unsigned h2 = e4m3x2_to_f16x2(u[e]);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+          o[e] = pack2<false>(f.x * sc[r], f.y * sc[r]);
+        }
+        *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * row_elems + c * 8) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    } else {
+      uint4 w[ROWS_PER_WARP];
+#pragma unroll
+      for (int r = 0; r < ROWS_PER_WARP; ++r) {
+        w[r] = make_uint4(0u, 0u, 0u, 0u);
+        if (from[r] >= 0)
+          w[r] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) +
+                                                 (kv_base + from[r]) * row_elems + c * 8);
+      }
+#pragma unroll
+      for (int r = 0; r < ROWS_PER_WARP; ++r)
+        if (from[r] != -2)
+          *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * row_elems + c * 8) = w[r];
+    }
+  }
+}
+
+}  // namespace
+}  // namespace pattn
+
+using namespace pattn;
+
+extern "C" pattn_status_t pattn_gather_cache(const void* kv_cache, const int32_t* block_table,
+                                             const int32_t* key_starts,
+                                             const int32_t* out_start_loc, void* key_out,
+                                             void* value_out, int num_seqs, int num_rows,
+                                             int max_blocks_per_seq, int num_blocks,
+                                             int num_kv_heads, int head_size, int block_size,
+                                             int kv_dtype, const float* kv_scale,
+                                             unsigned* device_status, void* stream) {
+  if (!kv_cache || !block_table || !out_start_loc || !key_out || !value_out)
+    return PATTN_ERR_INVALID_ARGUMENT;
+  if (num_seqs < 0 || num_rows < 0 || max_blocks_per_seq < 0 || num_blocks < 0 ||
+      num_kv_heads <= 0 || block_size <= 0 || block_size % 16 != 0)
+    return PATTN_ERR_INVALID_ARGUMENT;
+  if (head_size <= 0 || head_size % 8 != 0) return PATTN_ERR_UNSUPPORTED;
+  if (kv_dtype != PATTN_KV_BF16 && kv_dtype != PATTN_KV_FP8_E4M3 && kv_dtype != PATTN_KV_F16 &&
+      kv_dtype != PATTN_KV_FP8_E4M3_ROW)
+    return PATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_kv_heads) * head_size > (1 << 24)) return PATTN_ERR_UNSUPPORTED;
+  GatherParams p = {};
+  p.scale[0] = p.scale[1] = 1.f;
+  if (kv_dtype == PATTN_KV_FP8_E4M3) {
+    if (!kv_scale || !(kv_scale[0] > 0.f) || !(kv_scale[1] > 0.f) || !(kv_scale[0] < INFINITY) ||
+        !(kv_scale[1] < INFINITY))
+      return PATTN_ERR_INVALID_ARGUMENT;
+    p.scale[0] = kv_scale[0];
+    p.scale[1] = kv_scale[1];
+  }
+  if (kv_dtype == PATTN_KV_FP8_E4M3_ROW && !kv_scale) return PATTN_ERR_INVALID_ARGUMENT;
+  if ((reinterpret_cast<uintptr_t>(kv_cache) | reinterpret_cast<uintptr_t>(key_out) |
+       reinterpret_cast<uintptr_t>(value_out)) & 15)
+    return PATTN_ERR_INVALID_ARGUMENT;
+  if (num_rows == 0 || num_seqs == 0) return PATTN_OK;
+  p.cache = kv_cache;
+  p.row_scales = kv_dtype == PATTN_KV_FP8_E4M3_ROW ? kv_scale : nullptr;
+  p.block_table = block_table;
+  p.key_starts = key_starts;
+  p.osl = out_start_loc;
+  p.out[0] = key_out;
+  p.out[1] = value_out;
+  p.status = device_status;
+  p.B = num_seqs;
+  p.rows = num_rows;
+  p.mbps = max_blocks_per_seq;
+  p.NB = num_blocks;
+  p.Hkv = num_kv_heads;
+  p.D = head_size;
+  p.bs = block_size;
+  const long long units = 2LL * ((static_cast<long long>(num_rows) + ROWS_PER_WARP - 1) / ROWS_PER_WARP);
+  const unsigned grid = static_cast<unsigned>((units + GC_THREADS / 32 - 1) / (GC_THREADS / 32));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (kv_dtype) {
+    case PATTN_KV_FP8_E4M3: gather_cache_kernel<PATTN_KV_FP8_E4M3><<<grid, GC_THREADS, 0, st>>>(p); break;
+    case PATTN_KV_FP8_E4M3_ROW:
+      gather_cache_kernel<PATTN_KV_FP8_E4M3_ROW><<<grid, GC_THREADS, 0, st>>>(p);
+      break;
+    default: gather_cache_kernel<PATTN_KV_BF16><<<grid, GC_THREADS, 0, st>>>(p); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? PATTN_OK : PATTN_ERR_CUDA;
+}
