@@ -403,10 +403,13 @@ def cascade_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scal
     """pattn_cascade_fwd on torch tensors: pattn_varlen_fwd for a batch whose
     requests share their first common_prefix_len keys (same blocks).
     ``sinks``: optional fp32 [num_heads] device tensor of attention-sink logits.
-    Returns ``out``; raises PattnError."""
+    ``kv_scale``: (k_scale, v_scale), or the row-scale tensor of a
+    KV_FP8_E4M3_ROW cache.  Returns ``out``; raises PattnError."""
     import torch
     dev = q.device
     T = q.shape[0]
+    if kv_dtype == KV_FP8_E4M3_ROW:
+        _check_row_scales(kv_scale, kv_cache.shape[1], block_size, num_kv_heads, dev)
     if out is None:
         odt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
         out = torch.empty((T, num_heads, head_size), dtype=odt, device=dev)
@@ -544,7 +547,9 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
     """pattn_varlen_fwd on torch tensors (all on one CUDA device).
 
     max_query_len / max_seq_len are host ints (as in FlashAttentionMetadata):
-    the library never reads device memory on the host.  ``timing_events``:
+    the library never reads device memory on the host.  ``kv_scale``: (k_scale,
+    v_scale) of an e4m3 cache, or the row-scale tensor of a KV_FP8_E4M3_ROW cache
+    (see ``row_scales_shape``).  ``timing_events``:
     optional 8 raw cudaEvent_t handles (see pattn_ext_t).  ``sinks``: optional
     fp32 [num_heads] device tensor of attention-sink logits.  ``head_size_v``:
     > 0 selects the DiffKV cache layout [num_blocks, block_size, num_kv_heads,
@@ -561,6 +566,8 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     num_blocks = kv_cache.shape[0] if head_size_v else kv_cache.shape[1]
+    if kv_dtype == KV_FP8_E4M3_ROW:
+        _check_row_scales(kv_scale, num_blocks, block_size, num_kv_heads, dev)
     ext = make_ext(num_seqs=seq_lens.shape[0], num_tokens=T,
                    max_blocks_per_seq=block_table.shape[1], num_blocks=num_blocks,
                    max_query_len=max_query_len, max_seq_len=max_seq_len,

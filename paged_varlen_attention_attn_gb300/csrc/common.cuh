@@ -174,6 +174,16 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16) between 16-byte-aligned addresses.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, unsigned bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Named barrier over `count` threads (a multiple of 32) of the CTA; id 0 is
 // the one __syncthreads uses.
 __device__ __forceinline__ void named_bar_sync(unsigned id, unsigned count) {

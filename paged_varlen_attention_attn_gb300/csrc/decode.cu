@@ -52,7 +52,10 @@ __host__ __device__ constexpr int decode_head_group(int Hkv, int D, bool fp8) {
                           : 1;
 }
 
-template <int D, bool FP8, int NT, int HG, int WPH>
+// ROWS: an e4m3 cache with a scale per row; a unit's 32 scales of each head (16
+// of K, 16 of V, one 128-byte line) ride in a ring of their own beside the
+// stages.
+template <int D, bool FP8, int NT, int HG, int WPH, bool ROWS = false>
 struct DecodeCfg {
   static constexpr int ES = FP8 ? 1 : 2;
   static constexpr int RAW_ROW = D * ES;            // bytes of one key row of one head
@@ -75,7 +78,9 @@ struct DecodeCfg {
   static constexpr int MERGE_FLOATS = (D / 16) * NT * 4 + 4 * NT;
   static constexpr int MERGE_BYTES = (WPH - 1) * HG * MERGE_FLOATS * 32 * 4;
   static constexpr int RING_BYTES = NST * STAGE;
-  static constexpr int BAR_OFF = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
+  static constexpr int SC_UNIT = ROWS ? HG * 128 : 0;  // row scales of a unit
+  static constexpr int SC_OFF = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
+  static constexpr int BAR_OFF = SC_OFF + NST * SC_UNIT;
   // block ids of the next 32 units, one buffer per producer warp
   static constexpr int ID_OFF = BAR_OFF + 2 * NST * 8 <= BAR_OFF + 256 ? BAR_OFF + 256 : -1;
   static_assert(ID_OFF > 0, "barriers fit in 256 bytes");
@@ -196,11 +201,19 @@ __device__ __forceinline__ void merge_partitions(const Problem& p, int r, int h,
 
 // HALF: q, a 16-bit cache and out are f16 (else bf16; an e4m3 cache goes with
 // bf16 q and out).
-template <int D, bool FP8, int NT, int HG, int WPH, bool HALF>
-__global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH > 1 ? 2 : 1)
+//
+// ROWS: every key row of K and V has a scale, ks_k and vs_k.  Scores are
+// x_k = sl2 ks_k (q . ck_k) in log2 units; the weight that multiplies the V
+// codes is p_k vs_k = 2^(x_k + log2 vs_k), so the running reference is taken
+// over y_k = x_k + log2 vs_k: the packed f16 weights 2^(y_k - m) keep their
+// range whatever the V scales are, and the normaliser sum_k 2^(x_k - m) =
+// sum_k 2^(y_k - m) / vs_k is summed in fp32 beside them.
+template <int D, bool FP8, int NT, int HG, int WPH, bool HALF, bool ROWS>
+__global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH, ROWS>::THREADS, WPH > 1 ? 2 : 1)
     decode_split_kernel(const Problem p, const __grid_constant__ CUtensorMap kvmap, float sl2,
                         float out_scale) {
-  using C = DecodeCfg<D, FP8, NT, HG, WPH>;
+  using C = DecodeCfg<D, FP8, NT, HG, WPH, ROWS>;
+  static_assert(!ROWS || FP8, "row scales go with an e4m3 cache");
   constexpr int NST = C::NST;
   extern __shared__ unsigned char smem_raw[];
   // TMA's 128-byte swizzle is laid out from 1024-byte aligned boxes
@@ -326,7 +339,15 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
           const int key0 = (u_begin + i) * UNIT;
           const int slot = p.bs_shift >= 0 ? (key0 & (p.bs - 1)) : (key0 % p.bs);
           unsigned char* dst = smem + st * C::STAGE + kv * C::KV_UNIT;
-          mbar_arrive_expect_tx(&full[st], C::KV_UNIT);
+          // the two warps take turns with the row scales (neighbouring heads'
+          // lines: one copy of HG * 128 bytes)
+          const bool scales = ROWS && (i & 1) == kv;
+          mbar_arrive_expect_tx(&full[st], C::KV_UNIT + (scales ? C::SC_UNIT : 0));
+          if (scales)
+            bulk_load(smem + C::SC_OFF + st * C::SC_UNIT,
+                      p.row_scales + ((static_cast<int64_t>(ids[l]) * (p.bs >> 4) + (slot >> 4)) *
+                                          p.Hkv + grp * HG) * 32,
+                      C::SC_UNIT, &full[st]);
           if constexpr (FP8)
             tma_load_4d(dst, &kvmap, &full[st], 0, slot, grp * HG, kv * p.NB + ids[l]);
           else
@@ -426,10 +447,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
   // reference max of heads nt*8 + 2*c4 + h2 (identical across the lanes of
   // a column group), and the row sums of the weights, accumulated by MMAs in
   // the output fragment layout (every row of o_l holds the sums)
+  // (ROWS: the sums of each lane's own keys in l_run)
   float m_run[NT][2], l_run[NT][2], o_l[NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m_run[nt][0] = m_run[nt][1] = -INFINITY;
+    l_run[nt][0] = l_run[nt][1] = 0.f;
     o_l[nt][0] = o_l[nt][1] = o_l[nt][2] = o_l[nt][3] = 0.f;
   }
 
@@ -456,7 +479,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
     const int key_base = (u_begin + i0) * UNIT;
     // Rows at or past seq_len may hold anything (NaN included): zero this
     // head's rows (only the partition's last unit can have any).
-    if (key_base + nu * UNIT > s) {
+    // (with row scales also those below the window, in its first unit.)
+    if (key_base + nu * UNIT > s || (ROWS && key_base < kmin)) {
       const int u = nu - 1;
       unsigned char* sk = smem + ((i0 + u) % NST) * C::STAGE;
       unsigned char* sv = sk + C::KV_UNIT;
@@ -464,7 +488,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
       constexpr int CH_ROW = C::RAW_ROW / 16;
       for (int c = lane; c < UNIT * CH_ROW; c += 32) {
         const int j = c / CH_ROW, cc = c % CH_ROW;
-        if (key0 + j >= s) {
+        if (key0 + j >= s || (ROWS && key0 + j < kmin)) {
           *reinterpret_cast<uint4*>(sk + raw_off<D, FP8, HG>(hh, j, cc)) = make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(sv + raw_off<D, FP8, HG>(hh, j, cc)) = make_uint4(0, 0, 0, 0);
         }
@@ -531,17 +555,34 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
     // below 2^RESCALE_LOG2.  O and the row sums (accumulated by the same MMAs)
     // are relative to the same reference, so the final O / l is exact.
     float x[U][NT][4];
+    float iv[U][2];  // ROWS: 1 / vs of the lane's keys
     bool grow = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int ka = key_base + u * UNIT + quad, kb2 = ka + 8;
       const bool va = ka >= kmin && ka < kmax, vb = kb2 >= kmin && kb2 < kmax;
+      float ks[2] = {1.f, 1.f}, lv[2] = {0.f, 0.f};
+      if constexpr (ROWS) {
+        const float* sr = reinterpret_cast<const float*>(smem + C::SC_OFF +
+                                                         ((i0 + u) % NST) * C::SC_UNIT) +
+                          hh * 32 + quad;
+        ks[0] = sr[0];
+        ks[1] = sr[8];
+        // a masked key's scales may be anything
+        const float v0 = va ? sr[16] : 1.f, v1 = vb ? sr[24] : 1.f;
+        lv[0] = __log2f(v0);
+        lv[1] = __log2f(v1);
+        iv[u][0] = __fdividef(1.f, v0);
+        iv[u][1] = __fdividef(1.f, v1);
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = sc[u][0][nt][e] + sc[u][1][nt][e];
-          x[u][nt][e] = ((e < 2) ? va : vb) ? v * sl2h[nt][e & 1] : -INFINITY;
+          const float xs = ROWS ? v * (sl2h[nt][e & 1] * ks[e >> 1]) + lv[e >> 1]
+                                : v * sl2h[nt][e & 1];
+          x[u][nt][e] = ((e < 2) ? va : vb) ? xs : -INFINITY;
           grow |= x[u][nt][e] > m_run[nt][e & 1] + RESCALE_LOG2;
         }
     }
@@ -568,6 +609,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o_l[nt][e] *= alpha[nt][e & 1];
+        if constexpr (ROWS) {
+          l_run[nt][0] *= alpha[nt][0];
+          l_run[nt][1] *= alpha[nt][1];
+        }
 #pragma unroll
         for (int m = 0; m < D / 16; ++m)
 #pragma unroll
@@ -582,8 +627,14 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         // key quad / quad + 8, heads 2*c4, 2*c4+1
-        pk_lo[u][nt] = pack2<FP8 || HALF>(fast_exp2(x[u][nt][0] - r0), fast_exp2(x[u][nt][1] - r1));
-        pk_hi[u][nt] = pack2<FP8 || HALF>(fast_exp2(x[u][nt][2] - r0), fast_exp2(x[u][nt][3] - r1));
+        const float w0 = fast_exp2(x[u][nt][0] - r0), w1 = fast_exp2(x[u][nt][1] - r1);
+        const float w2 = fast_exp2(x[u][nt][2] - r0), w3 = fast_exp2(x[u][nt][3] - r1);
+        pk_lo[u][nt] = pack2<FP8 || HALF>(w0, w1);
+        pk_hi[u][nt] = pack2<FP8 || HALF>(w2, w3);
+        if constexpr (ROWS) {
+          l_run[nt][0] += w0 * iv[u][0] + w2 * iv[u][1];
+          l_run[nt][1] += w1 * iv[u][0] + w3 * iv[u][1];
+        }
       }
     }
 
@@ -644,10 +695,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
       }
       // Row sums l = 1^T P^T by the tensor core: every row of the all-ones A
       // tile gives each head's sum of this unit's (rounded) weights.
-      constexpr unsigned ONES = (FP8 || HALF) ? 0x3C003C00u : 0x3F803F80u;
+      if constexpr (!ROWS) {
+        constexpr unsigned ONES = (FP8 || HALF) ? 0x3C003C00u : 0x3F803F80u;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        mma_16816<FP8 || HALF>(o_l[nt], ONES, ONES, ONES, ONES, pb0[nt], pb1[nt]);
+        for (int nt = 0; nt < NT; ++nt)
+          mma_16816<FP8 || HALF>(o_l[nt], ONES, ONES, ONES, ONES, pb0[nt], pb1[nt]);
+      }
     }
     // Release the stages once every lane of every consumer warp has read them.
     __syncwarp();
@@ -659,10 +712,19 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
   }
 
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    l_run[nt][0] = o_l[nt][0];
-    l_run[nt][1] = o_l[nt][1];
-  }
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int h2 = 0; h2 < 2; ++h2) {
+      if constexpr (ROWS) {
+        // the lanes of a column group hold the sums of their own keys
+        float l = l_run[nt][h2];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l_run[nt][h2] = l + __shfl_xor_sync(0xffffffffu, l, 16);
+      } else {
+        l_run[nt][h2] = o_l[nt][h2];
+      }
+    }
 
   // ---------------------------------------------------------------- merge
   // The WPH warps of a KV head saw disjoint units of the partition: the
@@ -796,10 +858,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH>::THREADS, WPH >
   }
 }
 
-template <int D, bool FP8, int NT, int HG, int WPH, bool HALF>
+template <int D, bool FP8, int NT, int HG, int WPH, bool HALF, bool ROWS>
 cudaError_t launch_decode_t(const Problem& p, const CUtensorMap& kvmap) {
-  using C = DecodeCfg<D, FP8, NT, HG, WPH>;
-  auto kern = decode_split_kernel<D, FP8, NT, HG, WPH, HALF>;
+  using C = DecodeCfg<D, FP8, NT, HG, WPH, ROWS>;
+  auto kern = decode_split_kernel<D, FP8, NT, HG, WPH, HALF, ROWS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   // e4m3 data is widened to its f16 value; the per-tensor scales go here.
@@ -827,24 +889,25 @@ cudaError_t launch_decode_t(const Problem& p, const CUtensorMap& kvmap) {
 
 // Up to 8 query heads per KV head (one head tile): two warps per KV head
 // share each partition; more: one warp per KV head, two head tiles.
-template <int D, bool FP8, int HG, bool HALF>
+template <int D, bool FP8, int HG, bool HALF, bool ROWS>
 cudaError_t launch_decode_g(const Problem& p, const CUtensorMap& kvmap) {
-  return (p.G <= 8) ? launch_decode_t<D, FP8, 1, HG, 2, HALF>(p, kvmap)
-                    : launch_decode_t<D, FP8, 2, HG, 1, HALF>(p, kvmap);
+  return (p.G <= 8) ? launch_decode_t<D, FP8, 1, HG, 2, HALF, ROWS>(p, kvmap)
+                    : launch_decode_t<D, FP8, 2, HG, 1, HALF, ROWS>(p, kvmap);
 }
 
-template <int D, bool FP8, bool HALF>
+template <int D, bool FP8, bool HALF, bool ROWS = false>
 cudaError_t launch_decode_hg(const Problem& p, const CUtensorMap& kvmap) {
   switch (decode_head_group(p.Hkv, D, FP8)) {
-    case 4: return launch_decode_g<D, FP8, 4, HALF>(p, kvmap);
-    case 2: return launch_decode_g<D, FP8, 2, HALF>(p, kvmap);
-    default: return launch_decode_g<D, FP8, 1, HALF>(p, kvmap);
+    case 4: return launch_decode_g<D, FP8, 4, HALF, ROWS>(p, kvmap);
+    case 2: return launch_decode_g<D, FP8, 2, HALF, ROWS>(p, kvmap);
+    default: return launch_decode_g<D, FP8, 1, HALF, ROWS>(p, kvmap);
   }
 }
 
 template <int D>
 cudaError_t launch_decode_d(const Problem& p, const CUtensorMap& kvmap) {
   if (p.kv_dtype == PATTN_KV_FP8_E4M3) return launch_decode_hg<D, true, false>(p, kvmap);
+  if (p.kv_dtype == PATTN_KV_FP8_E4M3_ROW) return launch_decode_hg<D, true, false, true>(p, kvmap);
   if (p.kv_dtype == PATTN_KV_F16) return launch_decode_hg<D, false, true>(p, kvmap);
   return launch_decode_hg<D, false, false>(p, kvmap);
 }
@@ -856,7 +919,7 @@ cudaError_t launch_decode(const Problem& p, const CUtensorMap& kvmap) {
 }
 
 int decode_heads_per_cta(int Hkv, int D, int kv_dtype) {
-  return decode_head_group(Hkv, D, kv_dtype == PATTN_KV_FP8_E4M3);
+  return decode_head_group(Hkv, D, kv_is_e4m3(kv_dtype));
 }
 
 }  // namespace pattn

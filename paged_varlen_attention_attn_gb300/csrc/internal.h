@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/pattn.h"
+
 namespace pattn {
 
 // Prefill tiles are BLOCK_M query rows of one head.
@@ -35,6 +37,7 @@ struct Problem {
   int H, Hkv, G, D, bs, window, causal, kv_dtype;
   int bs_shift;  // log2(bs) when bs is a power of two, else -1
   float k_scale, v_scale;
+  const float* row_scales;  // PATTN_KV_FP8_E4M3_ROW: [NB][bs / 16][Hkv][2][16]
   int B, T, mbps, NB, max_q, max_s, splits;
   int bt_stride;     // row stride of block_table (>= mbps; the cascade suffix
                      // pass starts rows past the shared prefix)
@@ -100,6 +103,23 @@ struct Problem {
 extern "C" void pattn_test_set_wait_skip(int mode);
 int test_wait_skip();
 #endif
+
+// Whether the cache holds e4m3 codes (scaled per tensor or per row).
+__host__ __device__ constexpr bool kv_is_e4m3(int kv_dtype) { 
+  return kv_dtype == PATTN_KV_FP8_E4M3 || kv_dtype == PATTN_KV_FP8_E4M3_ROW;
+}
+
+// Checks a call's cache type and kv_scale (host only; the row scales of
+// PATTN_KV_FP8_E4M3_ROW are a device address).
+pattn_status_t check_kv_scale(int kv_dtype, const float* kv_scale);
+
+// Sets the scales of a Problem from a call's kv_scale argument.
+inline void set_scales(Problem& p, int kv_dtype, const float* kv_scale) {
+  const bool tensor = kv_dtype == PATTN_KV_FP8_E4M3, rows = kv_dtype == PATTN_KV_FP8_E4M3_ROW;
+  p.k_scale = tensor ? kv_scale[0] : 1.f;
+  p.v_scale = tensor ? kv_scale[1] : 1.f;
+  p.row_scales = rows ? kv_scale : nullptr;
+}
 
 // Workspace layout for a problem (offsets in bytes, 256-byte aligned).
 // The header and the counters come first, so one memset of counters_end

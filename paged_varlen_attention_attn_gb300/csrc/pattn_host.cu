@@ -135,15 +135,10 @@ pattn_status_t check_call(const void* q, const void* kv_cache, const int32_t* bl
     return PATTN_ERR_INVALID_ARGUMENT;
   if (!(scale >= 0.f) || std::isinf(scale)) return PATTN_ERR_INVALID_ARGUMENT;
   if (causal != 0 && causal != 1) return PATTN_ERR_INVALID_ARGUMENT;
-  if (kv_dtype != PATTN_KV_BF16 && kv_dtype != PATTN_KV_FP8_E4M3 && kv_dtype != PATTN_KV_F16)
-    return PATTN_ERR_UNSUPPORTED;
-  if (kv_dtype == PATTN_KV_FP8_E4M3) {
-    if (!kv_scale || !(kv_scale[0] > 0.f) || !(kv_scale[1] > 0.f) || std::isinf(kv_scale[0]) ||
-        std::isinf(kv_scale[1]))
-      return PATTN_ERR_INVALID_ARGUMENT;
-  }
+  v = check_kv_scale(kv_dtype, kv_scale);
+  if (v != PATTN_OK) return v;
   if (!causal && window > 0) return PATTN_ERR_UNSUPPORTED;
-  if (ext_head_size_v(ext) > 0 && kv_dtype == PATTN_KV_FP8_E4M3) return PATTN_ERR_UNSUPPORTED;
+  if (ext_head_size_v(ext) > 0 && kv_is_e4m3(kv_dtype)) return PATTN_ERR_UNSUPPORTED;
   // Prefill key tiles of the tensor-core kernel are 128 keys: a page must
   // divide the tile or be a whole number of tiles.
   if (ext->max_query_len > 1 && !(BLOCK_N % block_size == 0 || block_size % BLOCK_N == 0))
@@ -167,7 +162,7 @@ pattn_status_t check_call(const void* q, const void* kv_cache, const int32_t* bl
 // not depend on it.
 void set_cost_model(Problem& p) {
   p.num_sms = sm_count();
-  const bool fp8 = p.kv_dtype == PATTN_KV_FP8_E4M3;
+  const bool fp8 = kv_is_e4m3(p.kv_dtype);
   p.pf_us_per_tile = (p.D == 128 ? 2.1f : 1.3f) * (fp8 ? 1.3f : 1.f);
   p.dec_bytes_per_us = fp8 ? 100000.f : 120000.f;
   p.hbm_bytes_per_us = 0.85f * 6800000.f;
@@ -189,8 +184,7 @@ void base_problem(Problem& p, const void* q, const void* kv_cache, void* out, fl
   p.bs = block_size;
   p.bs_shift = (block_size & (block_size - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(block_size)) : -1;
   p.kv_dtype = kv_dtype;
-  p.k_scale = (kv_dtype == PATTN_KV_FP8_E4M3) ? kv_scale[0] : 1.f;
-  p.v_scale = (kv_dtype == PATTN_KV_FP8_E4M3) ? kv_scale[1] : 1.f;
+  set_scales(p, kv_dtype, kv_scale);
   p.T = ext->num_tokens;
   p.NB = ext->num_blocks;
   p.rows_per_item = prefill_rows_per_item(p.G);
@@ -303,7 +297,7 @@ bool encode_kv_map(CUtensorMap* map, const void* kv_cache, int kv_dtype, int D, 
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  if (kv_dtype == PATTN_KV_FP8_E4M3) {
+  if (kv_is_e4m3(kv_dtype)) {
     // e4m3 rows: for the prefill kernel's 8-bit score MMAs (d 128, v_groups
     // false) in the 128-byte-swizzled K-major layout; otherwise unswizzled,
     // into the ring stage where the producers widen them to the swizzled f16
@@ -359,7 +353,7 @@ bool encode_decode_map(CUtensorMap* map, const void* kv_cache, int kv_dtype, int
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  if (kv_dtype == PATTN_KV_FP8_E4M3) {
+  if (kv_is_e4m3(kv_dtype)) {
     const cuuint64_t row = static_cast<cuuint64_t>(D);
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(bs),
                           static_cast<cuuint64_t>(Hkv), 2ull * static_cast<cuuint64_t>(NB)};
@@ -398,6 +392,20 @@ bool encode_diffkv_map(CUtensorMap* map, const void* cache, int kv_dtype, int dk
              4, const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The cache type and its scales (host only).
+pattn_status_t check_kv_scale(int kv_dtype, const float* kv_scale) {
+  if (kv_dtype < PATTN_KV_BF16 || kv_dtype > PATTN_KV_FP8_E4M3_ROW) return PATTN_ERR_UNSUPPORTED;
+  if (kv_dtype == PATTN_KV_FP8_E4M3 &&
+      (!kv_scale || !(kv_scale[0] > 0.f) || !(kv_scale[1] > 0.f) || std::isinf(kv_scale[0]) ||
+       std::isinf(kv_scale[1])))
+    return PATTN_ERR_INVALID_ARGUMENT;
+  // the row scales are a device buffer
+  if (kv_dtype == PATTN_KV_FP8_E4M3_ROW &&
+      (!kv_scale || (reinterpret_cast<uintptr_t>(kv_scale) & 15)))
+    return PATTN_ERR_INVALID_ARGUMENT;
+  return PATTN_OK;
 }
 
 WsLayout workspace_layout(int B, int T, int H, int Hkv, int D, int max_q, int splits) {
@@ -584,8 +592,7 @@ pattn_status_t pattn_varlen_fwd(const void* q, const void* kv_cache, const int32
   p.window = window;
   p.causal = causal;
   p.kv_dtype = kv_dtype;
-  p.k_scale = (kv_dtype == PATTN_KV_FP8_E4M3) ? kv_scale[0] : 1.f;
-  p.v_scale = (kv_dtype == PATTN_KV_FP8_E4M3) ? kv_scale[1] : 1.f;
+  set_scales(p, kv_dtype, kv_scale);
   p.B = ext->num_seqs;
   p.T = ext->num_tokens;
   p.mbps = ext->max_blocks_per_seq;

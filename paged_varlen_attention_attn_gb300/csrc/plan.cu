@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Problem p) {
   const int np = ((p.G % 2) == 0 ? p.H / 2 : p.H) * p.kv_chunks;
   const int n_items = min(run, p.max_tiles) * np;  // (run: every thread has it)
   const float dec_bytes = static_cast<float>(s_dec_blocks) * static_cast<float>(p.bs * p.Hkv) *
-                          2.f * p.D * (p.kv_dtype == PATTN_KV_FP8_E4M3 ? 1.f : 2.f);
+                          2.f * p.D * (kv_is_e4m3(p.kv_dtype) ? 1.f : 2.f);
   const float work_items = static_cast<float>(s_tile_work) * np;
   float best = INFINITY;
   int best_gs = p.num_sms;

@@ -109,8 +109,16 @@ constexpr unsigned FULL = 0xffffffffu;
 template <bool FP8>
 __host__ __device__ constexpr int v_rows() { return FP8 ? BLOCK_N : 16; }
 
+// Row scales of a key tile (ROWS): eight 128-byte lines (16 K scales, 16 V
+// scales) of 16 keys each, in a ring of four tiles.  Four need no barrier of
+// their own for reuse: the K producer fetches tile j's scales after it has
+// waited for the scores of tile j - 3, whose issuers had waited for P and V of
+// tile j - 4, so every reader of that tile's scales is done.
+constexpr int SC_STAGES = 4;
+constexpr int SC_TILE = BLOCK_N / 16 * 128;
+
 // NK: e4m3 K codes used as they are (an e4m3 cache at d 128).
-template <int D, bool NK = false>
+template <int D, bool NK = false, bool ROWS = false>
 struct PrefillCfg {
   static constexpr int DH = D / 64;                 // 128-byte column blocks
   static constexpr int HALF = BLOCK_M * 128;        // bytes of one 128-row column block
@@ -123,7 +131,8 @@ struct PrefillCfg {
   static constexpr int Q_OFF = 0;                   // two Q tiles
   static constexpr int K_OFF = Q_OFF + 2 * TILE;
   static constexpr int V_OFF = K_OFF + PF_KST * KSTAGE;
-  static constexpr int BAR_OFF = V_OFF + VST * TILE;
+  static constexpr int SC_OFF = V_OFF + VST * TILE;
+  static constexpr int BAR_OFF = SC_OFF + (ROWS ? SC_STAGES * SC_TILE : 0);
   // + barriers + alignment slack; at least 116 KB so one CTA holds an SM (and
   // its 512 TMEM columns) alone
   static constexpr int SMEM_RAW = BAR_OFF + 512 + 1024;
@@ -148,6 +157,7 @@ struct Bars {
   uint64_t q_empty;     // every S MMA of an item issued and done: Q may be replaced
   uint64_t drain;       // every MMA issued, before TMEM is released
   uint64_t tok[2];      // issuer X may take its turn (two MMA issuers)
+  uint64_t sc_full[SC_STAGES];   // row scales of a key tile (ROWS)
   uint64_t ring_full[PF_RING];   // slot i holds the index of this CTA's next item
   uint64_t ring_empty[PF_RING];  // every role has taken slot i
   int ring[PF_RING];
@@ -197,9 +207,16 @@ __device__ __forceinline__ void ffma2(float& a0, float& a1, float b, float c) {
 // and row1 are multiples of 16, so passes come in whole batches.  At d 128,
 // where f16 row r overlaps source row r alone, warps may widen disjoint row
 // ranges of one tile at the same time.
-template <int D>
+//
+// ROWS: row r is also multiplied by its V scale times `mul`, a power of two that
+// puts the tile's largest scale in [2^6, 2^7) (tile_exponent), so the f16 tile
+// holds vs_r * mul * code: scale and product are each rounded to f16 (2^-11).
+// mul 0 (a WILD_TILE) leaves the codes as they are.  Rows outside [lo, hi)
+// become zero.
+template <int D, bool ROWS = false>
 __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int row0, int row1,
-                                                    int lane) {
+                                                    int lane, const float* sc = nullptr,
+                                                    float mul = 1.f, int lo = 0, int hi = 0) {
   constexpr int RPP = 512 / D;
   constexpr int U = (D == 128) ? 4 : 2;
   constexpr int HALF = BLOCK_M * 128;  // bytes of one d half of a tile
@@ -223,12 +240,26 @@ __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int ro
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      __half2 f;
+      if constexpr (ROWS) {
+        const int r = (ps + u) * RPP + r0;
+        const bool in = r >= lo && r < hi;
+        f = __float2half2_rn(!in ? 0.f : mul == 0.f ? 1.f : sc[(r >> 4) * 32 + 16 + (r & 15)] * mul);
+        if (!in) w[u] = make_uint4(0u, 0u, 0u, 0u);
+      }
       const unsigned v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
       unsigned h[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         h[2 * e] = e4m3x2_to_f16x2(v[e]);
         h[2 * e + 1] = e4m3x2_to_f16x2(v[e] >> 16);
+      }
+      if constexpr (ROWS) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), f);
+          h[e] = *reinterpret_cast<const unsigned*>(&y);
+        }
       }
       // ps * RPP is a multiple of 8: the row's swizzle phase is that of
       // r0 + u * RPP
@@ -240,6 +271,33 @@ __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int ro
     __syncwarp();
   }
 }
+
+// The exponent er of a key tile: the largest V scale of its rows [lo, hi) is in
+// [2^(er - 1), 2^er).  WILD_TILE if the smallest is below 2^-WILD_OCTAVES of it:
+// f16 then has no one power of two that suits every row of the tile.  Every
+// warp that works on the tile computes the same.
+constexpr int WILD_OCTAVES = 14;
+constexpr int WILD_TILE = 1 << 20;
+__device__ __forceinline__ int tile_exponent(const float* sc, int lo, int hi, int lane) {
+  const float4 v = *reinterpret_cast<const float4*>(sc + (lane >> 2) * 32 + 16 + (lane & 3) * 4);
+  const float x[4] = {v.x, v.y, v.z, v.w};
+  unsigned m = 0u, least = 0xffffffffu;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r = lane * 4 + e;
+    if (r >= lo && r < hi) {
+      m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+      least = min(least, __float_as_uint(x[e]) & 0x7fffffffu);
+    }
+  }
+  m = __reduce_max_sync(FULL, m);
+  least = __reduce_min_sync(FULL, least);
+  const int top = static_cast<int>(m >> 23);
+  if (top - static_cast<int>(least >> 23) > WILD_OCTAVES) return WILD_TILE;
+  return min(100, max(-100, top - 126));
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
 // Converts a Q tile (bf16, as TMA loaded it: DH 128-byte-swizzled d halves)
 // to f16 in place for the f16 MMAs of an e4m3 call at d 64, once its copy has
@@ -362,6 +420,27 @@ __device__ __forceinline__ void fadd2(float& s0, float& s1, float a0, float a1) 
       : "f"(a0), "f"(a1));
 }
 
+// (a0, a1) *= (b0, b1)
+__device__ __forceinline__ void fmul2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb;\n\t"
+      "mov.b64 ra, {%0, %1};\n\t"
+      "mov.b64 rb, {%2, %3};\n\t"
+      "mul.f32x2 ra, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, ra;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+
+// The scores of a tile times their keys' K scales.
+__device__ __forceinline__ void scale_scores(float (&sv)[BLOCK_N], const float* sc) {
+#pragma unroll
+  for (int q = 0; q < BLOCK_N; q += 4) {
+    const float4 k = *reinterpret_cast<const float4*>(sc + (q >> 4) * 32 + (q & 15));
+    fmul2(sv[q], sv[q + 1], k.x, k.y);
+    fmul2(sv[q + 2], sv[q + 3], k.z, k.w);
+  }
+}
+
 // The weights 2^(x sl2 - ref) of 32 scores, packed in pairs (bf16, or f16
 // when F16) as P; returns their sum.
 template <bool F16>
@@ -433,6 +512,13 @@ __device__ __forceinline__ Sub make_sub(const Problem& p, const Item& it, bool h
   return u;
 }
 
+// The first key any row of the item sees (0 without a window).
+__device__ __forceinline__ int first_key(const Problem& p, const Item& it, bool head_pairs) {
+  return p.window > 0 ? max(0, it.s - it.q_len + it.qt * (head_pairs ? BLOCK_M : 2 * BLOCK_M) -
+                                   p.window + 1)
+                      : 0;
+}
+
 // Key tiles [u0, u0 + n) that either sub-tile visits (the two ranges touch or
 // overlap); a sub-tile without key tiles does not widen the range.
 __device__ __forceinline__ int union_tiles(const Sub& a, const Sub& b, int& u0) {
@@ -450,6 +536,19 @@ __device__ __forceinline__ int union_tiles(const Sub& a, const Sub& b, int& u0) 
 // and converted to f16 in place.  The per-row scale of Q, the K scale and
 // sl2 make the row's score scale; the V scale is out_scale.
 //
+// ROWS: the e4m3 cache has a scale per key row of K (ks) and of V (vs).  A score
+// column is multiplied by its ks in the softmax; vs goes into the widened V
+// tile, up to the power of two 2^(7 - er) of the tile (er: tile_exponent).  The
+// running reference m is taken over x + er, so P = 2^(x + er - m) keeps f16's
+// range whatever the scales are, O is relative to m with the constant factor
+// 2^7 that out_scale takes back, and the sum of a tile's P counts 2^-er times
+// in the normaliser.  Where the V scales of a tile's rows are further apart
+// than f16 allows (WILD_TILE), the tile holds the codes alone and the weights
+// take the scales instead, P = 2^(x + log2 vs + 7 - m) with each P counting
+// 2^-7 / vs times in the normaliser: exact for any scales, and slow (the path
+// that takes the row max, two more MUFU operations a weight), which only data
+// far from a model's reaches.
+//
 // Persistent: the grid holds at most one CTA per SM; its items come from the
 // LPT-ordered list, in a fixed order for the first rounds and claimed as
 // CTAs get free for the last ones (warp 8 posts them in the item ring, see
@@ -461,7 +560,7 @@ __device__ __forceinline__ int union_tiles(const Sub& a, const Sub& b, int& u0) 
 // that follows the item's last S MMA, and the first P V of the next item
 // (which overwrites O) waits on p_full, which the softmax warps arrive on only
 // after their epilogue has read O.
-template <int D, bool HALF, bool FP8, bool TWO>
+template <int D, bool HALF, bool FP8, bool TWO, bool ROWS>
 __global__ void __launch_bounds__(PF_THREADS, 1)
     prefill_kernel(const __grid_constant__ Problem p, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
@@ -469,7 +568,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   // e4m3 at d 128: the score MMAs read the cache's K codes as they are (8-bit
   // MMAs against the split Q), so only V tiles are widened
   constexpr bool NK = FP8 && D == 128;
-  using C = PrefillCfg<D, NK>;
+  using C = PrefillCfg<D, NK, ROWS>;
+  static_assert(!ROWS || FP8, "row scales go with an e4m3 cache");
   constexpr bool MMA_F16 = HALF || FP8;  // operand and P type of the P V MMAs
   constexpr int VST = C::VST;
   constexpr int V_SPLIT = 80;  // NK: first V row that warp 8 widens
@@ -518,6 +618,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     mbar_init(&bars->tok[1], 1);
     for (int i = 0; i < PF_KST; ++i) mbar_init(&bars->k_land[i], 1);
     for (int i = 0; i < VST; ++i) mbar_init(&bars->v_land[i], 1);
+    for (int i = 0; i < SC_STAGES; ++i) mbar_init(&bars->sc_full[i], 1);
     mbar_init(&bars->q_conv[0], 4);  // one arrival per warp of the softmax warpgroup
     mbar_init(&bars->q_conv[1], 4);
     mbar_init(&bars->drain, TWO ? 2 : 1);
@@ -575,6 +676,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   unsigned char* sQ = smem + C::Q_OFF;
   unsigned char* sK = smem + C::K_OFF;
   unsigned char* sV = smem + C::V_OFF;
+  // row scales of the key tile at ring position jt
+  auto sc_of = [&](int jt) {
+    return reinterpret_cast<const float*>(smem + C::SC_OFF + (jt % SC_STAGES) * SC_TILE);
+  };
   const int rows_box = p.bs < BLOCK_N ? p.bs : BLOCK_N;  // rows of one cache copy
   const int pages_per_tile = BLOCK_N / rows_box;         // copies of one key tile
 
@@ -672,6 +777,56 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         break;
       }
       const int* bt = p.block_table + static_cast<int64_t>(it.r) * p.bt_stride;
+      const int klo = ROWS ? first_key(p, it, head_pairs) : 0;
+      // ROWS (the K producer): a tile's row scales, 64 pieces of 16 bytes, two
+      // per lane.  They are loaded when the tile's copies go out and stored in
+      // the ring (and announced) one step later, so their latency is hidden.
+      float4 sc_piece[2];
+      int sc_jt = -1;  // the tile whose pieces are in flight
+      // blk: the block id of the lane's page of the tile
+      auto load_scales = [&](int jt, int key_base, int blk) {
+        sc_jt = jt;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int group = 4 * h + (lane >> 3);
+          const int b = __shfl_sync(FULL, blk, group * 16 / rows_box);
+          const int key0 = key_base + group * 16;
+          if (key0 >= s) {
+            sc_piece[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+            continue;
+          }
+          const int slot = p.bs_shift >= 0 ? (key0 & (p.bs - 1)) : (key0 % p.bs);
+          sc_piece[h] = __ldg(reinterpret_cast<const float4*>(
+              p.row_scales + ((static_cast<int64_t>(b) * (p.bs >> 4) + (slot >> 4)) * p.Hkv + g) * 32 +
+              (lane & 7) * 4));
+        }
+      };
+      auto store_scales = [&]() {
+        if (sc_jt < 0) return;
+        float4* dst = reinterpret_cast<float4*>(smem + C::SC_OFF + (sc_jt % SC_STAGES) * SC_TILE);
+        dst[lane] = sc_piece[0];
+        dst[32 + lane] = sc_piece[1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->sc_full[sc_jt % SC_STAGES]);
+        sc_jt = -1;
+      };
+      // Widens rows [row0, row1) of the V tile at ring position jt, whose first
+      // key is key_base (ROWS: with its scales, once they are there).
+      auto widen_v = [&](unsigned char* stage, int jt, int key_base, int row0, int row1) -> int {
+        if constexpr (ROWS) {
+          if (!__all_sync(FULL, mbar_wait(&bars->sc_full[jt % SC_STAGES], (jt / SC_STAGES) & 1,
+                                          status, abort_flag)))
+            return 0;
+          const float* sc = sc_of(jt);
+          const int er = tile_exponent(sc, klo - key_base, s - key_base, lane);
+          widen_e4m3_in_place<D, true>(stage, row0, row1, lane, sc,
+                                       er == WILD_TILE ? 0.f : pow2i(7 - er), klo - key_base,
+                                       s - key_base);
+        } else {
+          widen_e4m3_in_place<D>(stage, row0, row1, lane);
+        }
+        return 1;
+      };
       // block id of page `lane` of key tile kt (0 when that page is past seq_len)
       auto page_block = [&](int kt) {
         const int key0 = kt * BLOCK_N + lane * rows_box;
@@ -697,7 +852,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         auto issue_k = [&]() {
           const int kt = u0 + n_issued, jt = jg + n_issued;
           const int key_base = kt * BLOCK_N;
-          const int my_blk = __shfl_sync(FULL, blk_next, lane);
+          const int my_blk = blk_next;
           if (n_issued + 1 < n_union) blk_next = page_block(kt + 1);
           const int n_load = min(pages_per_tile, (s - key_base + rows_box - 1) / rows_box);
           const int my_key0 = key_base + lane * rows_box;
@@ -718,10 +873,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if (lane < n_load)
             tma_load_4d(sK + st * C::KSTAGE + lane * rows_box * 128, &kmap, &bars->k_full[st], 0,
                         g, my_slot, my_blk);
+          if constexpr (ROWS) load_scales(jt, key_base, my_blk);
           ++n_issued;
           return 1;
         };
-        while (ok && n_issued < min(PF_KST - 1, n_union)) ok = issue_k();
+        while (ok && n_issued < min(PF_KST - 1, n_union)) {
+          ok = issue_k();
+          if constexpr (ROWS) store_scales();
+        }
         for (int j = 0; ok && j < n_union; ++j) {
           if (n_issued < n_union && !(ok = issue_k())) break;
           const int jt = jg + j, st = jt % VST;
@@ -731,10 +890,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           }
           const int key_base = (u0 + j) * BLOCK_N;
           const int rows = min(pages_per_tile, (s - key_base + rows_box - 1) / rows_box) * rows_box;
-          widen_e4m3_in_place<D>(sV + st * C::TILE, V_SPLIT, max(rows, V_SPLIT), lane);
+          if (!widen_v(sV + st * C::TILE, jt, key_base, V_SPLIT, max(rows, V_SPLIT))) {
+            ok = 0;
+            break;
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->v_full[st]);
+          if constexpr (ROWS) store_scales();
         }
         jg += n_union;
       } else if (direct) {
@@ -802,6 +965,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             tma_load_4d(ring + st * stage_bytes + C::SRC8 + lane * rows_box * D, &vmap, &lands[st],
                         0, g, slot, kv * p.NB + blkv);
           }
+          if constexpr (ROWS)
+            if (good && kv == 0) load_scales(jt, key_base, blkv);
           return good;
         };
         int blk_next = page_block(u0);
@@ -813,7 +978,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           ++n_issued;
           return good;
         };
-        while (ok && n_issued < min(nst - 1, n_union)) ok = issue_next();
+        while (ok && n_issued < min(nst - 1, n_union)) {
+          ok = issue_next();
+          if constexpr (ROWS) store_scales();
+        }
         for (int j = 0; ok && j < n_union; ++j) {
           const int jt = jg + j, st = jt % nst;
           if (!__all_sync(FULL, mbar_wait(&lands[st], (jt / nst) & 1, status, abort_flag))) {
@@ -822,8 +990,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           }
           const int key_base = (u0 + j) * BLOCK_N;
           const int n_load = min(pages_per_tile, (s - key_base + rows_box - 1) / rows_box);
-          widen_e4m3_in_place<D>(ring + st * stage_bytes, 0,
-                                 NK ? min(n_load * rows_box, V_SPLIT) : n_load * rows_box, lane);
+          const int rows = NK ? min(n_load * rows_box, V_SPLIT) : n_load * rows_box;
+          if (kv == 0) {
+            widen_e4m3_in_place<D>(ring + st * stage_bytes, 0, rows, lane);
+          } else if (!widen_v(ring + st * stage_bytes, jt, key_base, 0, rows)) {
+            ok = 0;
+            break;
+          }
+          if constexpr (ROWS) store_scales();
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(kv ? &bars->v_full[st] : &bars->k_full[st]);
@@ -1131,6 +1305,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     // kept normal so that a masked score (-inf) still maps to -inf.  Set when
     // the item's Q tile is converted (the previous item no longer needs it).
     float sl2r = sl2;
+    // ROWS: ring position of the item's first key tile modulo 2 x SC_STAGES
+    unsigned sc_pos = 0;
     // An e4m3 call converts each item's Q tile at the end of the previous
     // item (below), so its loop starts one step early, on an empty item, to
     // convert the first one there too: one copy of that long code.
@@ -1178,6 +1354,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       // output row of the epilogue
       const int64_t orow_i = static_cast<int64_t>(it.t0 + i) * p.H + u.h;
       const int chunk = it.chunk;
+      const int klo = ROWS ? first_key(p, it, head_pairs) : 0;
       float m_run = -INFINITY, l_run = 0.f;
       const int nt = u.x1 - u.x0;
       for (int c = 0; c < nt; ++c) {
@@ -1186,6 +1363,24 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         if (!__all_sync(FULL, mbar_wait(&bars->s_full[X], (ph ^ c) & 1, status, abort_flag))) {
           ok = false;
           break;
+        }
+        const float* sc = nullptr;
+        float er = 0.f, l_mul = 1.f;  // ROWS: the tile's exponent and 2^-er
+        bool wild = false;            // ROWS: a WILD_TILE
+        if constexpr (ROWS) {
+          const unsigned pos = (sc_pos + static_cast<unsigned>(kt - u0)) % (2 * SC_STAGES);
+          if (!__all_sync(FULL, mbar_wait(&bars->sc_full[pos % SC_STAGES], pos / SC_STAGES, status,
+                                          abort_flag))) {
+            ok = false;
+            break;
+          }
+          sc = sc_of(static_cast<int>(pos));
+          const int e = tile_exponent(sc, klo - key0, s - key0, lane);
+          wild = e == WILD_TILE;
+          if (!wild) {
+            er = static_cast<float>(e);
+            l_mul = pow2i(-e);
+          }
         }
         tc_fence_after();
         const bool edge = key0 > edge_hi || key0 <= edge_lo;
@@ -1200,7 +1395,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         // columns per 32 scores) is stored at columns [0, 64) only once the
         // tile is known to stay on this path, so the scores are still in TMEM
         // for the other one.
-        bool slow = (m_run == -INFINITY);
+        bool slow = (m_run == -INFINITY) || wild;
         float ps = 0.f;
         if (!__any_sync(FULL, slow)) {
           float sv[BLOCK_N];
@@ -1208,6 +1403,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           for (int g = 0; g < BLOCK_N / 32; ++g)
             tc_ld32(s_t + g * 32, *reinterpret_cast<float(*)[32]>(&sv[g * 32]));
           tc_wait_ld();
+          if constexpr (ROWS) scale_scores(sv, sc);
           if (edge) {
 #pragma unroll
             for (int q = 0; q < BLOCK_N; ++q)
@@ -1217,7 +1413,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll
           for (int g = 0; g < BLOCK_N / 32; ++g)
             ps += exp_piece<MMA_F16>(*reinterpret_cast<const float(*)[32]>(&sv[g * 32]), sl2r,
-                                     m_run, *reinterpret_cast<unsigned(*)[16]>(&pk[g * 16]));
+                                     ROWS ? m_run - er : m_run,
+                                     *reinterpret_cast<unsigned(*)[16]>(&pk[g * 16]));
           slow = !(ps <= FAST_SUM_LIMIT);
           if (!__any_sync(FULL, slow)) {
 #pragma unroll
@@ -1233,6 +1430,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           for (int g = 0; g < BLOCK_N / 32; ++g)
             tc_ld32(s_t + g * 32, *reinterpret_cast<float(*)[32]>(&sv[g * 32]));
           tc_wait_ld();
+          if constexpr (ROWS) scale_scores(sv, sc);
+          if constexpr (ROWS) {
+            if (wild) {
+#pragma unroll
+              for (int q = 0; q < BLOCK_N; ++q)
+                sv[q] = sv[q] * sl2r + (__log2f(sc[(q >> 4) * 32 + 16 + (q & 15)]) + 7.f);
+            }
+          }
+          const float mul = wild ? 1.f : sl2r;
           if (edge) {
 #pragma unroll
             for (int q = 0; q < BLOCK_N; ++q)
@@ -1249,7 +1455,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           m4[0] = max3(m4[0], sv[BLOCK_N - 4], sv[BLOCK_N - 3]);
           m4[1] = max3(m4[1], sv[BLOCK_N - 2], sv[BLOCK_N - 1]);
           const float mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
-          const float mx_s = (mx == -INFINITY) ? -INFINITY : mx * sl2r;
+          const float mx_s = (mx == -INFINITY) ? -INFINITY : ROWS ? mx * mul + er : mx * sl2r;
           // Lazy rescale: move the reference max only when it grows by > 2^8,
           // or, for a row whose own weights summed above the limit, whenever
           // it grows (else that row would take this path on every tile).
@@ -1263,13 +1469,25 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           }
           // The weights, each 32 columns' P stored as soon as it is packed
           // (to columns [16g, 16g + 16), whose scores are in registers).
-          const float ref = (m_run == -INFINITY) ? 0.f : m_run;
+          const float ref = (m_run == -INFINITY) ? 0.f : ROWS ? m_run - er : m_run;
           ps = 0.f;
 #pragma unroll
           for (int g = 0; g < BLOCK_N / 32; ++g) {
             unsigned pk[16];
-            ps += exp_piece<MMA_F16>(*reinterpret_cast<const float(*)[32]>(&sv[g * 32]), sl2r,
-                                     ref, pk);
+            float part = exp_piece<MMA_F16>(*reinterpret_cast<const float(*)[32]>(&sv[g * 32]),
+                                            ROWS ? mul : sl2r, ref, pk);
+            if constexpr (ROWS) {
+              if (wild) {  // each weight over its key's scale
+                part = 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const int q = g * 32 + e;
+                  const float w = fast_exp2(sv[q] - ref);
+                  part += w > 0.f ? __fdividef(w, sc[(q >> 4) * 32 + 16 + (q & 15)]) * 0x1p-7f : 0.f;
+                }
+              }
+            }
+            ps += part;
             tc_st16u(s_t + g * 16, pk);
           }
           // O is rescaled last, once the score registers are free.  P V of
@@ -1288,7 +1506,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             }
           }
         }
-        l_run += ps;
+        l_run += ROWS ? ps * l_mul : ps;
         tc_wait_st();
 
         // Zero V rows at or past seq_len before P V reads them (done by the
@@ -1317,6 +1535,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         mbar_arrive(&bars->p_full[X]);
       }
       ph = ((ph ^ (nt & 1)) & 3) | ((((ph >> 2) + static_cast<unsigned>(n_union)) % VPOS) << 2);
+      if constexpr (ROWS) sc_pos = (sc_pos + static_cast<unsigned>(n_union)) % (2 * SC_STAGES);
       // The next item's metadata is fetched here, where the score registers
       // are dead, and lands while the epilogue runs.
       const int idx_next = ok ? take_warp(k + 1) : -1;
@@ -1420,12 +1639,12 @@ static int prefill_sms() {
   return counts[dev];
 }
 
-template <int D, bool HALF, bool FP8, bool TWO>
+template <int D, bool HALF, bool FP8, bool TWO, bool ROWS = false>
 cudaError_t launch_prefill_t(const Problem& p, const CUtensorMap& q_map, const CUtensorMap& k_map,
                              const CUtensorMap& v_map,
                              unsigned grid) {
-  using C = PrefillCfg<D, FP8 && D == 128>;
-  auto k = prefill_kernel<D, HALF, FP8, TWO>;
+  using C = PrefillCfg<D, FP8 && D == 128, ROWS>;
+  auto k = prefill_kernel<D, HALF, FP8, TWO, ROWS>;
   cudaFuncAttributes attr;
   cudaError_t e = cudaFuncGetAttributes(&attr, k);
   if (e != cudaSuccess) return e;
@@ -1440,7 +1659,8 @@ cudaError_t launch_prefill_t(const Problem& p, const CUtensorMap& q_map, const C
   // become ~1e-30 * q.k, whose exp2 is 1.0f exactly (uniform weights, as the
   // definition gives).  out_scale is the V scale of an e4m3 cache.
   const float sl2 = fmaxf(p.scale * LOG2E * (FP8 ? p.k_scale : 1.f), 1e-30f);
-  const float out_scale = FP8 ? p.v_scale : 1.f;
+  // ... and with row scales the constant of the widened V tiles.
+  const float out_scale = ROWS ? 0x1p-7f : FP8 ? p.v_scale : 1.f;
   k<<<grid, PF_THREADS, C::SMEM, p.stream>>>(p, q_map, k_map, v_map, sl2, out_scale);
   return cudaGetLastError();
 }
@@ -1463,6 +1683,9 @@ cudaError_t launch_prefill(const Problem& p, const CUtensorMap& q_map, const CUt
   if (p.kv_dtype == PATTN_KV_FP8_E4M3)
     return p.D == 128 ? launch_prefill_t<128, false, true, true>(p, q_map, k_map, v_map, g)
                       : launch_prefill_t<64, false, true, false>(p, q_map, k_map, v_map, g);
+  if (p.kv_dtype == PATTN_KV_FP8_E4M3_ROW)
+    return p.D == 128 ? launch_prefill_t<128, false, true, true, true>(p, q_map, k_map, v_map, g)
+                      : launch_prefill_t<64, false, true, false, true>(p, q_map, k_map, v_map, g);
   return p.D == 128 ? launch_prefill_t<128, false, false, true>(p, q_map, k_map, v_map, g)
                     : launch_prefill_t<64, false, false, true>(p, q_map, k_map, v_map, g);
 }
