@@ -109,13 +109,27 @@ constexpr unsigned FULL = 0xffffffffu;
 template <bool FP8>
 __host__ __device__ constexpr int v_rows() { return FP8 ? BLOCK_N : 16; }
 
-// Row scales of a key tile (ROWS): eight 128-byte lines (16 K scales, 16 V
-// scales) of 16 keys each, in a ring of four tiles.  Four need no barrier of
-// their own for reuse: the K producer fetches tile j's scales after it has
-// waited for the scores of tile j - 3, whose issuers had waited for P and V of
-// tile j - 4, so every reader of that tile's scales is done.
+// What the other roles need of a key tile's row scales (ROWS), in a ring of
+// four tiles that the K producer fills.  Four need no barrier for reuse: the
+// producer writes tile j's entry after it has waited for the scores of tile
+// j - 3, whose issuers had waited for P and V of tile j - 4, so every reader of
+// that tile's entry is done.
+struct ScaleTile {
+  float ks[BLOCK_N];     // K scales
+  unsigned vs[BLOCK_N];  // V scales times 2^(7 - er) as f16 pairs; the fp32 bits of
+                         // the V scales themselves if er is WILD_TILE
+};
 constexpr int SC_STAGES = 4;
-constexpr int SC_TILE = BLOCK_N / 16 * 128;
+constexpr int SC_TILE = sizeof(ScaleTile);
+// The smallest V scale of a tile may be 2^-WILD_OCTAVES of the largest; below
+// that f16 has no one power of two that suits every row (er = WILD_TILE).
+constexpr int WILD_OCTAVES = 14;
+constexpr int WILD_TILE = 1 << 20;
+// As FAST_SUM_LIMIT, with row scales: rows of uneven size outgrow the first
+// tile's reference more often (at 2^8 most tiles of keys with log-normal row
+// norms, sigma 0.4, did in some row of a warp), and f16 weights have room up to
+// 2^15.  A prompt batch took 0.57 instead of 0.90 ms.
+constexpr float ROWS_SUM_LIMIT = 16384.0f;
 
 // NK: e4m3 K codes used as they are (an e4m3 cache at d 128).
 template <int D, bool NK = false, bool ROWS = false>
@@ -158,6 +172,7 @@ struct Bars {
   uint64_t drain;       // every MMA issued, before TMEM is released
   uint64_t tok[2];      // issuer X may take its turn (two MMA issuers)
   uint64_t sc_full[SC_STAGES];   // row scales of a key tile (ROWS)
+  int sc_er[SC_STAGES];          // their exponent er, or WILD_TILE
   uint64_t ring_full[PF_RING];   // slot i holds the index of this CTA's next item
   uint64_t ring_empty[PF_RING];  // every role has taken slot i
   int ring[PF_RING];
@@ -208,15 +223,13 @@ __device__ __forceinline__ void ffma2(float& a0, float& a1, float b, float c) {
 // where f16 row r overlaps source row r alone, warps may widen disjoint row
 // ranges of one tile at the same time.
 //
-// ROWS: row r is also multiplied by its V scale times `mul`, a power of two that
-// puts the tile's largest scale in [2^6, 2^7) (tile_exponent), so the f16 tile
-// holds vs_r * mul * code: scale and product are each rounded to f16 (2^-11).
-// mul 0 (a WILD_TILE) leaves the codes as they are.  Rows outside [lo, hi)
-// become zero.
+// ROWS: row r is also multiplied by vs[r], an f16 pair (`wild`: it is not); scale
+// and product are each rounded to f16 (2^-11).  Rows below lo become zero (rows
+// at or past seq_len are zeroed by the softmax warps).
 template <int D, bool ROWS = false>
 __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int row0, int row1,
-                                                    int lane, const float* sc = nullptr,
-                                                    float mul = 1.f, int lo = 0, int hi = 0) {
+                                                    int lane, const unsigned* vs = nullptr,
+                                                    bool wild = false, int lo = 0) {
   constexpr int RPP = 512 / D;
   constexpr int U = (D == 128) ? 4 : 2;
   constexpr int HALF = BLOCK_M * 128;  // bytes of one d half of a tile
@@ -240,12 +253,14 @@ __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int ro
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      __half2 f;
+      unsigned f = 0x3C003C00u;  // 1, 1
       if constexpr (ROWS) {
         const int r = (ps + u) * RPP + r0;
-        const bool in = r >= lo && r < hi;
-        f = __float2half2_rn(!in ? 0.f : mul == 0.f ? 1.f : sc[(r >> 4) * 32 + 16 + (r & 15)] * mul);
-        if (!in) w[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (!wild) f = vs[r];
+        if (r < lo) {
+          f = 0u;
+          w[u] = make_uint4(0u, 0u, 0u, 0u);
+        }
       }
       const unsigned v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
       unsigned h[8];
@@ -257,7 +272,8 @@ __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int ro
       if constexpr (ROWS) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), f);
+          const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]),
+                                    *reinterpret_cast<const __half2*>(&f));
           h[e] = *reinterpret_cast<const unsigned*>(&y);
         }
       }
@@ -270,31 +286,6 @@ __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int ro
     }
     __syncwarp();
   }
-}
-
-// The exponent er of a key tile: the largest V scale of its rows [lo, hi) is in
-// [2^(er - 1), 2^er).  WILD_TILE if the smallest is below 2^-WILD_OCTAVES of it:
-// f16 then has no one power of two that suits every row of the tile.  Every
-// warp that works on the tile computes the same.
-constexpr int WILD_OCTAVES = 14;
-constexpr int WILD_TILE = 1 << 20;
-__device__ __forceinline__ int tile_exponent(const float* sc, int lo, int hi, int lane) {
-  const float4 v = *reinterpret_cast<const float4*>(sc + (lane >> 2) * 32 + 16 + (lane & 3) * 4);
-  const float x[4] = {v.x, v.y, v.z, v.w};
-  unsigned m = 0u, least = 0xffffffffu;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int r = lane * 4 + e;
-    if (r >= lo && r < hi) {
-      m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-      least = min(least, __float_as_uint(x[e]) & 0x7fffffffu);
-    }
-  }
-  m = __reduce_max_sync(FULL, m);
-  least = __reduce_min_sync(FULL, least);
-  const int top = static_cast<int>(m >> 23);
-  if (top - static_cast<int>(least >> 23) > WILD_OCTAVES) return WILD_TILE;
-  return min(100, max(-100, top - 126));
 }
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
@@ -431,11 +422,12 @@ __device__ __forceinline__ void fmul2(float& a0, float& a1, float b0, float b1) 
       : "f"(b0), "f"(b1));
 }
 
-// The scores of a tile times their keys' K scales.
-__device__ __forceinline__ void scale_scores(float (&sv)[BLOCK_N], const float* sc) {
+// N scores times their keys' K scales.
+template <int N>
+__device__ __forceinline__ void scale_scores(float (&sv)[N], const float* ks) {
 #pragma unroll
-  for (int q = 0; q < BLOCK_N; q += 4) {
-    const float4 k = *reinterpret_cast<const float4*>(sc + (q >> 4) * 32 + (q & 15));
+  for (int q = 0; q < N; q += 4) {
+    const float4 k = *reinterpret_cast<const float4*>(ks + q);
     fmul2(sv[q], sv[q + 1], k.x, k.y);
     fmul2(sv[q + 2], sv[q + 3], k.z, k.w);
   }
@@ -538,7 +530,8 @@ __device__ __forceinline__ int union_tiles(const Sub& a, const Sub& b, int& u0) 
 //
 // ROWS: the e4m3 cache has a scale per key row of K (ks) and of V (vs).  A score
 // column is multiplied by its ks in the softmax; vs goes into the widened V
-// tile, up to the power of two 2^(7 - er) of the tile (er: tile_exponent).  The
+// tile, up to the power of two 2^(7 - er) of the tile (the largest vs is in
+// [2^(er - 1), 2^er)).  The
 // running reference m is taken over x + er, so P = 2^(x + er - m) keeps f16's
 // range whatever the scales are, O is relative to m with the constant factor
 // 2^7 that out_scale takes back, and the sum of a tile's P counts 2^-er times
@@ -572,7 +565,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   static_assert(!ROWS || FP8, "row scales go with an e4m3 cache");
   constexpr bool MMA_F16 = HALF || FP8;  // operand and P type of the P V MMAs
   constexpr int VST = C::VST;
-  constexpr int V_SPLIT = 80;  // NK: first V row that warp 8 widens
+  constexpr int V_SPLIT = ROWS ? 96 : 80;  // NK: first V row that warp 8 widens
   static_assert(!(FP8 && D != 128 && TWO), "an e4m3 call at d 64 has one MMA issuer");
   static_assert(!NK || TWO, "the 8-bit score MMAs are issued by the two-issuer loop");
   extern __shared__ unsigned char smem_raw[];
@@ -678,7 +671,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   unsigned char* sV = smem + C::V_OFF;
   // row scales of the key tile at ring position jt
   auto sc_of = [&](int jt) {
-    return reinterpret_cast<const float*>(smem + C::SC_OFF + (jt % SC_STAGES) * SC_TILE);
+    return reinterpret_cast<ScaleTile*>(smem + C::SC_OFF + (jt % SC_STAGES) * SC_TILE);
   };
   const int rows_box = p.bs < BLOCK_N ? p.bs : BLOCK_N;  // rows of one cache copy
   const int pages_per_tile = BLOCK_N / rows_box;         // copies of one key tile
@@ -778,37 +771,49 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       }
       const int* bt = p.block_table + static_cast<int64_t>(it.r) * p.bt_stride;
       const int klo = ROWS ? first_key(p, it, head_pairs) : 0;
-      // ROWS (the K producer): a tile's row scales, 64 pieces of 16 bytes, two
-      // per lane.  They are loaded when the tile's copies go out and stored in
-      // the ring (and announced) one step later, so their latency is hidden.
-      float4 sc_piece[2];
-      int sc_jt = -1;  // the tile whose pieces are in flight
-      // blk: the block id of the lane's page of the tile
-      auto load_scales = [&](int jt, int key_base, int blk) {
-        sc_jt = jt;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int group = 4 * h + (lane >> 3);
-          const int b = __shfl_sync(FULL, blk, group * 16 / rows_box);
-          const int key0 = key_base + group * 16;
-          if (key0 >= s) {
-            sc_piece[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-            continue;
-          }
-          const int slot = p.bs_shift >= 0 ? (key0 & (p.bs - 1)) : (key0 % p.bs);
-          sc_piece[h] = __ldg(reinterpret_cast<const float4*>(
-              p.row_scales + ((static_cast<int64_t>(b) * (p.bs >> 4) + (slot >> 4)) * p.Hkv + g) * 32 +
-              (lane & 7) * 4));
+      // ROWS (the K producer): lane l takes the scales of keys 4l .. 4l + 3 of a
+      // tile.  Loads them (blk: the block id of the lane's page of the tile; keys
+      // at or past seq_len or below the window count as absent) ...
+      auto load_scales = [&](int key_base, int blk, float4& k4, float4& v4) {
+        const int b = __shfl_sync(FULL, blk, (lane >> 2) * 16 / rows_box);
+        const int key0 = key_base + (lane >> 2) * 16;
+        const int slot = p.bs_shift >= 0 ? (key0 & (p.bs - 1)) : (key0 % p.bs);
+        k4 = v4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (key0 < s) {
+          const float4* src = reinterpret_cast<const float4*>(
+              p.row_scales + ((static_cast<int64_t>(b) * (p.bs >> 4) + (slot >> 4)) * p.Hkv + g) * 32);
+          k4 = __ldg(src + (lane & 3));
+          v4 = __ldg(src + 4 + (lane & 3));
         }
       };
-      auto store_scales = [&]() {
-        if (sc_jt < 0) return;
-        float4* dst = reinterpret_cast<float4*>(smem + C::SC_OFF + (sc_jt % SC_STAGES) * SC_TILE);
-        dst[lane] = sc_piece[0];
-        dst[32 + lane] = sc_piece[1];
+      // ... and, once the ring entry of position jt is free, writes it.
+      auto store_scales = [&](int jt, int key_base, const float4& k4, const float4& v4) {
+        const unsigned v[4] = {__float_as_uint(v4.x), __float_as_uint(v4.y), __float_as_uint(v4.z),
+                               __float_as_uint(v4.w)};
+        unsigned top = 0u, low = 0x7fffffffu;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key_base + lane * 4 + e;
+          if (key >= klo && key < s) {
+            top = max(top, v[e] & 0x7fffffffu);
+            low = min(low, v[e] & 0x7fffffffu);
+          }
+        }
+        const int hi = static_cast<int>(__reduce_max_sync(FULL, top) >> 23);
+        const int lo = static_cast<int>(__reduce_min_sync(FULL, low) >> 23);
+        const bool wild = hi - lo > WILD_OCTAVES;
+        const int er = min(100, max(-100, hi - 126));
+        const float mul = pow2i(7 - er);
+        ScaleTile* t = sc_of(jt);
+        *reinterpret_cast<float4*>(&t->ks[lane * 4]) = k4;
+        uint4 h = make_uint4(v[0], v[1], v[2], v[3]);
+        if (!wild)
+          h = make_uint4(pack2<true>(v4.x * mul, v4.x * mul), pack2<true>(v4.y * mul, v4.y * mul),
+                         pack2<true>(v4.z * mul, v4.z * mul), pack2<true>(v4.w * mul, v4.w * mul));
+        *reinterpret_cast<uint4*>(&t->vs[lane * 4]) = h;
+        if (lane == 0) bars->sc_er[jt % SC_STAGES] = wild ? WILD_TILE : er;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->sc_full[sc_jt % SC_STAGES]);
-        sc_jt = -1;
+        if (lane == 0) mbar_arrive(&bars->sc_full[jt % SC_STAGES]);
       };
       // Widens rows [row0, row1) of the V tile at ring position jt, whose first
       // key is key_base (ROWS: with its scales, once they are there).
@@ -817,11 +822,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if (!__all_sync(FULL, mbar_wait(&bars->sc_full[jt % SC_STAGES], (jt / SC_STAGES) & 1,
                                           status, abort_flag)))
             return 0;
-          const float* sc = sc_of(jt);
-          const int er = tile_exponent(sc, klo - key_base, s - key_base, lane);
-          widen_e4m3_in_place<D, true>(stage, row0, row1, lane, sc,
-                                       er == WILD_TILE ? 0.f : pow2i(7 - er), klo - key_base,
-                                       s - key_base);
+          widen_e4m3_in_place<D, true>(
+              stage, row0, row1, lane, sc_of(jt)->vs,
+              *static_cast<volatile int*>(&bars->sc_er[jt % SC_STAGES]) == WILD_TILE,
+              klo - key_base);
         } else {
           widen_e4m3_in_place<D>(stage, row0, row1, lane);
         }
@@ -854,6 +858,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           const int key_base = kt * BLOCK_N;
           const int my_blk = blk_next;
           if (n_issued + 1 < n_union) blk_next = page_block(kt + 1);
+          float4 k4, v4;
+          if constexpr (ROWS) load_scales(key_base, my_blk, k4, v4);
           const int n_load = min(pages_per_tile, (s - key_base + rows_box - 1) / rows_box);
           const int my_key0 = key_base + lane * rows_box;
           const int my_slot = p.bs_shift >= 0 ? (my_key0 & (p.bs - 1)) : (my_key0 % p.bs);
@@ -873,16 +879,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if (lane < n_load)
             tma_load_4d(sK + st * C::KSTAGE + lane * rows_box * 128, &kmap, &bars->k_full[st], 0,
                         g, my_slot, my_blk);
-          if constexpr (ROWS) load_scales(jt, key_base, my_blk);
+          if constexpr (ROWS) store_scales(jt, key_base, k4, v4);
           ++n_issued;
           return 1;
         };
-        while (ok && n_issued < min(PF_KST - 1, n_union)) {
-          ok = issue_k();
-          if constexpr (ROWS) store_scales();
-        }
+        while (ok && n_issued < min(PF_KST - 1, n_union)) ok = issue_k();
         for (int j = 0; ok && j < n_union; ++j) {
-          if (n_issued < n_union && !(ok = issue_k())) break;
           const int jt = jg + j, st = jt % VST;
           if (!__all_sync(FULL, mbar_wait(&bars->v_land[st], (jt / VST) & 1, status, abort_flag))) {
             ok = 0;
@@ -897,7 +899,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->v_full[st]);
-          if constexpr (ROWS) store_scales();
+          if (n_issued < n_union && !(ok = issue_k())) break;
         }
         jg += n_union;
       } else if (direct) {
@@ -947,6 +949,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         uint64_t* lands = kv ? bars->v_land : bars->k_land;
         auto issue = [&](int jt, int kt, int blkv) {
           const int key_base = kt * BLOCK_N;
+          float4 k4, v4;
+          if constexpr (ROWS)
+            if (kv == 0) load_scales(key_base, blkv, k4, v4);
           const int n_load = min(pages_per_tile, (s - key_base + rows_box - 1) / rows_box);
           const int st = jt % nst;
           uint64_t* empty = kv ? &bars->v_empty[st] : &bars->k_empty[st];
@@ -966,7 +971,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                         0, g, slot, kv * p.NB + blkv);
           }
           if constexpr (ROWS)
-            if (good && kv == 0) load_scales(jt, key_base, blkv);
+            if (good && kv == 0) store_scales(jt, key_base, k4, v4);
           return good;
         };
         int blk_next = page_block(u0);
@@ -978,10 +983,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           ++n_issued;
           return good;
         };
-        while (ok && n_issued < min(nst - 1, n_union)) {
-          ok = issue_next();
-          if constexpr (ROWS) store_scales();
-        }
+        while (ok && n_issued < min(nst - 1, n_union)) ok = issue_next();
         for (int j = 0; ok && j < n_union; ++j) {
           const int jt = jg + j, st = jt % nst;
           if (!__all_sync(FULL, mbar_wait(&lands[st], (jt / nst) & 1, status, abort_flag))) {
@@ -997,7 +999,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             ok = 0;
             break;
           }
-          if constexpr (ROWS) store_scales();
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(kv ? &bars->v_full[st] : &bars->k_full[st]);
@@ -1354,19 +1355,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       // output row of the epilogue
       const int64_t orow_i = static_cast<int64_t>(it.t0 + i) * p.H + u.h;
       const int chunk = it.chunk;
-      const int klo = ROWS ? first_key(p, it, head_pairs) : 0;
       float m_run = -INFINITY, l_run = 0.f;
       const int nt = u.x1 - u.x0;
       for (int c = 0; c < nt; ++c) {
         const int kt = u.x0 + c;
         const int key0 = kt * BLOCK_N;
-        if (!__all_sync(FULL, mbar_wait(&bars->s_full[X], (ph ^ c) & 1, status, abort_flag))) {
-          ok = false;
-          break;
-        }
-        const float* sc = nullptr;
-        float er = 0.f, l_mul = 1.f;  // ROWS: the tile's exponent and 2^-er
-        bool wild = false;            // ROWS: a WILD_TILE
+        // ROWS: the tile's scales came with its K copies, before the scores
+        const ScaleTile* sc = nullptr;
+        int er = 0;  // its exponent
         if constexpr (ROWS) {
           const unsigned pos = (sc_pos + static_cast<unsigned>(kt - u0)) % (2 * SC_STAGES);
           if (!__all_sync(FULL, mbar_wait(&bars->sc_full[pos % SC_STAGES], pos / SC_STAGES, status,
@@ -1375,12 +1371,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             break;
           }
           sc = sc_of(static_cast<int>(pos));
-          const int e = tile_exponent(sc, klo - key0, s - key0, lane);
-          wild = e == WILD_TILE;
-          if (!wild) {
-            er = static_cast<float>(e);
-            l_mul = pow2i(-e);
-          }
+          er = *static_cast<volatile int*>(&bars->sc_er[pos % SC_STAGES]);
+        }
+        const bool wild = ROWS && er == WILD_TILE;
+        if (!__all_sync(FULL, mbar_wait(&bars->s_full[X], (ph ^ c) & 1, status, abort_flag))) {
+          ok = false;
+          break;
         }
         tc_fence_after();
         const bool edge = key0 > edge_hi || key0 <= edge_lo;
@@ -1396,6 +1392,22 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         // tile is known to stay on this path, so the scores are still in TMEM
         // for the other one.
         bool slow = (m_run == -INFINITY) || wild;
+        // O times a where a row needs it: P V of the previous tile is complete
+        // (the commit that announced these scores was issued after it).
+        auto rescale_o = [&](bool need_o, float alpha) {
+          if (__any_sync(FULL, need_o)) {
+            const float a = need_o ? alpha : 1.f;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              float ov[32];
+              tc_ld32(o_t + q * 32, ov);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ov[e] *= a;
+              tc_st32(o_t + q * 32, ov);
+            }
+          }
+        };
         float ps = 0.f;
         if (!__any_sync(FULL, slow)) {
           float sv[BLOCK_N];
@@ -1403,7 +1415,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           for (int g = 0; g < BLOCK_N / 32; ++g)
             tc_ld32(s_t + g * 32, *reinterpret_cast<float(*)[32]>(&sv[g * 32]));
           tc_wait_ld();
-          if constexpr (ROWS) scale_scores(sv, sc);
+          if constexpr (ROWS) scale_scores(sv, sc->ks);
           if (edge) {
 #pragma unroll
             for (int q = 0; q < BLOCK_N; ++q)
@@ -1413,16 +1425,16 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll
           for (int g = 0; g < BLOCK_N / 32; ++g)
             ps += exp_piece<MMA_F16>(*reinterpret_cast<const float(*)[32]>(&sv[g * 32]), sl2r,
-                                     ROWS ? m_run - er : m_run,
+                                     ROWS ? m_run - static_cast<float>(er) : m_run,
                                      *reinterpret_cast<unsigned(*)[16]>(&pk[g * 16]));
-          slow = !(ps <= FAST_SUM_LIMIT);
+          slow = !(ps <= (ROWS ? ROWS_SUM_LIMIT : FAST_SUM_LIMIT));
           if (!__any_sync(FULL, slow)) {
 #pragma unroll
             for (int g = 0; g < BLOCK_N / 32; ++g)
               tc_st16u(s_t + g * 16, *reinterpret_cast<const unsigned(*)[16]>(&pk[g * 16]));
           }
         }
-        if (__any_sync(FULL, slow)) {
+        if (!wild && __any_sync(FULL, slow)) {
           // The scores again (still in TMEM: nothing was stored over them),
           // all 128 columns in one round trip.
           float sv[BLOCK_N];
@@ -1430,15 +1442,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           for (int g = 0; g < BLOCK_N / 32; ++g)
             tc_ld32(s_t + g * 32, *reinterpret_cast<float(*)[32]>(&sv[g * 32]));
           tc_wait_ld();
-          if constexpr (ROWS) scale_scores(sv, sc);
-          if constexpr (ROWS) {
-            if (wild) {
-#pragma unroll
-              for (int q = 0; q < BLOCK_N; ++q)
-                sv[q] = sv[q] * sl2r + (__log2f(sc[(q >> 4) * 32 + 16 + (q & 15)]) + 7.f);
-            }
-          }
-          const float mul = wild ? 1.f : sl2r;
+          if constexpr (ROWS) scale_scores(sv, sc->ks);
           if (edge) {
 #pragma unroll
             for (int q = 0; q < BLOCK_N; ++q)
@@ -1455,7 +1459,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           m4[0] = max3(m4[0], sv[BLOCK_N - 4], sv[BLOCK_N - 3]);
           m4[1] = max3(m4[1], sv[BLOCK_N - 2], sv[BLOCK_N - 1]);
           const float mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
-          const float mx_s = (mx == -INFINITY) ? -INFINITY : ROWS ? mx * mul + er : mx * sl2r;
+          const float mx_s = (mx == -INFINITY) ? -INFINITY : mx * sl2r + static_cast<float>(er);
           // Lazy rescale: move the reference max only when it grows by > 2^8,
           // or, for a row whose own weights summed above the limit, whenever
           // it grows (else that row would take this path on every tile).
@@ -1469,44 +1473,73 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           }
           // The weights, each 32 columns' P stored as soon as it is packed
           // (to columns [16g, 16g + 16), whose scores are in registers).
-          const float ref = (m_run == -INFINITY) ? 0.f : ROWS ? m_run - er : m_run;
+          const float ref = (m_run == -INFINITY) ? 0.f : m_run - static_cast<float>(er);
           ps = 0.f;
 #pragma unroll
           for (int g = 0; g < BLOCK_N / 32; ++g) {
             unsigned pk[16];
-            float part = exp_piece<MMA_F16>(*reinterpret_cast<const float(*)[32]>(&sv[g * 32]),
-                                            ROWS ? mul : sl2r, ref, pk);
-            if constexpr (ROWS) {
-              if (wild) {  // each weight over its key's scale
-                part = 0.f;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const int q = g * 32 + e;
-                  const float w = fast_exp2(sv[q] - ref);
-                  part += w > 0.f ? __fdividef(w, sc[(q >> 4) * 32 + 16 + (q & 15)]) * 0x1p-7f : 0.f;
-                }
-              }
-            }
-            ps += part;
+            ps += exp_piece<MMA_F16>(*reinterpret_cast<const float(*)[32]>(&sv[g * 32]), sl2r,
+                                     ref, pk);
             tc_st16u(s_t + g * 16, pk);
           }
           // O is rescaled last, once the score registers are free.  P V of
           // the previous tile is complete: the commit that announced these
           // scores was issued after it.
-          if (__any_sync(FULL, need_o)) {
-            const float a = need_o ? alpha : 1.f;
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              float ov[32];
-              tc_ld32(o_t + q * 32, ov);
+          rescale_o(need_o, alpha);
+        }
+        if constexpr (ROWS) {
+          if (wild) {
+            // The weights take the V scales: y = x + log2 vs + 7.  32 scores at a
+            // time, from TMEM twice: their max, then the weights (P of a piece
+            // goes over scores of pieces already done).
+            auto piece = [&](int g, float (&y)[32]) {
+              tc_ld32(s_t + g * 32, y);
               tc_wait_ld();
+              scale_scores(y, sc->ks + g * 32);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] *= a;
-              tc_st32(o_t + q * 32, ov);
+              for (int e = 0; e < 32; ++e) {
+                const int q = g * 32 + e;
+                const float lv = __log2f(__uint_as_float(sc->vs[q])) + 7.f;
+                y[e] = (q < lim_hi && q >= lim_lo) ? y[e] * sl2r + lv : -INFINITY;
+              }
+            };
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int g = 0; g < BLOCK_N / 32; ++g) {
+              float y[32];
+              piece(g, y);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx = fmaxf(mx, y[e]);
             }
+            const bool grow = mx > m_run;
+            const bool need_o = grow && (m_run != -INFINITY) && (c > 0);
+            float alpha = 1.f;
+            if (grow) {
+              alpha = (m_run == -INFINITY) ? 0.f : fast_exp2(m_run - mx);
+              l_run *= alpha;
+              m_run = mx;
+            }
+            const float ref = (m_run == -INFINITY) ? 0.f : m_run;
+            ps = 0.f;
+#pragma unroll 1
+            for (int g = 0; g < BLOCK_N / 32; ++g) {
+              float y[32];
+              unsigned pk[16];
+              piece(g, y);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                y[e] = fast_exp2(y[e] - ref);
+                ps += y[e] > 0.f ? __fdividef(y[e], __uint_as_float(sc->vs[g * 32 + e])) : 0.f;
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = pack2<MMA_F16>(y[2 * e], y[2 * e + 1]);
+              tc_st16u(s_t + g * 16, pk);
+            }
+            er = 7;  // each weight counts 2^-7 / vs times
+            rescale_o(need_o, alpha);
           }
         }
-        l_run += ROWS ? ps * l_mul : ps;
+        l_run += ROWS ? ps * pow2i(-er) : ps;
         tc_wait_st();
 
         // Zero V rows at or past seq_len before P V reads them (done by the
