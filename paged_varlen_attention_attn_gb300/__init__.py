@@ -13,6 +13,7 @@ torch (plumbing; the library itself allocates nothing).
 """
 import ctypes
 import os
+import struct
 
 from . import _build
 
@@ -71,6 +72,18 @@ class RopeArgs(ctypes.Structure):
                                              "num_blocks")])
 
 
+def _packer(cls):
+    """struct.Struct with a ctypes structure's layout: building a call's arguments
+    in one step costs a quarter of setting the fields one by one."""
+    codes = {ctypes.c_size_t: "N", ctypes.c_longlong: "q", ctypes.c_float: "f", ctypes.c_int: "i"}
+    fmt = "@" + "".join(codes.get(t, "P") for _, t in cls._fields_)
+    pad = ctypes.sizeof(cls) - struct.calcsize(fmt)
+    return struct.Struct(fmt + "x" * pad)
+
+
+_ROPE_PACK = _packer(RopeArgs)
+_EXT_PACK = _packer(Ext)
+
 PHASES = ("plan", "prefill", "decode", "combine")
 
 
@@ -119,7 +132,7 @@ def load(path=None):
     lib.pattn_reshape_and_cache_rows.restype = i
     lib.pattn_reshape_and_cache_rows.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
     lib.pattn_rope_and_cache.restype = i
-    lib.pattn_rope_and_cache.argtypes = [ctypes.POINTER(RopeArgs)]
+    lib.pattn_rope_and_cache.argtypes = [vp]  # a RopeArgs by reference, or its bytes
     lib.pattn_gather_cache.restype = i
     lib.pattn_gather_cache.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp]
     if path is None:
@@ -231,16 +244,26 @@ def rope_pair_axis(sections, interleaved=False):
     return out
 
 
-def _rows_of(x, name, dtype):
-    """(address, elements between tokens) of a [T, heads, head_size] tensor whose
-    token rows are contiguous."""
-    if x.dim() != 3 or x.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor [num_tokens, heads, head_size]")
-    T, H, D = x.shape
+def _raw_stream(stream, dev):
+    """The cudaStream_t of ``stream``, or of the device's current stream (read
+    without building a Stream object: 2 us less per call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    from torch._C import _cuda_getCurrentRawStream
+    return _cuda_getCurrentRawStream(dev.index)
+
+
+def _rows_of(x, name, dtype, dev):
+    """(address, elements between tokens, shape) of a [T, heads, head_size] tensor
+    whose token rows are contiguous."""
+    shape = x.shape
+    if len(shape) != 3 or x.dtype != dtype or x.device != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor [num_tokens, heads, head_size] on one device")
+    T, H, D = shape
     st, sh, sd = x.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return x.data_ptr(), (st if T > 1 else H * D)
+    return x.data_ptr(), st if T > 1 else H * D, shape
 
 
 def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *, block_size,
@@ -268,72 +291,74 @@ def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *,
         raise ValueError("rope_and_cache needs q or key")
     dt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
     dev = x.device
-    a = RopeArgs()
-    a.struct_size = ctypes.sizeof(RopeArgs)
-    T, a.head_size = x.shape[0], x.shape[2]
-    a.num_tokens = T
+    q_at = qo_at = k_at = v_at = q_st = qo_st = k_st = v_st = 0
+    H = Hkv = NB = cache_at = slots_at = rows_at = scale_at = 0
     if q is not None:
-        a.q, a.q_stride = _rows_of(q, "q", dt)
-        a.num_heads = q.shape[1]
+        q_at, q_st, shape = _rows_of(q, "q", dt, dev)
+        T, H, D = shape
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=dev)
-        elif q_out.shape != q.shape or q_out.device != dev:
-            raise ValueError("q_out must have q's shape and device")
-        a.q_out, a.q_out_stride = _rows_of(q_out, "q_out", dt)
+            q_out = torch.empty(shape, dtype=dt, device=dev)
+        qo_at, qo_st, out_shape = _rows_of(q_out, "q_out", dt, dev)
+        if out_shape != shape:
+            raise ValueError("q_out must have q's shape")
     if key is not None:
-        if (value is None or key.shape != value.shape or key.shape[0] != T or
-                key.shape[2] != a.head_size or key.device != dev or value.device != dev):
+        if value is None:
+            raise ValueError("key needs a value")
+        k_at, k_st, shape = _rows_of(key, "key", dt, dev)
+        v_at, v_st, v_shape = _rows_of(value, "value", dt, dev)
+        if v_shape != shape or (q is not None and (shape[0] != T or shape[2] != D)):
             raise ValueError("key and value must be [num_tokens, num_kv_heads, head_size] like q")
-        a.key, a.key_stride = _rows_of(key, "key", dt)
-        a.value, a.value_stride = _rows_of(value, "value", dt)
-        Hkv, NB = key.shape[1], kv_cache.shape[1]
-        if (tuple(kv_cache.shape) != (2, NB, block_size, Hkv, a.head_size) or
+        T, Hkv, D = shape
+        quantised = kv_dtype == KV_FP8_E4M3_ROW or kv_dtype == KV_FP8_E4M3
+        cache_shape = kv_cache.shape
+        if (len(cache_shape) != 5 or cache_shape != (2, cache_shape[1], block_size, Hkv, D) or
                 not kv_cache.is_contiguous() or kv_cache.device != dev or
-                kv_cache.element_size() != (1 if kv_dtype in (KV_FP8_E4M3, KV_FP8_E4M3_ROW) else 2)):
+                kv_cache.element_size() != (1 if quantised else 2)):
             raise ValueError("kv_cache must be a contiguous [2, num_blocks, block_size, "
                              "num_kv_heads, head_size] tensor of the cache's type")
         if (slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or
                 slot_mapping.device != dev or not slot_mapping.is_contiguous()):
             raise ValueError("slot_mapping must be a contiguous int64 [num_tokens] tensor")
-        a.num_kv_heads, a.num_blocks = Hkv, NB
-        a.kv_cache, a.slot_mapping = kv_cache.data_ptr(), slot_mapping.data_ptr()
+        NB = cache_shape[1]
+        cache_at, slots_at = kv_cache.data_ptr(), slot_mapping.data_ptr()
         if kv_dtype == KV_FP8_E4M3_ROW:
             _check_row_scales(kv_scale, NB, block_size, Hkv, dev)
-            a.row_scales = kv_scale.data_ptr()
-        elif kv_dtype == KV_FP8_E4M3 and kv_scale is not None:
+            rows_at = kv_scale.data_ptr()
+        elif quantised and kv_scale is not None:
             scale = _scale_arg(kv_dtype, kv_scale)
-            a.kv_scale = ctypes.addressof(scale)
-    a.kv_dtype, a.block_size = int(kv_dtype), int(block_size)
+            scale_at = ctypes.addressof(scale)
+    pos_at = pos_st = table_at = axes_at = axes = max_pos = rot = 0
     if positions is not None:
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if (positions.dtype != torch.int64 or positions.shape[-1] != T or positions.dim() > 2 or
+        pos_shape = positions.shape
+        axes = 1 if len(pos_shape) == 1 else pos_shape[0]
+        if (positions.dtype != torch.int64 or not 1 <= len(pos_shape) <= 2 or pos_shape[-1] != T or
                 positions.device != dev or (T > 1 and positions.stride(-1) != 1)):
             raise ValueError("positions must be int64 [num_tokens] or [axes, num_tokens]")
         if (cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.device != dev or
                 not cos_sin.is_contiguous()):
             raise ValueError("cos_sin must be a contiguous fp32 [max_position, rot_dim] tensor")
-        a.positions, a.num_axes = positions.data_ptr(), axes
-        a.positions_stride = positions.stride(0) if axes > 1 else T
-        a.cos_sin = cos_sin.data_ptr()
-        a.max_position, a.rot_dim = cos_sin.shape
+        pos_at, table_at = positions.data_ptr(), cos_sin.data_ptr()
+        max_pos, rot = cos_sin.shape
         if axes > 1:
-            if pair_axis is None or len(pair_axis) != a.rot_dim // 2:
+            pos_st = positions.stride(0)
+            if pair_axis is None or len(pair_axis) != rot // 2:
                 raise ValueError("positions of several axes need pair_axis with rot_dim / 2 entries")
-            pairs = bytes(pair_axis)
-            a.pair_axis = ctypes.cast(ctypes.c_char_p(pairs), ctypes.c_void_p)
-    a.interleaved = int(interleaved)
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            pairs = ctypes.c_char_p(bytes(pair_axis))
+            axes_at = ctypes.cast(pairs, ctypes.c_void_p).value
+    norms = [0, 0]
+    for i, (name, w) in enumerate((("q_norm", q_norm), ("k_norm", k_norm))):
         if w is not None:
-            if w.dtype != dt or w.shape != (a.head_size,) or w.device != dev or not w.is_contiguous():
+            if w.dtype != dt or w.shape != (D,) or w.device != dev or not w.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dt} [head_size] tensor")
-            setattr(a, name, w.data_ptr())
-    a.norm_eps = norm_eps
-    if device_status is not None:
-        a.device_status = device_status.data_ptr()
+            norms[i] = w.data_ptr()
     if T == 0:  # (an empty tensor has no address)
         return q_out
-    a.stream = (stream or torch.cuda.current_stream(dev)).cuda_stream
-    st = load().pattn_rope_and_cache(ctypes.byref(a))
+    args = _ROPE_PACK.pack(
+        _ROPE_PACK.size, q_at, qo_at, k_at, v_at, q_st, qo_st, k_st, v_st, table_at, pos_at, pos_st,
+        axes_at, norms[0], norms[1], cache_at, rows_at, scale_at, slots_at,
+        0 if device_status is None else device_status.data_ptr(), _raw_stream(stream, dev),
+        norm_eps, T, H, Hkv, D, rot, interleaved, axes, max_pos, kv_dtype, block_size, NB)
+    st = load().pattn_rope_and_cache(args)
     if st != 0:
         raise PattnError(st, "pattn_rope_and_cache")
     return q_out
@@ -350,39 +375,47 @@ def gather_cache(kv_cache, block_table, out_start_loc, *, num_rows, block_size, 
     PattnError or ValueError."""
     import torch
     dev = kv_cache.device
-    NB, Hkv, D = kv_cache.shape[1], kv_cache.shape[3], kv_cache.shape[4]
-    if kv_cache.shape[2] != block_size or not kv_cache.is_contiguous():
+    cache_shape = kv_cache.shape
+    if len(cache_shape) != 5 or cache_shape[2] != block_size or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be a contiguous [2, num_blocks, block_size, num_kv_heads, "
                          "head_size] tensor")
-    if kv_cache.element_size() != (1 if kv_dtype in (KV_FP8_E4M3, KV_FP8_E4M3_ROW) else 2):
+    _, NB, _, Hkv, D = cache_shape
+    quantised = kv_dtype == KV_FP8_E4M3_ROW or kv_dtype == KV_FP8_E4M3
+    if kv_cache.element_size() != (1 if quantised else 2):
         raise ValueError("kv_cache must be of the cache's type")
-    B = block_table.shape[0]
-    for name, x, shape in (("block_table", block_table, (B, block_table.shape[1])),
-                           ("out_start_loc", out_start_loc, (B + 1,)),
-                           ("key_starts", key_starts, (B,))):
-        if x is not None and (x.dtype != torch.int32 or x.shape != shape or x.device != dev or
-                              not x.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}")
+    B, mbps = block_table.shape
+    i32 = torch.int32
+    if (block_table.dtype != i32 or block_table.device != dev or not block_table.is_contiguous() or
+            out_start_loc.dtype != i32 or out_start_loc.shape != (B + 1,) or
+            out_start_loc.device != dev or not out_start_loc.is_contiguous()):
+        raise ValueError("block_table and out_start_loc must be contiguous int32 tensors "
+                         "[num_seqs, blocks] and [num_seqs + 1]")
+    starts_at = 0
+    if key_starts is not None:
+        if (key_starts.dtype != i32 or key_starts.shape != (B,) or key_starts.device != dev or
+                not key_starts.is_contiguous()):
+            raise ValueError("key_starts must be a contiguous int32 [num_seqs] tensor")
+        starts_at = key_starts.data_ptr()
     if kv_dtype == KV_FP8_E4M3_ROW:
         _check_row_scales(kv_scale, NB, block_size, Hkv, dev)
     dt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
     shape = (num_rows, Hkv, D)
-    if key_out is None:
-        key_out = torch.empty(shape, dtype=dt, device=dev)
-    if value_out is None:
-        value_out = torch.empty(shape, dtype=dt, device=dev)
+    outs = []
     for x in (key_out, value_out):
-        if x.shape != shape or x.dtype != dt or x.device != dev or not x.is_contiguous():
+        if x is None:
+            x = torch.empty(shape, dtype=dt, device=dev)
+        elif x.shape != shape or x.dtype != dt or x.device != dev or not x.is_contiguous():
             raise ValueError(f"key_out and value_out must be contiguous {dt} tensors of shape {shape}")
+        outs.append(x)
+    key_out, value_out = outs
     if num_rows == 0 or B == 0:  # (an empty tensor has no address)
         return key_out, value_out
     st = load().pattn_gather_cache(
-        kv_cache.data_ptr(), block_table.data_ptr(),
-        None if key_starts is None else key_starts.data_ptr(), out_start_loc.data_ptr(),
-        key_out.data_ptr(), value_out.data_ptr(), B, int(num_rows), block_table.shape[1], NB, Hkv, D,
-        int(block_size), int(kv_dtype), _scale_arg(kv_dtype, kv_scale),
-        None if device_status is None else device_status.data_ptr(),
-        (stream or torch.cuda.current_stream(dev)).cuda_stream)
+        kv_cache.data_ptr(), block_table.data_ptr(), starts_at or None, out_start_loc.data_ptr(),
+        key_out.data_ptr(), value_out.data_ptr(), B, int(num_rows), mbps, NB, Hkv, D,
+        int(block_size), int(kv_dtype),
+        _scale_arg(kv_dtype, kv_scale), None if device_status is None else device_status.data_ptr(),
+        _raw_stream(stream, dev))
     if st != 0:
         raise PattnError(st, "pattn_gather_cache")
     return key_out, value_out
@@ -517,6 +550,10 @@ class Workspace:
     def __init__(self):
         self.buf = None
 
+    def current(self, device):
+        """The buffer it has on ``device``, or None."""
+        return self.buf if self.buf is not None and self.buf.device == device else None
+
     def get(self, nbytes, device):
         import torch
         nbytes = max(256, int(nbytes))
@@ -563,27 +600,37 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
     if out is None:
         odt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
         out = torch.empty((T, num_heads, head_size_v or head_size), dtype=odt, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
     num_blocks = kv_cache.shape[0] if head_size_v else kv_cache.shape[1]
     if kv_dtype == KV_FP8_E4M3_ROW:
         _check_row_scales(kv_scale, num_blocks, block_size, num_kv_heads, dev)
-    ext = make_ext(num_seqs=seq_lens.shape[0], num_tokens=T,
-                   max_blocks_per_seq=block_table.shape[1], num_blocks=num_blocks,
-                   max_query_len=max_query_len, max_seq_len=max_seq_len,
-                   num_splits=num_splits, stream=stream.cuda_stream,
-                   timing_events=timing_events, sinks=_sinks_ptr(sinks, num_heads, dev),
-                   head_size_v=head_size_v)
-    need = pattn_workspace_bytes(ext, num_heads, num_kv_heads, head_size, block_size, lib=lib)
-    if need == 0:
-        raise PattnError(1, "pattn_workspace_bytes")
-    ws = (workspace or _default_ws).get(need, dev)
-    ext.workspace = ws.data_ptr()
-    ext.workspace_bytes = ws.numel()
-    st = pattn_varlen_fwd(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
-                          seq_lens.data_ptr(), query_start_loc.data_ptr(), out.data_ptr(),
-                          scale, num_heads, num_kv_heads, head_size, block_size, window,
-                          causal, kv_dtype, kv_scale, ext, lib=lib)
+    mbps = block_table.shape[1]
+    raw_stream = _raw_stream(stream, dev)
+    events = None
+    if timing_events is not None:
+        events = (ctypes.c_void_p * 8)(*[int(x) for x in timing_events])
+    ws = workspace or _default_ws
+    buf = ws.current(dev)
+    ext = Ext.from_buffer_copy(_EXT_PACK.pack(
+        _EXT_PACK.size, seq_lens.shape[0], T, mbps, num_blocks, max_query_len, max_seq_len,
+        num_splits, 0 if buf is None else buf.data_ptr(), 0 if buf is None else buf.numel(),
+        raw_stream, 0 if events is None else ctypes.addressof(events),
+        _sinks_ptr(sinks, num_heads, dev), head_size_v))
+    ext._events_keepalive = events
+    run = (lib or load()).pattn_varlen_fwd
+    args = (q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            query_start_loc.data_ptr(), out.data_ptr(), float(scale), int(num_heads),
+            int(num_kv_heads), int(head_size), int(block_size), int(window), int(causal),
+            int(kv_dtype), _scale_arg(kv_dtype, kv_scale), ext)
+    # the library itself says when the workspace is missing or too small
+    st = 3 if buf is None else run(*args)
+    if st != 0:
+        need = pattn_workspace_bytes(ext, num_heads, num_kv_heads, head_size, block_size, lib=lib)
+        if need == 0:
+            raise PattnError(1, "pattn_workspace_bytes")
+        if st == 3:
+            buf = ws.get(need, dev)
+            ext.workspace, ext.workspace_bytes = buf.data_ptr(), buf.numel()
+            st = run(*args)
     if check and st != 0:
         raise PattnError(st, "pattn_varlen_fwd")
     forward.last_ext = ext
