@@ -109,6 +109,10 @@ __host__ __device__ constexpr bool kv_is_e4m3(int kv_dtype) {
   return kv_dtype == PATTN_KV_FP8_E4M3 || kv_dtype == PATTN_KV_FP8_E4M3_ROW;
 }
 
+// Number of SMs of the current device (cached per device; 152 if it cannot be
+// asked).
+int current_sms();
+
 // Checks a call's cache type and kv_scale (host only; the row scales of
 // PATTN_KV_FP8_E4M3_ROW are a device address).
 pattn_status_t check_kv_scale(int kv_dtype, const float* kv_scale);

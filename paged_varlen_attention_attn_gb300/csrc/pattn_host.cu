@@ -39,20 +39,6 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Number of SMs of the current device (cached per device).
-int sm_count() {
-  static int counts[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-  if (counts[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-      n = 152;
-    counts[dev] = n;
-  }
-  return counts[dev];
-}
-
 // The struct grows at its end: a struct_size that reaches the field before
 // `sinks` is a complete older struct.
 bool ext_ok(const pattn_ext_t* ext) {
@@ -88,7 +74,7 @@ int choose_splits(const pattn_ext_t* ext, int num_kv_heads, int block_size, int 
                                    : ext->max_seq_len;
   const int max_blocks = std::max(1, (visible + block_size - 1) / block_size);
   const long long items = static_cast<long long>(std::max(1, ext->num_seqs)) * num_kv_heads;
-  const int sms = sm_count();
+  const int sms = current_sms();
   int by_grid = static_cast<int>(7LL * sms / items);
   int by_len = (visible + 8191) / 8192;
   int s = std::max(1, std::max(by_grid, by_len));
@@ -161,7 +147,7 @@ pattn_status_t check_call(const void* q, const void* kv_cache, const int32_t* bl
 // reproduce.)  The estimate only balances the two kernels; the result does
 // not depend on it.
 void set_cost_model(Problem& p) {
-  p.num_sms = sm_count();
+  p.num_sms = current_sms();
   const bool fp8 = kv_is_e4m3(p.kv_dtype);
   p.pf_us_per_tile = (p.D == 128 ? 2.1f : 1.3f) * (fp8 ? 1.3f : 1.f);
   p.dec_bytes_per_us = fp8 ? 100000.f : 120000.f;
@@ -259,7 +245,7 @@ CascadeLayout cascade_layout(const pattn_ext_t* ext, int H, int Hkv, int D, int 
     const long long items = static_cast<long long>((ext->num_tokens + prefill_rows_per_item(G) - 1) /
                                                    prefill_rows_per_item(G)) *
                             ((G % 2 == 0) ? H / 2 : H);
-    const long long want = (2LL * sm_count() + items - 1) / std::max(1LL, items);
+    const long long want = (2LL * current_sms() + items - 1) / std::max(1LL, items);
     long long kc = std::min(want, 16LL);
     kc = std::min(kc, static_cast<long long>((prefix + BLOCK_N - 1) / BLOCK_N));
     c.kc = static_cast<int>(std::max(1LL, kc));
@@ -392,6 +378,19 @@ bool encode_diffkv_map(CUtensorMap* map, const void* cache, int kv_dtype, int dk
              4, const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int current_sms() {
+  static int counts[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  if (counts[dev] == 0) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+      n = 152;
+    counts[dev] = n;
+  }
+  return counts[dev];
 }
 
 // The cache type and its scales (host only).

@@ -1658,20 +1658,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 
 int prefill_rows_per_item(int G) { return (G % 2 == 0) ? BLOCK_M : 2 * BLOCK_M; }
 
-// Number of SMs of the current device (cached per device).
-static int prefill_sms() {
-  static int counts[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-  if (counts[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-      n = 152;
-    counts[dev] = n;
-  }
-  return counts[dev];
-}
-
 template <int D, bool HALF, bool FP8, bool TWO, bool ROWS = false>
 cudaError_t launch_prefill_t(const Problem& p, const CUtensorMap& q_map, const CUtensorMap& k_map,
                              const CUtensorMap& v_map,
@@ -1705,7 +1691,7 @@ cudaError_t launch_prefill(const Problem& p, const CUtensorMap& q_map, const CUt
   // columns of one CTA fill an SM), capped by the host-side bound on items.
   const long long items = static_cast<long long>(p.max_tiles) * NP * p.kv_chunks;
   if (items == 0) return cudaSuccess;
-  const unsigned g = static_cast<unsigned>(std::min<long long>(items, prefill_sms()));
+  const unsigned g = static_cast<unsigned>(std::min<long long>(items, current_sms()));
   // A 16-bit cache takes two MMA issuers (measured against one: varlen prefill
   // 1.279 -> 1.199 ms, the mixed chunked-prefill step 1.149 -> 1.108 ms).
   if (p.kv_dtype == PATTN_KV_F16)

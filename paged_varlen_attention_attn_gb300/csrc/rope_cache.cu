@@ -18,10 +18,8 @@
 // lanes own one head row (head sizes up to 64 / 128 / 256), 16 elements each
 // as two 16-byte pieces: the two pieces that a rotation in halves pairs up, so
 // a lane holds both elements of its eight pairs and a row's sum of squares and
-// largest magnitude are log2(LPR) shuffles.  A warp serves 32 / LPR rows of
-// one token at a time and walks the token's rows, so the eight cos and sin
-// values of its lanes are loaded once, and the next rows' pieces load while
-// the current ones are worked on.
+// largest magnitude are log2(LPR) shuffles.  A warp's step serves 32 / LPR rows
+// of one token, of one kind (q, k or v).
 #include <algorithm>
 #include <cmath>
 
@@ -50,10 +48,12 @@ struct RopeParams {
   void* cache;
   float* row_scales;
   unsigned* status;
-  float eps, k_scale, v_scale;
+  float eps, inv_d, k_scale, v_scale;
   int T, H, Hkv, D, rot, max_pos, axes, adjacent, vec4;
-  int nq, rows;            // q rows of a token (0 without q), all its rows
-  int chunks, iters;       // warps per token, steps of 32 / LPR rows each takes
+  int steps_q, steps_kv;   // steps of 32 / LPR rows of a token's q; of its k (and v)
+  int stages, stage_bytes;  // ring of the streaming kernel
+  int team;                 // warps per token there
+  int packed;               // a token's q, k and v rows follow one another
   int bs, NB;
   unsigned char axis[128];  // axis of each rotary pair (axes > 1)
 };
@@ -94,49 +94,237 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float sc) {
   return make_uint2(w[0], w[1]);
 }
 
-// LPR: lanes per row.  KIND: the cache (PATTN_KV_*); f16 data goes with KIND
-// PATTN_KV_F16, bf16 data with every other.
-template <int LPR, int KIND>
-__global__ void __launch_bounds__(RC_THREADS)
-    rope_cache_kernel(const __grid_constant__ RopeParams p) {
+// (a0, a1) * (b0, b1) + (c0, c1) and (a0, a1) * (b0, b1) on the paired fp32 pipe.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// The eight pairs of a lane, a[] and b[], turned: a c - b s, b c + a s.
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&cs)[8],
+                                     const float (&sn)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 a2 = make_float2(a[e], a[e + 1]), b2 = make_float2(b[e], b[e + 1]);
+    const float2 c2 = make_float2(cs[e], cs[e + 1]), s2 = make_float2(sn[e], sn[e + 1]);
+    const float2 x = fma2(make_float2(-b2.x, -b2.y), s2, mul2(a2, c2));
+    const float2 y = fma2(a2, s2, mul2(b2, c2));
+    a[e] = x.x;
+    a[e + 1] = x.y;
+    b[e] = y.x;
+    b[e + 1] = y.y;
+  }
+}
+
+enum RowKind { ROW_Q, ROW_K, ROW_V };
+
+// A lane's place: lane j of the LPR that own a row, and the first elements c0 and
+// c1 of its two pieces: of a rotating lane pieces j and j + rot / 16, of the
+// others the pieces behind the rotated part, in pairs.
+struct LanePlace {
+  int j, g, c0, c1;
+  bool on, turns;
+};
+template <int LPR>
+__device__ __forceinline__ LanePlace lane_place(const RopeParams& p, int lane) {
+  LanePlace l;
+  l.j = lane % LPR;
+  l.g = lane / LPR;
+  const int half = p.rot / 16;  // 8-element pieces of one half of the rotated part
+  l.on = l.j < p.D / 16;
+  l.turns = l.on && l.j < half;
+  l.c0 = (l.turns ? l.j : 2 * l.j) * 8;
+  l.c1 = (l.turns ? l.j + half : 2 * l.j + 1) * 8;
+  return l;
+}
+
+// The cos and sin of a lane's eight pairs: pairs 8j .. 8j + 7 (halves), or, of
+// adjacent elements, the four of each piece.  row(a): the table row of the
+// token's position on axis a.
+template <class Row>
+__device__ __forceinline__ void load_turns(const RopeParams& p, const LanePlace& l, Row row,
+                                           float (&cs)[8], float (&sn)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int p0 = p.adjacent ? (h ? l.c1 : l.c0) / 2 : 8 * l.j + 4 * h;
+    if (p.vec4) {
+      const float* r = row(p.axes > 1 ? p.axis[p0] : 0) + p0;
+      const float4 c = *reinterpret_cast<const float4*>(r);
+      const float4 s = *reinterpret_cast<const float4*>(r + p.rot / 2);
+      cs[4 * h] = c.x; cs[4 * h + 1] = c.y; cs[4 * h + 2] = c.z; cs[4 * h + 3] = c.w;
+      sn[4 * h] = s.x; sn[4 * h + 1] = s.y; sn[4 * h + 2] = s.z; sn[4 * h + 3] = s.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float* r = row(p.axis[p0 + e]) + p0 + e;
+        cs[4 * h + e] = r[0];
+        sn[4 * h + e] = r[p.rot / 2];
+      }
+    }
+  }
+}
+
+// A lane's pieces of a norm's weights.
+struct NormWeights {
+  uint4 a, b;
+  bool on;
+};
+__device__ __forceinline__ NormWeights norm_weights(const LanePlace& l, const uint16_t* w) {
+  NormWeights n;
+  n.on = w != nullptr;
+  n.a = n.b = make_uint4(0u, 0u, 0u, 0u);
+  if (n.on && l.on) {
+    n.a = *reinterpret_cast<const uint4*>(w + l.c0);
+    n.b = *reinterpret_cast<const uint4*>(w + l.c1);
+  }
+  return n;
+}
+
+// One step of a warp: head h's row of the token (one row per LPR lanes, all of
+// one kind; pieces wa and wb) normed, turned and written.  slot: the token's
+// cache slot (k and v).  live: the lane has a part of a row that exists.
+template <int LPR, int KIND, RowKind R>
+__device__ __forceinline__ void serve_row(const RopeParams& p, const LanePlace& l,
+                                          const NormWeights& w, const uint4& wa, const uint4& wb,
+                                          const float (&cs)[8], const float (&sn)[8], int t, int h,
+                                          int64_t slot, bool live) {
   constexpr bool HALF = KIND == PATTN_KV_F16;
   constexpr bool QUANT = KIND == PATTN_KV_FP8_E4M3 || KIND == PATTN_KV_FP8_E4M3_ROW;
-  constexpr int RPS = 32 / LPR;  // rows per step of a warp
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (RC_THREADS / 32) + (threadIdx.x >> 5);
-  const int t = static_cast<int>(unit / p.chunks);
-  if (t >= p.T) return;
-  const int chunk = static_cast<int>(unit - static_cast<int64_t>(t) * p.chunks);
-  const int lane = threadIdx.x & 31;
-  const int j = lane % LPR, g = lane / LPR;
-  const int half = p.rot / 16;      // 8-element pieces of one half of the rotated part
-  const bool lane_on = j < p.D / 16;
-  const bool turns = lane_on && j < half;
-  // this lane's two pieces: a rotating lane's j and j + half, then pairs of
-  // pieces behind the rotated part
-  const int c0 = turns ? j : 2 * j, c1 = turns ? j + half : 2 * j + 1;
-
-  // row `row` of the token: q heads, then k heads, then v heads
-  const int row0 = chunk * p.iters * RPS + g;
-  const int row_end = min(p.rows, (chunk + 1) * p.iters * RPS);
-  auto src_of = [&](int row) -> const uint16_t* {
-    if (row < p.nq) return p.q + t * p.q_stride + static_cast<int64_t>(row) * p.D;
-    row -= p.nq;
-    return row < p.Hkv ? p.key + t * p.k_stride + static_cast<int64_t>(row) * p.D
-                       : p.value + t * p.v_stride + static_cast<int64_t>(row - p.Hkv) * p.D;
-  };
-  auto load = [&](int row, uint4& a, uint4& b) {
-    a = b = make_uint4(0u, 0u, 0u, 0u);
-    if (lane_on && row < row_end) {
-      const uint16_t* s = src_of(row);
-      a = *reinterpret_cast<const uint4*>(s + c0 * 8);
-      b = *reinterpret_cast<const uint4*>(s + c1 * 8);
+  float x[8], y[8];
+  unpack8<HALF>(wa, x);
+  unpack8<HALF>(wb, y);
+  if (R != ROW_V && w.on) {
+    float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float2 a = make_float2(x[e], x[e + 1]), b = make_float2(y[e], y[e + 1]);
+      s2 = fma2(b, b, fma2(a, a, s2));
     }
-  };
-  // two steps' rows are in flight while the positions and the table load
-  uint4 na0, nb0, na1, nb1;
-  load(row0, na0, nb0);
-  load(row0 + RPS, na1, nb1);
+    float ss = s2.x + s2.y;
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(ss * p.inv_d + p.eps);
+    const float2 r2 = make_float2(r, r);
+    float wx[8], wy[8];
+    unpack8<HALF>(w.a, wx);
+    unpack8<HALF>(w.b, wy);
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float2 a = mul2(make_float2(x[e], x[e + 1]), mul2(r2, make_float2(wx[e], wx[e + 1])));
+      const float2 b = mul2(make_float2(y[e], y[e + 1]), mul2(r2, make_float2(wy[e], wy[e + 1])));
+      x[e] = a.x;
+      x[e + 1] = a.y;
+      y[e] = b.x;
+      y[e + 1] = b.y;
+    }
+  }
+  if (R != ROW_V && l.turns) {
+    if (p.adjacent) {
+      float a[8], b[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] = x[2 * e];
+        b[e] = x[2 * e + 1];
+        a[4 + e] = y[2 * e];
+        b[4 + e] = y[2 * e + 1];
+      }
+      turn(a, b, cs, sn);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = a[e];
+        x[2 * e + 1] = b[e];
+        y[2 * e] = a[4 + e];
+        y[2 * e + 1] = b[4 + e];
+      }
+    } else {
+      turn(x, y, cs, sn);
+    }
+  }
+  if constexpr (R == ROW_Q) {
+    if (live) {
+      uint16_t* d = p.q_out + t * p.qo_stride + h * p.D;
+      *reinterpret_cast<uint4*>(d + l.c0) = pack8<HALF>(x);
+      *reinterpret_cast<uint4*>(d + l.c1) = pack8<HALF>(y);
+    }
+  } else {
+    constexpr int kv = R == ROW_V ? 1 : 0;
+    const int64_t dst = ((static_cast<int64_t>(kv) * p.NB * p.bs + slot) * p.Hkv + h) * p.D;
+    if constexpr (QUANT) {
+      float scale = kv ? p.v_scale : p.k_scale;
+      if constexpr (KIND == PATTN_KV_FP8_E4M3_ROW) {
+        // the row's largest magnitude (NaN elements do not count)
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(x[e]), fabsf(y[e])));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        scale = fminf(fmaxf(__fdiv_rn(m, E4M3_MAX), PATTN_ROW_SCALE_MIN), PATTN_ROW_SCALE_MAX);
+      }
+      if (live) {
+        unsigned char* d = static_cast<unsigned char*>(p.cache) + dst;
+        *reinterpret_cast<uint2*>(d + l.c0) = codes8(x, scale);
+        *reinterpret_cast<uint2*>(d + l.c1) = codes8(y, scale);
+        // slot = block * bs + offset, so slot / 16 counts the groups of 16 slots
+        if constexpr (KIND == PATTN_KV_FP8_E4M3_ROW)
+          if (l.j == 0)
+            p.row_scales[((slot >> 4) * p.Hkv + h) * 32 + kv * 16 + (slot & 15)] = scale;
+      }
+    } else if (live) {
+      uint16_t* d = static_cast<uint16_t*>(p.cache) + dst;
+      *reinterpret_cast<uint4*>(d + l.c0) = pack8<HALF>(x);
+      *reinterpret_cast<uint4*>(d + l.c1) = pack8<HALF>(y);
+    }
+  }
+}
 
+// ------------------------------------------------------------- few tokens
+// One warp per step (latency: every load of the call is in flight at once).
+template <int LPR, int KIND>
+__global__ void __launch_bounds__(RC_THREADS)
+    rope_few_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int RPS = 32 / LPR;  // rows per step
+  const int steps = p.steps_q + 2 * p.steps_kv;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (RC_THREADS / 32) + (threadIdx.x >> 5);
+  const int t = static_cast<int>(unit / steps);
+  if (t >= p.T) return;
+  const int step = static_cast<int>(unit - static_cast<int64_t>(t) * steps);
+  const int lane = threadIdx.x & 31;
+  const LanePlace l = lane_place<LPR>(p, lane);
+  int i = step;
+  const RowKind kind = i < p.steps_q ? ROW_Q : i < p.steps_q + p.steps_kv ? ROW_K : ROW_V;
+  i -= kind == ROW_Q ? 0 : kind == ROW_K ? p.steps_q : p.steps_q + p.steps_kv;
+  const int h = i * RPS + l.g;
+  const bool live = l.on && h < (kind == ROW_Q ? p.H : p.Hkv);
+  uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
+  if (live) {
+    const uint16_t* src = (kind == ROW_Q   ? p.q + t * p.q_stride
+                           : kind == ROW_K ? p.key + t * p.k_stride
+                                           : p.value + t * p.v_stride) +
+                          h * p.D;
+    wa = *reinterpret_cast<const uint4*>(src + l.c0);
+    wb = *reinterpret_cast<const uint4*>(src + l.c1);
+  }
+  int64_t slot = 0;
+  if (kind != ROW_Q) slot = p.slots[t];
   // The token's positions: a negative first one marks padding (nothing of the
   // token is written), any other outside the table is reported and skipped.
   float cs[8], sn[8];
@@ -149,170 +337,238 @@ __global__ void __launch_bounds__(RC_THREADS)
       bad |= pos[a] < 0 || pos[a] >= p.max_pos;
     }
     if (bad) {
-      if (pos[0] >= 0 && chunk == 0 && lane == 0) flag_status(p.status, PATTN_DEV_BAD_METADATA);
+      if (pos[0] >= 0 && step == 0 && lane == 0) flag_status(p.status, PATTN_DEV_BAD_METADATA);
       return;
     }
-    if (turns) {
-      // pairs of the lane: 8j .. 8j + 7 (halves), or, of adjacent elements,
-      // the four of each piece
+    if (l.turns && kind != ROW_V)
+      load_turns(p, l, [&](int a) {
+        return p.table + (a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3]) * p.rot;
+      }, cs, sn);
+  }
+  if (kind != ROW_Q && slot >= static_cast<int64_t>(p.NB) * p.bs) {
+    if (step == p.steps_q && lane == 0) flag_status(p.status, PATTN_DEV_BAD_METADATA);
+    return;
+  }
+  if (slot < 0) return;
+  const NormWeights w = norm_weights(l, kind == ROW_Q ? p.q_norm : kind == ROW_K ? p.k_norm : nullptr);
+  if (kind == ROW_Q) serve_row<LPR, KIND, ROW_Q>(p, l, w, wa, wb, cs, sn, t, h, slot, live);
+  else if (kind == ROW_K) serve_row<LPR, KIND, ROW_K>(p, l, w, wa, wb, cs, sn, t, h, slot, live);
+  else serve_row<LPR, KIND, ROW_V>(p, l, w, wa, wb, cs, sn, t, h, slot, live);
+}
+
+// ------------------------------------------------------------- many tokens
+// Persistent CTAs stream their tokens through a ring of shared-memory stages:
+// a producer warp reads positions and slots 32 tokens at a time and copies each
+// token's q, k and v rows and table rows with untiled bulk copies (one for the
+// rows of a packed projection, q, k and v side by side), up to a ring of them
+// ahead.  The bytes in flight then depend on the ring, not on what the warps'
+// registers hold.  Eight consumer warps work in teams of one to eight, a team
+// per token: the smaller, the more rows share a warp's cos, sin and norm
+// weights, the larger, the fewer stages the teams hold.
+constexpr int RS_WARPS = 8;  // consumer warps
+constexpr int RS_STAGES_MAX = 8;
+constexpr int RS_RING_BYTES = 100 * 1024;  // two CTAs per SM
+constexpr int RS_HEAD = 256;               // barriers and the stages' tokens
+
+struct StreamHead {
+  uint64_t full[RS_STAGES_MAX], empty[RS_STAGES_MAX];
+  int64_t slot[RS_STAGES_MAX];  // the stage's token: its cache slot, -1 for none
+  int token[RS_STAGES_MAX];     // and index; -1: no more tokens
+};
+static_assert(sizeof(StreamHead) <= RS_HEAD, "the ring's head fits the space kept for it");
+
+template <int LPR, int KIND>
+__global__ void __launch_bounds__((RS_WARPS + 1) * 32, 2)
+    rope_stream_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int RPS = 32 / LPR;
+  extern __shared__ __align__(128) unsigned char smem[];
+  StreamHead* hd = reinterpret_cast<StreamHead*>(smem);
+  unsigned char* ring = smem + RS_HEAD;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q_bytes = p.H * p.D * 2, kv_bytes = p.Hkv * p.D * 2;
+  const int row_bytes = p.rot * 4;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&hd->full[i], 1);
+      mbar_init(&hd->empty[i], p.team);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp == RS_WARPS) {
+    // ---------------------------------------------------------- producer
+    int n = 0;  // stages filled so far
+    bool ok = true;
+    auto stage_free = [&]() {
+      return n < p.stages || mbar_wait(&hd->empty[n % p.stages], ((n / p.stages) - 1) & 1, p.status,
+                                       nullptr);
+    };
+    for (int64_t base = blockIdx.x; ok && base < p.T; base += 32LL * gridDim.x) {
+      const int64_t mine = base + static_cast<int64_t>(lane) * gridDim.x;
+      int64_t slot = -1;
+      int pos[4] = {0, 0, 0, 0};
+      bool skip = mine >= p.T;
+      if (!skip) {
+        // as in rope_few_kernel: padding and bad tokens
+        bool bad = false, padding = false;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int p0 = p.adjacent ? 4 * (h ? c1 : c0) : 8 * j + 4 * h;
-        if (p.vec4) {
-          const int a = p.axes > 1 ? p.axis[p0] : 0;
-          const int64_t at = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
-          const float* trow = p.table + at * p.rot + p0;
-          const float4 c = *reinterpret_cast<const float4*>(trow);
-          const float4 s = *reinterpret_cast<const float4*>(trow + p.rot / 2);
-          cs[4 * h] = c.x; cs[4 * h + 1] = c.y; cs[4 * h + 2] = c.z; cs[4 * h + 3] = c.w;
-          sn[4 * h] = s.x; sn[4 * h + 1] = s.y; sn[4 * h + 2] = s.z; sn[4 * h + 3] = s.w;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int a = p.axis[p0 + e];
-            const int64_t at = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
-            cs[4 * h + e] = p.table[at * p.rot + p0 + e];
-            sn[4 * h + e] = p.table[at * p.rot + p.rot / 2 + p0 + e];
+        for (int a = 0; a < 4; ++a) {
+          const int64_t x = a < p.axes ? p.positions[a * p.pos_stride + mine] : 0;
+          bad |= x < 0 || x >= p.max_pos;
+          if (a == 0) padding = x < 0;
+          pos[a] = static_cast<int>(x);
+        }
+        skip = p.axes > 0 && bad;
+        if (skip && !padding) flag_status(p.status, PATTN_DEV_BAD_METADATA);
+        if (p.Hkv > 0 && !skip) {
+          slot = p.slots[mine];
+          if (slot >= static_cast<int64_t>(p.NB) * p.bs) {
+            flag_status(p.status, PATTN_DEV_BAD_METADATA);
+            slot = -1;
           }
         }
       }
+      if (p.H == 0 && slot < 0) skip = true;  // nothing to write
+      unsigned todo = __ballot_sync(0xffffffffu, !skip);
+      while (ok && todo) {
+        const int from = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int t = static_cast<int>(base + static_cast<int64_t>(from) * gridDim.x);
+        const int64_t s = __shfl_sync(0xffffffffu, slot, from);
+        int at[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) at[a] = __shfl_sync(0xffffffffu, pos[a], from);
+        if (lane == 0) {
+          ok = stage_free();
+          if (ok) {
+            const int st = n % p.stages;
+            unsigned char* d = ring + st * p.stage_bytes;
+            hd->token[st] = t;
+            hd->slot[st] = s;
+            const int kvb = s >= 0 ? kv_bytes : 0;
+            mbar_arrive_expect_tx(&hd->full[st], q_bytes + 2 * kvb + p.axes * row_bytes);
+            if (q_bytes)
+              bulk_load(d, p.q + t * p.q_stride, p.packed ? q_bytes + 2 * kvb : q_bytes,
+                        &hd->full[st]);
+            if (kvb && !p.packed) {
+              bulk_load(d + q_bytes, p.key + t * p.k_stride, kvb, &hd->full[st]);
+              bulk_load(d + q_bytes + kv_bytes, p.value + t * p.v_stride, kvb, &hd->full[st]);
+            }
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+              if (a < p.axes)
+                bulk_load(d + q_bytes + 2 * kv_bytes + a * row_bytes,
+                          p.table + static_cast<int64_t>(at[a]) * p.rot, row_bytes, &hd->full[st]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (ok) ++n;
+      }
     }
-  }
-  // Where the token's key and value rows go; -1: nowhere.
-  int64_t blk = -1;
-  int off = 0;
-  if (p.Hkv > 0) {
-    const int64_t s = p.slots[t];
-    if (s >= static_cast<int64_t>(p.NB) * p.bs) {
-      if (chunk == 0 && lane == 0) flag_status(p.status, PATTN_DEV_BAD_METADATA);
-    } else if (s >= 0) {
-      blk = s / p.bs;
-      off = static_cast<int>(s - blk * p.bs);
+    if (lane == 0) {
+      // one end mark for each team
+      const int end = n + RS_WARPS / p.team;
+      for (; ok && n < end; ++n) {
+        if (!(ok = stage_free())) break;
+        hd->token[n % p.stages] = -1;
+        mbar_arrive(&hd->full[n % p.stages]);
+      }
+      if (!ok) {
+        // a wait gave up: no copy may still be writing shared memory at the exit
+        drain_armed(hd->full, p.stages, n, -1, p.status);
+      }
     }
+    return;
   }
-  const bool normed = p.q_norm != nullptr || p.k_norm != nullptr;
-  const float inv_d = 1.f / static_cast<float>(p.D);
 
-  for (int i = 0; i < p.iters; ++i) {
-    const int row = row0 + i * RPS;
-    const uint4 wa = na0, wb = nb0;
-    na0 = na1;
-    nb0 = nb1;
-    load(row + 2 * RPS, na1, nb1);
-    const bool live = row < row_end;
-    const int kind = row < p.nq ? 0 : row < p.nq + p.Hkv ? 1 : 2;  // q, k, v
-    float x[8], y[8];
-    unpack8<HALF>(wa, x);
-    unpack8<HALF>(wb, y);
-    if (normed) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss += x[e] * x[e] + y[e] * y[e];
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const uint16_t* w = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
-      if (w && lane_on) {
-        const float r = rsqrtf(ss * inv_d + p.eps);
-        float wx[8], wy[8];
-        unpack8<HALF>(*reinterpret_cast<const uint4*>(w + c0 * 8), wx);
-        unpack8<HALF>(*reinterpret_cast<const uint4*>(w + c1 * 8), wy);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] *= r * wx[e];
-          y[e] *= r * wy[e];
-        }
+  // ------------------------------------------------------------ consumers
+  const LanePlace l = lane_place<LPR>(p, lane);
+  const NormWeights wq = norm_weights(l, p.q_norm);
+  const int steps = p.steps_q + 2 * p.steps_kv;
+  const int teams = RS_WARPS / p.team, me = warp % p.team;
+  for (int n = warp / p.team;; n += teams) {
+    const int st = n % p.stages;
+    if (!__all_sync(0xffffffffu, mbar_wait(&hd->full[st], (n / p.stages) & 1, p.status, nullptr)))
+      return;
+    const int t = *static_cast<volatile int*>(&hd->token[st]);
+    if (t < 0) return;
+    const int64_t slot = *static_cast<volatile int64_t*>(&hd->slot[st]);
+    const unsigned char* d = ring + st * p.stage_bytes;
+    float cs[8], sn[8];
+    if (l.turns) {
+      const float* rows = reinterpret_cast<const float*>(d + q_bytes + 2 * kv_bytes);
+      load_turns(p, l, [&](int a) { return rows + a * p.rot; }, cs, sn);
+    }
+    // the members' shares of the steps move on by one with each token
+    const int end = slot >= 0 ? steps : p.steps_q;
+    for (int i = (me + n) % p.team; i < end; i += p.team) {
+      const bool is_q = i < p.steps_q, is_k = !is_q && i < p.steps_q + p.steps_kv;
+      const int h = (i - (is_q ? 0 : is_k ? p.steps_q : p.steps_q + p.steps_kv)) * RPS + l.g;
+      const bool live = l.on && h < (is_q ? p.H : p.Hkv);
+      uint4 wa = make_uint4(0u, 0u, 0u, 0u), wb = wa;
+      if (live) {
+        const unsigned char* src = d + (is_q ? 0 : is_k ? q_bytes : q_bytes + kv_bytes) + h * p.D * 2;
+        wa = *reinterpret_cast<const uint4*>(src + l.c0 * 2);
+        wb = *reinterpret_cast<const uint4*>(src + l.c1 * 2);
       }
+      if (is_q) serve_row<LPR, KIND, ROW_Q>(p, l, wq, wa, wb, cs, sn, t, h, slot, live);
+      else if (is_k)
+        serve_row<LPR, KIND, ROW_K>(p, l, norm_weights(l, p.k_norm), wa, wb, cs, sn, t, h, slot, live);
+      else serve_row<LPR, KIND, ROW_V>(p, l, wq, wa, wb, cs, sn, t, h, slot, live);
     }
-    if (p.axes > 0 && kind < 2 && turns) {
-      if (p.adjacent) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = x[2 * e], b = x[2 * e + 1], c = y[2 * e], d = y[2 * e + 1];
-          x[2 * e] = a * cs[e] - b * sn[e];
-          x[2 * e + 1] = b * cs[e] + a * sn[e];
-          y[2 * e] = c * cs[4 + e] - d * sn[4 + e];
-          y[2 * e + 1] = d * cs[4 + e] + c * sn[4 + e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float a = x[e], b = y[e];
-          x[e] = a * cs[e] - b * sn[e];
-          y[e] = b * cs[e] + a * sn[e];
-        }
-      }
-    }
-    float scale = kind == 1 ? p.k_scale : p.v_scale;
-    if constexpr (KIND == PATTN_KV_FP8_E4M3_ROW) {
-      // the row's largest magnitude (NaN elements do not count)
-      float m = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fmaxf(fabsf(x[e]), fabsf(y[e])));
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      scale = fminf(fmaxf(__fdiv_rn(m, E4M3_MAX), PATTN_ROW_SCALE_MIN), PATTN_ROW_SCALE_MAX);
-    }
-    if (!live || !lane_on) continue;
-    if (kind == 0) {
-      uint16_t* d = p.q_out + t * p.qo_stride + static_cast<int64_t>(row) * p.D;
-      *reinterpret_cast<uint4*>(d + c0 * 8) = pack8<HALF>(x);
-      *reinterpret_cast<uint4*>(d + c1 * 8) = pack8<HALF>(y);
-      continue;
-    }
-    if (blk < 0) continue;
-    const int kv = kind - 1, h = row - p.nq - kv * p.Hkv;
-    const int64_t dst =
-        (((static_cast<int64_t>(kv) * p.NB + blk) * p.bs + off) * p.Hkv + h) * p.D;
-    if constexpr (QUANT) {
-      unsigned char* d = static_cast<unsigned char*>(p.cache) + dst;
-      *reinterpret_cast<uint2*>(d + c0 * 8) = codes8(x, scale);
-      *reinterpret_cast<uint2*>(d + c1 * 8) = codes8(y, scale);
-      if constexpr (KIND == PATTN_KV_FP8_E4M3_ROW)
-        if (j == 0)
-          p.row_scales[((blk * (p.bs / 16) + (off >> 4)) * p.Hkv + h) * 32 + kv * 16 + (off & 15)] =
-              scale;
-    } else {
-      uint16_t* d = static_cast<uint16_t*>(p.cache) + dst;
-      *reinterpret_cast<uint4*>(d + c0 * 8) = pack8<HALF>(x);
-      *reinterpret_cast<uint4*>(d + c1 * 8) = pack8<HALF>(y);
-    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&hd->empty[st]);
   }
+}
+
+template <int LPR, int KIND>
+cudaError_t launch_kind(RopeParams& p, int sms, cudaStream_t st) {
+  const long long steps = p.steps_q + 2LL * p.steps_kv;
+  const long long stage = (2LL * (p.H + 2LL * p.Hkv) * p.D + 4LL * p.axes * p.rot + 127) / 128 * 128;
+  // Many tokens: four or more for each of two CTAs per SM, and at least three
+  // stages of the ring (else one warp per step, every load in flight at once).
+  if (p.T >= 8 * sms && 3 * stage <= RS_RING_BYTES) {
+    p.stage_bytes = static_cast<int>(stage);
+    p.packed = p.H > 0 && p.Hkv > 0 && p.key == p.q + p.H * p.D && p.value == p.key + p.Hkv * p.D &&
+               p.q_stride == p.k_stride && p.q_stride == p.v_stride;
+    p.stages = static_cast<int>(std::min<long long>(RS_STAGES_MAX, RS_RING_BYTES / stage));
+    // the smallest team (one warp, two, ...) that leaves the producer as many
+    // stages as the teams hold
+    p.team = RS_WARPS;
+    while (p.team > 1 && 2 * (2 * RS_WARPS / p.team) <= p.stages) p.team /= 2;
+    const int smem = RS_HEAD + p.stages * p.stage_bytes;
+    auto kern = rope_stream_kernel<LPR, KIND>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<2 * sms, (RS_WARPS + 1) * 32, smem, st>>>(p);
+  } else {
+    const long long ctas = (p.T * steps + RC_THREADS / 32 - 1) / (RC_THREADS / 32);
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    rope_few_kernel<LPR, KIND><<<static_cast<unsigned>(ctas), RC_THREADS, 0, st>>>(p);
+  }
+  return cudaGetLastError();
 }
 
 template <int LPR>
-void launch_lpr(const RopeParams& p, int kv_dtype, unsigned grid, cudaStream_t st) {
+cudaError_t launch_lpr(RopeParams& p, int kv_dtype, int sms, cudaStream_t st) {
+  p.steps_q = (p.H + 32 / LPR - 1) / (32 / LPR);
+  p.steps_kv = (p.Hkv + 32 / LPR - 1) / (32 / LPR);
   switch (kv_dtype) {
-    case PATTN_KV_F16: rope_cache_kernel<LPR, PATTN_KV_F16><<<grid, RC_THREADS, 0, st>>>(p); break;
-    case PATTN_KV_FP8_E4M3:
-      rope_cache_kernel<LPR, PATTN_KV_FP8_E4M3><<<grid, RC_THREADS, 0, st>>>(p);
-      break;
-    case PATTN_KV_FP8_E4M3_ROW:
-      rope_cache_kernel<LPR, PATTN_KV_FP8_E4M3_ROW><<<grid, RC_THREADS, 0, st>>>(p);
-      break;
-    default: rope_cache_kernel<LPR, PATTN_KV_BF16><<<grid, RC_THREADS, 0, st>>>(p); break;
+    case PATTN_KV_F16: return launch_kind<LPR, PATTN_KV_F16>(p, sms, st);
+    case PATTN_KV_FP8_E4M3: return launch_kind<LPR, PATTN_KV_FP8_E4M3>(p, sms, st);
+    case PATTN_KV_FP8_E4M3_ROW: return launch_kind<LPR, PATTN_KV_FP8_E4M3_ROW>(p, sms, st);
+    default: return launch_kind<LPR, PATTN_KV_BF16>(p, sms, st);
   }
 }
 
-// Fills in how the rows are dealt out and launches.  Few tokens: one step per
-// warp (all rows at once, latency); many: up to MAX_ITERS steps per warp, so
-// that the cos and sin loads are shared, once that still leaves WARPS_WANTED.
 pattn_status_t launch(RopeParams& p, int kv_dtype, cudaStream_t st) {
-  constexpr long long WARPS_WANTED = 152 * 32;
-  constexpr int MAX_ITERS = 10;
-  const int lpr = p.D <= 64 ? 4 : p.D <= 128 ? 8 : 16;
-  const int steps = (p.rows + 32 / lpr - 1) / (32 / lpr);
-  const long long all = static_cast<long long>(p.T) * steps;
-  p.iters = static_cast<int>(
-      std::max(1LL, std::min<long long>(std::min(MAX_ITERS, steps), all / WARPS_WANTED)));
-  p.chunks = (steps + p.iters - 1) / p.iters;
-  const long long ctas = (static_cast<long long>(p.T) * p.chunks + RC_THREADS / 32 - 1) /
-                         (RC_THREADS / 32);
-  if (ctas > 0x7fffffffLL) return PATTN_ERR_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>(ctas);
-  if (lpr == 4) launch_lpr<4>(p, kv_dtype, grid, st);
-  else if (lpr == 8) launch_lpr<8>(p, kv_dtype, grid, st);
-  else launch_lpr<16>(p, kv_dtype, grid, st);
-  return cudaGetLastError() == cudaSuccess ? PATTN_OK : PATTN_ERR_CUDA;
+  const int sms = current_sms();
+  const cudaError_t e = p.D <= 64    ? launch_lpr<4>(p, kv_dtype, sms, st)
+                        : p.D <= 128 ? launch_lpr<8>(p, kv_dtype, sms, st)
+                                     : launch_lpr<16>(p, kv_dtype, sms, st);
+  return e == cudaSuccess ? PATTN_OK : PATTN_ERR_CUDA;
 }
 
 bool misaligned(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) != 0; }
@@ -404,12 +660,11 @@ extern "C" pattn_status_t pattn_rope_and_cache(const pattn_rope_t* a) {
   p.H = has_q ? a->num_heads : 0;
   p.Hkv = has_kv ? a->num_kv_heads : 0;
   p.D = D;
+  p.inv_d = 1.f / static_cast<float>(D);
   p.rot = a->num_axes > 0 ? rot : 0;
   p.max_pos = a->max_position;
   p.axes = a->num_axes;
   p.adjacent = a->interleaved;
-  p.nq = p.H;
-  p.rows = p.H + 2 * p.Hkv;
   p.bs = a->block_size;
   p.NB = a->num_blocks;
   return launch(p, a->kv_dtype, static_cast<cudaStream_t>(a->stream));

@@ -121,6 +121,14 @@ def check(c, before, q_out, axis=None, interleaved=False):
     (301, 3, 1, 80, 80, 16, 4, True, False),
     (5, 2, 2, 16, 16, 16, 1, False, True),
     (2050, 16, 2, 128, 64, 128, 1, False, True),
+    # enough tokens for the streaming kernel
+    (1300, 6, 2, 64, 64, 16, 1, True, True),
+    (1250, 32, 8, 128, 128, 64, 3, True, False),
+    (1217, 4, 1, 256, 64, 16, 2, False, True),
+    (1500, 3, 1, 80, 80, 16, 4, True, False),
+    (3001, 7, 7, 96, 48, 32, 1, False, False),
+    (1216, 1, 1, 16, 16, 16, 1, False, False),
+    (1400, 128, 8, 128, 128, 16, 1, False, False),   # three stages do not fit: one warp per step
 ])
 def test_matches_the_definition(kind, T, H, Hkv, D, rot, bs, axes, norm, interleaved):
     c = make(7 * T + D + rot + kind, T, H, Hkv, D, rot, bs, kind=kind, axes=axes, norm=norm)
@@ -249,6 +257,63 @@ def test_rows_are_quantised_bit_for_bit(T, Hkv, D, bs):
     assert (flat[:, rest] == 0).all()
     every = scales.cpu().permute(0, 1, 4, 2, 3).reshape(-1, Hkv, 2)
     assert (every[rest] == -1).all()
+
+
+@pytest.mark.parametrize("T", [40, 1300])
+def test_skipped_tokens_of_every_sort(T):
+    """Padding, bad positions, negative slots and slots past the pool scattered
+    over a batch: the others are as if those were not there."""
+    kind = pa.KV_FP8_E4M3_ROW
+    make_it = lambda: make(600 + T, T, 8, 2, 64, 64, 16, kind=kind, axes=3, max_pos=300, pad=False)
+    c, ok = make_it(), make_it()
+    axis = pa.rope_pair_axis((8, 12, 12))
+    for i in range(0, T, 10):
+        c["pos"][0, i] = -7
+        c["pos"][2, i + 1] = 300
+        c["slots"][i + 2] = -9
+        c["slots"][i + 3] = c["NB"] * 16 + i
+        c["pos"][1, i + 4] = -1
+    ref = call(ok, axis=axis)
+    marked = torch.full((T, 8, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    before, scales = c["cache"].clone(), c["scale"].clone()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = call(c, axis=axis, q_out=marked, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 1
+    i = torch.arange(T) % 10
+    gone, kv_gone = (i == 0) | (i == 1) | (i == 4), (i < 5)
+    assert (out[gone.to(DEV)] == 7.0).all() and torch.equal(out[~gone.to(DEV)], ref[~gone.to(DEV)])
+    flat = lambda x: x.reshape(2, -1, 2, 64)
+    flat_s = lambda x: x.permute(0, 1, 4, 2, 3).reshape(-1, 2, 2)
+    at = ok["slots"].to(DEV)
+    live, dead = at[~kv_gone.to(DEV)], at[kv_gone.to(DEV)]
+    assert torch.equal(flat(c["cache"])[:, live], flat(ok["cache"])[:, live])
+    assert torch.equal(flat_s(c["scale"])[live], flat_s(ok["scale"])[live])
+    assert torch.equal(flat(c["cache"])[:, dead], flat(before)[:, dead])
+    assert torch.equal(flat_s(c["scale"])[dead], flat_s(scales)[dead])
+
+
+def test_many_tokens_in_place_alone_and_without_rotation():
+    kind = pa.KV_FP8_E4M3_ROW
+    c, d, e = (make(620, 1999, 8, 2, 128, 128, 16, kind=kind) for _ in range(3))
+    ref = call(c)
+    rest = (d["slots"].to(DEV), d["pos"].to(DEV), d["table"].to(DEV))
+    q, k, v = parts(d)
+    kw = dict(block_size=16, kv_dtype=kind)
+    pa.rope_and_cache(None, k, v, d["cache"], *rest, kv_scale=d["scale"], **kw)
+    pa.rope_and_cache(q, None, None, None, None, *rest[1:], q_out=q, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(q, ref)
+    assert torch.equal(c["cache"], d["cache"]) and torch.equal(c["scale"], d["scale"])
+    q, k, v = parts(e)
+    pa.reshape_and_cache(k.contiguous(), v.contiguous(), e["cache"], rest[0], block_size=16,
+                         kv_dtype=kind, kv_scale=e["scale"])
+    torch.cuda.synchronize()
+    codes, s = R.row_codes_fp32(torch.stack([k, v]))
+    live = e["slots"] >= 0
+    at = e["slots"][live]
+    assert torch.equal(e["cache"].cpu().reshape(2, -1, 2, 128)[:, at], codes[:, live])
+    assert torch.equal(R.scales_at(e["scale"], at).permute(2, 0, 1), s[:, live].double())
 
 
 def test_the_tensor_scaled_write_without_rotation_is_the_plain_write():
