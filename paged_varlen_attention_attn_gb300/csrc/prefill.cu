@@ -116,8 +116,9 @@ __host__ __device__ constexpr int v_rows() { return FP8 ? BLOCK_N : 16; }
 // that tile's entry is done.
 struct ScaleTile {
   float ks[BLOCK_N];     // K scales
-  unsigned vs[BLOCK_N];  // V scales times 2^(7 - er) as f16 pairs; the fp32 bits of
-                         // the V scales themselves if er is WILD_TILE
+  unsigned vh[BLOCK_N];  // V scales times 2^(7 - er), each as an f16 pair (1 if er is
+                         // WILD_TILE)
+  float vs[BLOCK_N];     // V scales as they are, written only if er is WILD_TILE
 };
 constexpr int SC_STAGES = 4;
 constexpr int SC_TILE = sizeof(ScaleTile);
@@ -129,7 +130,7 @@ constexpr int WILD_TILE = 1 << 20;
 // tile's reference more often (at 2^8 most tiles of keys with log-normal row
 // norms, sigma 0.4, did in some row of a warp), and f16 weights have room up to
 // 2^15.  A prompt batch took 0.57 instead of 0.90 ms.
-constexpr float ROWS_SUM_LIMIT = 16384.0f;
+constexpr float ROWS_SUM_LIMIT = 65000.0f;
 
 // NK: e4m3 K codes used as they are (an e4m3 cache at d 128).
 template <int D, bool NK = false, bool ROWS = false>
@@ -223,13 +224,11 @@ __device__ __forceinline__ void ffma2(float& a0, float& a1, float b, float c) {
 // where f16 row r overlaps source row r alone, warps may widen disjoint row
 // ranges of one tile at the same time.
 //
-// ROWS: row r is also multiplied by vs[r], an f16 pair (`wild`: it is not); scale
-// and product are each rounded to f16 (2^-11).  Rows below lo become zero (rows
-// at or past seq_len are zeroed by the softmax warps).
+// ROWS: row r is also multiplied by vh[r], an f16 pair; scale and product are
+// each rounded to f16 (2^-11).
 template <int D, bool ROWS = false>
 __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int row0, int row1,
-                                                    int lane, const unsigned* vs = nullptr,
-                                                    bool wild = false, int lo = 0) {
+                                                    int lane, const unsigned* vh = nullptr) {
   constexpr int RPP = 512 / D;
   constexpr int U = (D == 128) ? 4 : 2;
   constexpr int HALF = BLOCK_M * 128;  // bytes of one d half of a tile
@@ -250,18 +249,14 @@ __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int ro
     uint4 w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) w[u] = *reinterpret_cast<const uint4*>(src0 + (ps + u) * RPP * D);
+    unsigned f[U];
+    if constexpr (ROWS) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) f[u] = vh[(ps + u) * RPP + r0];
+    }
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      unsigned f = 0x3C003C00u;  // 1, 1
-      if constexpr (ROWS) {
-        const int r = (ps + u) * RPP + r0;
-        if (!wild) f = vs[r];
-        if (r < lo) {
-          f = 0u;
-          w[u] = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
       const unsigned v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
       unsigned h[8];
 #pragma unroll
@@ -273,7 +268,7 @@ __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int ro
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[e]),
-                                    *reinterpret_cast<const __half2*>(&f));
+                                    *reinterpret_cast<const __half2*>(&f[u]));
           h[e] = *reinterpret_cast<const unsigned*>(&y);
         }
       }
@@ -289,6 +284,16 @@ __device__ __forceinline__ void widen_e4m3_in_place(unsigned char* stage, int ro
 }
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// Zeroes rows [row0, row1) of an f16 tile.  Not inlined: a tile at the edge of a
+// window calls it, and the warps that widen every tile have no registers to
+// spare for it.
+template <int DH>
+__device__ __noinline__ void zero_rows(unsigned char* stage, int row0, int row1, int lane) {
+  for (int i = row0 * 8 + lane; i < row1 * 8; i += 32)
+    for (int dh = 0; dh < DH; ++dh)
+      *reinterpret_cast<uint4*>(stage + dh * BLOCK_M * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
 
 // Converts a Q tile (bf16, as TMA loaded it: DH 128-byte-swizzled d halves)
 // to f16 in place for the f16 MMAs of an e4m3 call at d 64, once its copy has
@@ -806,11 +811,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         const float mul = pow2i(7 - er);
         ScaleTile* t = sc_of(jt);
         *reinterpret_cast<float4*>(&t->ks[lane * 4]) = k4;
-        uint4 h = make_uint4(v[0], v[1], v[2], v[3]);
-        if (!wild)
+        uint4 h = make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);
+        if (wild)
+          *reinterpret_cast<float4*>(&t->vs[lane * 4]) = v4;
+        else
           h = make_uint4(pack2<true>(v4.x * mul, v4.x * mul), pack2<true>(v4.y * mul, v4.y * mul),
                          pack2<true>(v4.z * mul, v4.z * mul), pack2<true>(v4.w * mul, v4.w * mul));
-        *reinterpret_cast<uint4*>(&t->vs[lane * 4]) = h;
+        *reinterpret_cast<uint4*>(&t->vh[lane * 4]) = h;
         if (lane == 0) bars->sc_er[jt % SC_STAGES] = wild ? WILD_TILE : er;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->sc_full[jt % SC_STAGES]);
@@ -822,10 +829,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           if (!__all_sync(FULL, mbar_wait(&bars->sc_full[jt % SC_STAGES], (jt / SC_STAGES) & 1,
                                           status, abort_flag)))
             return 0;
-          widen_e4m3_in_place<D, true>(
-              stage, row0, row1, lane, sc_of(jt)->vs,
-              *static_cast<volatile int*>(&bars->sc_er[jt % SC_STAGES]) == WILD_TILE,
-              klo - key_base);
+          widen_e4m3_in_place<D, true>(stage, row0, row1, lane, sc_of(jt)->vh);
+          // rows below the window may hold anything: they become zero
+          if (klo > key_base) zero_rows<C::DH>(stage, row0, min(row1, klo - key_base), lane);
         } else {
           widen_e4m3_in_place<D>(stage, row0, row1, lane);
         }
@@ -1397,15 +1403,16 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         auto rescale_o = [&](bool need_o, float alpha) {
           if (__any_sync(FULL, need_o)) {
             const float a = need_o ? alpha : 1.f;
+            float ov[D];  // one TMEM round trip: the score registers are free by now
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              float ov[32];
-              tc_ld32(o_t + q * 32, ov);
-              tc_wait_ld();
+            for (int q = 0; q < D / 32; ++q)
+              tc_ld32(o_t + q * 32, *reinterpret_cast<float(*)[32]>(&ov[q * 32]));
+            tc_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) ov[e] *= a;
-              tc_st32(o_t + q * 32, ov);
-            }
+            for (int e = 0; e < D; ++e) ov[e] *= a;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q)
+              tc_st32(o_t + q * 32, *reinterpret_cast<const float(*)[32]>(&ov[q * 32]));
           }
         };
         float ps = 0.f;
@@ -1423,10 +1430,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           }
           unsigned pk[BLOCK_N / 2];
 #pragma unroll
-          for (int g = 0; g < BLOCK_N / 32; ++g)
+          for (int g = 0; g < BLOCK_N / 32; ++g) {
             ps += exp_piece<MMA_F16>(*reinterpret_cast<const float(*)[32]>(&sv[g * 32]), sl2r,
                                      ROWS ? m_run - static_cast<float>(er) : m_run,
                                      *reinterpret_cast<unsigned(*)[16]>(&pk[g * 16]));
+          }
           slow = !(ps <= (ROWS ? ROWS_SUM_LIMIT : FAST_SUM_LIMIT));
           if (!__any_sync(FULL, slow)) {
 #pragma unroll
@@ -1499,7 +1507,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const int q = g * 32 + e;
-                const float lv = __log2f(__uint_as_float(sc->vs[q])) + 7.f;
+                const float lv = __log2f(sc->vs[q]) + 7.f;
                 y[e] = (q < lim_hi && q >= lim_lo) ? y[e] * sl2r + lv : -INFINITY;
               }
             };
@@ -1529,7 +1537,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 y[e] = fast_exp2(y[e] - ref);
-                ps += y[e] > 0.f ? __fdividef(y[e], __uint_as_float(sc->vs[g * 32 + e])) : 0.f;
+                ps += y[e] > 0.f ? __fdividef(y[e], sc->vs[g * 32 + e]) : 0.f;
               }
 #pragma unroll
               for (int e = 0; e < 16; ++e) pk[e] = pack2<MMA_F16>(y[2 * e], y[2 * e + 1]);
