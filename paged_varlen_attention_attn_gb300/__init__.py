@@ -187,18 +187,30 @@ def reshape_and_cache(key, value, kv_cache, slot_mapping, *, block_size, kv_dtyp
     ``kv_scale`` is the cache's row-scale tensor, updated as well
     (pattn_reshape_and_cache_rows).  Raises PattnError."""
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(key.device)
     if kv_dtype == KV_FP8_E4M3_ROW:
         _check_row_scales(kv_scale, kv_cache.shape[1], block_size, key.shape[1], kv_cache.device)
-        st = load().pattn_reshape_and_cache_rows(
-            key.data_ptr(), value.data_ptr(), kv_cache.data_ptr(), kv_scale.data_ptr(),
-            slot_mapping.data_ptr(), key.shape[0], key.shape[1], key.shape[2], int(block_size),
-            kv_cache.shape[1], None if device_status is None else device_status.data_ptr(),
-            stream.cuda_stream)
+        T, Hkv, D = key.shape
+        dev, NB = key.device, kv_cache.shape[1]
+        for name, x, shape, types in (
+                ("key", key, (T, Hkv, D), (torch.bfloat16,)),
+                ("value", value, (T, Hkv, D), (torch.bfloat16,)),
+                ("kv_cache", kv_cache, (2, NB, block_size, Hkv, D),
+                 (torch.uint8, torch.float8_e4m3fn)),
+                ("slot_mapping", slot_mapping, (T,), (torch.int64,))):
+            if x.shape != shape or x.dtype not in types or x.device != dev or not x.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {types[0]} tensor of shape {shape}")
+        if T == 0:  # (an empty tensor has no address)
+            return kv_cache
+        st = _call_on(
+            dev, load().pattn_reshape_and_cache_rows, key.data_ptr(), value.data_ptr(),
+            kv_cache.data_ptr(), kv_scale.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D,
+            int(block_size), NB, None if device_status is None else device_status.data_ptr(),
+            _raw_stream(stream, dev))
         if st != 0:
             raise PattnError(st, "pattn_reshape_and_cache_rows")
         return kv_cache
+    if stream is None:
+        stream = torch.cuda.current_stream(key.device)
     st = pattn_reshape_and_cache(key.data_ptr(), value.data_ptr(), kv_cache.data_ptr(),
                                  slot_mapping.data_ptr(), key.shape[0], key.shape[1],
                                  key.shape[2], block_size, kv_cache.shape[1], kv_dtype, kv_scale,
@@ -251,6 +263,16 @@ def _raw_stream(stream, dev):
         return stream.cuda_stream
     from torch._C import _cuda_getCurrentRawStream
     return _cuda_getCurrentRawStream(dev.index)
+
+
+def _call_on(dev, fn, *args):
+    """fn(*args) with ``dev`` the current device, as the library's launches need."""
+    from torch._C import _cuda_getDevice
+    if dev.index == _cuda_getDevice():
+        return fn(*args)
+    import torch
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _rows_of(x, name, dtype, dev):
@@ -358,7 +380,7 @@ def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *,
         axes_at, norms[0], norms[1], cache_at, rows_at, scale_at, slots_at,
         0 if device_status is None else device_status.data_ptr(), _raw_stream(stream, dev),
         norm_eps, T, H, Hkv, D, rot, interleaved, axes, max_pos, kv_dtype, block_size, NB)
-    st = load().pattn_rope_and_cache(args)
+    st = _call_on(dev, load().pattn_rope_and_cache, args)
     if st != 0:
         raise PattnError(st, "pattn_rope_and_cache")
     return q_out
@@ -410,8 +432,8 @@ def gather_cache(kv_cache, block_table, out_start_loc, *, num_rows, block_size, 
     key_out, value_out = outs
     if num_rows == 0 or B == 0:  # (an empty tensor has no address)
         return key_out, value_out
-    st = load().pattn_gather_cache(
-        kv_cache.data_ptr(), block_table.data_ptr(), starts_at or None, out_start_loc.data_ptr(),
+    st = _call_on(
+        dev, load().pattn_gather_cache, kv_cache.data_ptr(), block_table.data_ptr(), starts_at or None, out_start_loc.data_ptr(),
         key_out.data_ptr(), value_out.data_ptr(), B, int(num_rows), mbps, NB, Hkv, D,
         int(block_size), int(kv_dtype),
         _scale_arg(kv_dtype, kv_scale), None if device_status is None else device_status.data_ptr(),
@@ -457,7 +479,7 @@ def cascade_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scal
                                          common_prefix_len)
     if need == 0:
         raise PattnError(1, "pattn_cascade_workspace_bytes")
-    ws = (workspace or _default_ws).get(need, dev)
+    ws = _workspace(workspace, dev, stream.cuda_stream).get(need, dev)
     ext.workspace = ws.data_ptr()
     ext.workspace_bytes = ws.numel()
     ks = _scale_arg(kv_dtype, kv_scale)
@@ -562,7 +584,19 @@ class Workspace:
         return self.buf
 
 
-_default_ws = Workspace()
+_default_ws = {}  # (device index, cudaStream_t) -> Workspace
+
+
+def _workspace(workspace, dev, raw_stream):
+    """The caller's Workspace, or the stream's own: calls on one stream run one
+    after the other and may share scratch, calls on two streams may not.  (Two
+    captured graphs that may run at once need a Workspace each.)"""
+    if workspace is not None:
+        return workspace
+    key = (dev.index, raw_stream)
+    if key not in _default_ws:
+        _default_ws[key] = Workspace()
+    return _default_ws[key]
 
 
 def _sinks_ptr(sinks, num_heads, device):
@@ -586,7 +620,8 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
     max_query_len / max_seq_len are host ints (as in FlashAttentionMetadata):
     the library never reads device memory on the host.  ``kv_scale``: (k_scale,
     v_scale) of an e4m3 cache, or the row-scale tensor of a KV_FP8_E4M3_ROW cache
-    (see ``row_scales_shape``).  ``timing_events``:
+    (see ``row_scales_shape``).  ``workspace``: a Workspace (default: one per
+    stream; two graphs that may run at once need one each).  ``timing_events``:
     optional 8 raw cudaEvent_t handles (see pattn_ext_t).  ``sinks``: optional
     fp32 [num_heads] device tensor of attention-sink logits.  ``head_size_v``:
     > 0 selects the DiffKV cache layout [num_blocks, block_size, num_kv_heads,
@@ -608,7 +643,7 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
     events = None
     if timing_events is not None:
         events = (ctypes.c_void_p * 8)(*[int(x) for x in timing_events])
-    ws = workspace or _default_ws
+    ws = _workspace(workspace, dev, raw_stream)
     buf = ws.current(dev)
     ext = Ext.from_buffer_copy(_EXT_PACK.pack(
         _EXT_PACK.size, seq_lens.shape[0], T, mbps, num_blocks, max_query_len, max_seq_len,
@@ -622,7 +657,7 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
             int(num_kv_heads), int(head_size), int(block_size), int(window), int(causal),
             int(kv_dtype), _scale_arg(kv_dtype, kv_scale), ext)
     # the library itself says when the workspace is missing or too small
-    st = 3 if buf is None else run(*args)
+    st = 3 if buf is None else _call_on(dev, run, *args)
     if st != 0:
         need = pattn_workspace_bytes(ext, num_heads, num_kv_heads, head_size, block_size, lib=lib)
         if need == 0:
@@ -630,7 +665,7 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
         if st == 3:
             buf = ws.get(need, dev)
             ext.workspace, ext.workspace_bytes = buf.data_ptr(), buf.numel()
-            st = run(*args)
+            st = _call_on(dev, run, *args)
     if check and st != 0:
         raise PattnError(st, "pattn_varlen_fwd")
     forward.last_ext = ext

@@ -191,3 +191,41 @@ def test_the_binding_refuses_gather_tensors_that_do_not_fit():
                dict(key_out=torch.zeros(3, 2, 64, dtype=torch.bfloat16))):
         with pytest.raises(ValueError):
             pa.gather_cache(**{**ok, **kw})
+
+
+def test_the_binding_refuses_rows_that_do_not_fit():
+    bf = torch.bfloat16
+    ok = dict(key=torch.zeros(3, 2, 64, dtype=bf), value=torch.zeros(3, 2, 64, dtype=bf),
+              kv_cache=torch.zeros(2, 2, 16, 2, 64, dtype=torch.uint8),
+              slot_mapping=torch.zeros(3, dtype=torch.int64), block_size=16,
+              kv_dtype=pa.KV_FP8_E4M3_ROW, kv_scale=torch.zeros(pa.row_scales_shape(2, 16, 2)))
+    for kw in (dict(key=torch.zeros(3, 4, 64, dtype=bf)[:, ::2]), dict(value=torch.zeros(3, 2, 64)),
+               dict(value=torch.zeros(2, 2, 64, dtype=bf)), dict(slot_mapping=torch.zeros(3, dtype=torch.int32)),
+               dict(kv_cache=torch.zeros(2, 2, 16, 2, 64, dtype=bf)), dict(kv_scale=(1.0, 1.0)),
+               dict(kv_scale=torch.zeros(2, 2, 16, 2, 2).transpose(0, 1))):
+        with pytest.raises(ValueError):
+            pa.reshape_and_cache(**{**ok, **kw})
+
+
+def test_attention_refuses_row_scales_that_do_not_fit():
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    args = (q, torch.zeros(2, 2, 16, 2, 64, dtype=torch.uint8), torch.zeros(1, 1, dtype=torch.int32),
+            torch.ones(1, dtype=torch.int32), torch.tensor([0, 1], dtype=torch.int32))
+    kw = dict(scale=1.0, num_heads=4, num_kv_heads=2, head_size=64, block_size=16,
+              kv_dtype=pa.KV_FP8_E4M3_ROW, max_query_len=1, max_seq_len=16)
+    for scales in (None, (1.0, 1.0), torch.zeros(2, 1, 2, 2, 8), torch.zeros(pa.row_scales_shape(2, 16, 2)).double()):
+        with pytest.raises(ValueError):
+            pa.forward(*args, kv_scale=scales, **kw)
+        with pytest.raises(ValueError):
+            pa.cascade_forward(*args, kv_scale=scales, common_prefix_len=16, **kw)
+
+
+@pytest.mark.parametrize("kw,status", [(dict(ks=None), 1), (dict(ks=FAKE + 4), 1), (dict(ks=FAKE, hv=64), 2)])
+def test_row_scaled_attention_arguments_are_checked_on_the_host(lib, kw, status):
+    ext = pa.make_ext(num_seqs=2, num_tokens=9, max_blocks_per_seq=3, num_blocks=8, max_query_len=8,
+                      max_seq_len=40, workspace=FAKE, workspace_bytes=1 << 30, head_size_v=kw.get("hv", 0))
+    assert pa.pattn_varlen_fwd(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0.1, 4, 2, 64, 16, 0, 1,
+                               pa.KV_FP8_E4M3_ROW, kw["ks"], ext, lib=lib) == status
+    if "hv" not in kw:
+        assert pa.pattn_decode_fwd_static(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0.1, 4, 2, 64, 16, 0, 1,
+                                          pa.KV_FP8_E4M3_ROW, kw["ks"], 2, 2, 3, 8, 40, 0, 0, lib=lib) == status

@@ -356,3 +356,48 @@ def test_a_cache_past_32_bit_offsets():
         assert torch.equal(cache[0, at // bs, at % bs].cpu(), codes[i])
         assert torch.equal(cache[1, at // bs, at % bs].cpu(), codes[i])
         assert torch.equal(scales[at // bs, at % bs // 16, :, 1, at % 16].cpu(), s[i])
+
+
+def test_decode_over_blocks_that_are_no_power_of_two():
+    c = Case(230, [(1, 5), (1, 48), (1, 49), (1, 700)], 8, 2, 128, 48)
+    c.check(c.run())
+    c.check(c.run(window=60), window=60)
+
+
+def test_calls_on_two_streams_at_once_do_not_share_scratch():
+    """Default workspaces: two streams' calls, each with partitions, interleaved."""
+    a = Case(240, [(1, 3000), (1, 2500)], 8, 2, 128, 16)
+    b = Case(241, [(1, 2800), (40, 300), (1, 900)], 8, 2, 128, 16)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    prepared = [(c.args(), c.kw(num_splits=8)) for c in (a, b)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(pa.forward(*prepared[i][0], **prepared[i][1]))
+    torch.cuda.synchronize()
+    for c, got in zip((a, b), outs):
+        c.check(got[0])
+        assert all(torch.equal(x, got[0]) for x in got)
+
+
+def test_repeated_calls_give_the_same_bits():
+    c = Case(250, BATCHES["mixed"] + [(1, 4000)], 8, 2, 128, 16)
+    prepared, kw = c.args(), c.kw(num_splits=6)
+    first = pa.forward(*prepared, **kw)
+    for _ in range(5):
+        assert torch.equal(pa.forward(*prepared, **kw), first)
+
+
+def test_rows_outside_the_batch_stay():
+    """A padded batch: q and out have rows before and behind the requests'."""
+    c = Case(260, BATCHES["mixed"], 8, 2, 128, 16)
+    q, cache, bt, sl, qsl = c.args()
+    wide = torch.full((c.T + 9, 8, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide[4:4 + c.T] = q
+    out = torch.full_like(wide, 7.0)
+    pa.forward(wide, cache, bt, sl, qsl + 4, out=out, **c.kw())
+    torch.cuda.synchronize()
+    c.check(out[4:4 + c.T])
+    assert (out[:4] == 7.0).all() and (out[4 + c.T:] == 7.0).all()
