@@ -127,9 +127,10 @@ constexpr int SC_TILE = sizeof(ScaleTile);
 constexpr int WILD_OCTAVES = 14;
 constexpr int WILD_TILE = 1 << 20;
 // As FAST_SUM_LIMIT, with row scales: rows of uneven size outgrow the first
-// tile's reference more often (at 2^8 most tiles of keys with log-normal row
-// norms, sigma 0.4, did in some row of a warp), and f16 weights have room up to
-// 2^15.  A prompt batch took 0.57 instead of 0.90 ms.
+// tile's reference more often, and one such row of a warp holds up both
+// sub-tiles, so the reference moves only where f16 weights (up to 65504) would
+// not hold.  Keys with log-normal row norms (sigma 0.4), 8 prompts of 512 to
+// 4096 tokens: 0.90 ms at 2^8, 0.57 at 2^14, and then 1 % less at this limit.
 constexpr float ROWS_SUM_LIMIT = 65000.0f;
 
 // NK: e4m3 K codes used as they are (an e4m3 cache at d 128).
@@ -536,16 +537,21 @@ __device__ __forceinline__ int union_tiles(const Sub& a, const Sub& b, int& u0) 
 // ROWS: the e4m3 cache has a scale per key row of K (ks) and of V (vs).  A score
 // column is multiplied by its ks in the softmax; vs goes into the widened V
 // tile, up to the power of two 2^(7 - er) of the tile (the largest vs is in
-// [2^(er - 1), 2^er)).  The
-// running reference m is taken over x + er, so P = 2^(x + er - m) keeps f16's
-// range whatever the scales are, O is relative to m with the constant factor
-// 2^7 that out_scale takes back, and the sum of a tile's P counts 2^-er times
-// in the normaliser.  Where the V scales of a tile's rows are further apart
-// than f16 allows (WILD_TILE), the tile holds the codes alone and the weights
-// take the scales instead, P = 2^(x + log2 vs + 7 - m) with each P counting
-// 2^-7 / vs times in the normaliser: exact for any scales, and slow (the path
-// that takes the row max, two more MUFU operations a weight), which only data
-// far from a model's reaches.
+// [2^(er - 1), 2^er)).  The running reference m is taken over x + er, so
+// P = 2^(x + er - m) keeps f16's range whatever the scales are, O is relative
+// to m with the constant factor 2^7 that out_scale takes back, and the sum of a
+// tile's P counts 2^-er times in the normaliser.  Where the V scales of a
+// tile's rows are further apart than f16 allows (WILD_TILE), the tile holds
+// the codes alone and the weights take the scales instead,
+// P = 2^(x + log2 vs + 7 - m) with each P counting 2^-7 / vs times in the
+// normaliser: exact for any scales, and slow, which only data far from a
+// model's reaches.
+// Against the tensor-scaled instance the softmax has 64 paired products and 32
+// shared loads more per row and tile, the widening one f16 product per two
+// codes: 8 prompts of 512 to 4096 tokens, 32 / 8 heads of 128, 472 us (590
+// TFLOP/s) against 356.  Measured and dropped: V scales applied to the packed
+// weights instead (594 us, and less exact), K and V both scaled while they are
+// widened to f16 (685 us).
 //
 // Persistent: the grid holds at most one CTA per SM; its items come from the
 // LPT-ordered list, in a fixed order for the first rounds and claimed as
@@ -856,7 +862,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         // between copies this warp widens rows [V_SPLIT, BLOCK_N) of each V
         // tile (warp 10 rows [0, V_SPLIT)).  The copy of tile j + PF_KST - 1
         // waits for the scores of tile j - 1, whose MMAs need only V tiles
-        // before j - 1, so the two jobs never wait on each other.
+        // before j - 1, so the two jobs never wait on each other.  V tile j comes
+        // first, being needed a tile sooner (4 chunks of 2048 with a window of
+        // 4096: 1.30 -> 1.27 ms tensor-scaled, 1.73 -> 1.68 row-scaled).
         int blk_next = page_block(u0);
         int n_issued = 0;
         auto issue_k = [&]() {
