@@ -256,19 +256,30 @@ def rope_pair_axis(sections, interleaved=False):
     return out
 
 
+_torch_c = None
+
+
+def _torch():
+    """torch's C module (bound once: torch is imported by the first call that needs
+    it, and an import statement per call costs as much as a check or two)."""
+    global _torch_c
+    if _torch_c is None:
+        from torch import _C
+        _torch_c = _C
+    return _torch_c
+
+
 def _raw_stream(stream, dev):
     """The cudaStream_t of ``stream``, or of the device's current stream (read
     without building a Stream object: 2 us less per call)."""
     if stream is not None:
         return stream.cuda_stream
-    from torch._C import _cuda_getCurrentRawStream
-    return _cuda_getCurrentRawStream(dev.index)
+    return (_torch_c or _torch())._cuda_getCurrentRawStream(dev.index)
 
 
 def _call_on(dev, fn, *args):
     """fn(*args) with ``dev`` the current device, as the library's launches need."""
-    from torch._C import _cuda_getDevice
-    if dev.index == _cuda_getDevice():
+    if dev.index == (_torch_c or _torch())._cuda_getDevice():
         return fn(*args)
     import torch
     with torch.cuda.device(dev):
@@ -283,9 +294,15 @@ def _rows_of(x, name, dtype, dev):
         raise ValueError(f"{name} must be a {dtype} tensor [num_tokens, heads, head_size] on one device")
     T, H, D = shape
     st, sh, sd = x.stride()
-    if (sd != 1 and D > 1) or (sh != D and H > 1):
+    if (sh != D and H > 1) or (sd != 1 and D > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
     return x.data_ptr(), st if T > 1 else H * D, shape
+
+
+def _norm_at(w, name, dtype, dev, D):
+    if w.dtype != dtype or w.shape != (D,) or w.device != dev or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} [head_size] tensor")
+    return w.data_ptr()
 
 
 def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *, block_size,
@@ -367,17 +384,13 @@ def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *,
                 raise ValueError("positions of several axes need pair_axis with rot_dim / 2 entries")
             pairs = ctypes.c_char_p(bytes(pair_axis))
             axes_at = ctypes.cast(pairs, ctypes.c_void_p).value
-    norms = [0, 0]
-    for i, (name, w) in enumerate((("q_norm", q_norm), ("k_norm", k_norm))):
-        if w is not None:
-            if w.dtype != dt or w.shape != (D,) or w.device != dev or not w.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {dt} [head_size] tensor")
-            norms[i] = w.data_ptr()
+    qn_at = 0 if q_norm is None else _norm_at(q_norm, "q_norm", dt, dev, D)
+    kn_at = 0 if k_norm is None else _norm_at(k_norm, "k_norm", dt, dev, D)
     if T == 0:  # (an empty tensor has no address)
         return q_out
     args = _ROPE_PACK.pack(
         _ROPE_PACK.size, q_at, qo_at, k_at, v_at, q_st, qo_st, k_st, v_st, table_at, pos_at, pos_st,
-        axes_at, norms[0], norms[1], cache_at, rows_at, scale_at, slots_at,
+        axes_at, qn_at, kn_at, cache_at, rows_at, scale_at, slots_at,
         0 if device_status is None else device_status.data_ptr(), _raw_stream(stream, dev),
         norm_eps, T, H, Hkv, D, rot, interleaved, axes, max_pos, kv_dtype, block_size, NB)
     st = _call_on(dev, load().pattn_rope_and_cache, args)
