@@ -298,6 +298,7 @@ __device__ __forceinline__ void serve_row(const RopeParams& p, const LanePlace& 
 
 // ------------------------------------------------------------- few tokens
 // One warp per step (latency: every load of the call is in flight at once).
+// 1 token of 32 + 2 x 8 heads of 128: 2.6 us, an empty launch's time.
 template <int LPR, int KIND>
 __global__ void __launch_bounds__(RC_THREADS)
     rope_few_kernel(const __grid_constant__ RopeParams p) {
@@ -365,10 +366,16 @@ __global__ void __launch_bounds__(RC_THREADS)
 // registers hold.  Eight consumer warps work in teams of one to eight, a team
 // per token: the smaller, the more rows share a warp's cos, sin and norm
 // weights, the larger, the fewer stages the teams hold.
+// 8384 tokens, 64 q and 8 k and v heads of 128, row-scaled e4m3 cache: 56 us,
+// 87 % of the measured copy bandwidth (teams of 8 / 4 / 2 warps 62 / 56.5 / 56).
+// 5003 tokens, 32 and 4 heads, norm, three axes: 24.7 us (30.6 / 26.4 / 24.6).
+// A second producer warp: 60 and 23.8.
 constexpr int RS_WARPS = 8;  // consumer warps
 constexpr int RS_STAGES_MAX = 8;
 constexpr int RS_RING_BYTES = 100 * 1024;  // two CTAs per SM
 constexpr int RS_HEAD = 256;               // barriers and the stages' tokens
+constexpr long long RS_LEAST_STAGE = 4096;        // bytes of a token that streaming pays for
+constexpr long long RS_LEAST_CALL = 28ll << 20;   // and of a call
 
 struct StreamHead {
   uint64_t full[RS_STAGES_MAX], empty[RS_STAGES_MAX];
@@ -526,9 +533,13 @@ template <int LPR, int KIND>
 cudaError_t launch_kind(RopeParams& p, int sms, cudaStream_t st) {
   const long long steps = p.steps_q + 2LL * p.steps_kv;
   const long long stage = (2LL * (p.H + 2LL * p.Hkv) * p.D + 4LL * p.axes * p.rot + 127) / 128 * 128;
-  // Many tokens: four or more for each of two CTAs per SM, and at least three
-  // stages of the ring (else one warp per step, every load in flight at once).
-  if (p.T >= 8 * sms && 3 * stage <= RS_RING_BYTES) {
+  // Stream long calls of tokens with long rows (in us, one warp per step against
+  // streamed): 64 + 2 x 8 heads of 128, 608 tokens 7.2 / 6.7, 1216 14.4 / 13.9,
+  // 8384 77 / 56; 32 + 2 x 8, 1824 tokens 13.2 / 14.5, 2432 17.1 / 16.7, 4864
+  // 30.0 / 26.1; 16 + 2 x 2 of 128, 3000 tokens 11.0 / 11.7, 6000 21.0 / 19.3;
+  // of 64, 3000 tokens 8.0 / 9.8, 24000 53 / 58 (a copy's cost shows).  And the
+  // ring has to hold three tokens.
+  if (stage >= RS_LEAST_STAGE && p.T * stage >= RS_LEAST_CALL && 3 * stage <= RS_RING_BYTES) {
     p.stage_bytes = static_cast<int>(stage);
     p.packed = p.H > 0 && p.Hkv > 0 && p.key == p.q + p.H * p.D && p.value == p.key + p.Hkv * p.D &&
                p.q_stride == p.k_stride && p.q_stride == p.v_stride;

@@ -121,14 +121,17 @@ def check(c, before, q_out, axis=None, interleaved=False):
     (301, 3, 1, 80, 80, 16, 4, True, False),
     (5, 2, 2, 16, 16, 16, 1, False, True),
     (2050, 16, 2, 128, 64, 128, 1, False, True),
-    # enough tokens for the streaming kernel
+    # many tokens, short rows
     (1300, 6, 2, 64, 64, 16, 1, True, True),
-    (1250, 32, 8, 128, 128, 64, 3, True, False),
-    (1217, 4, 1, 256, 64, 16, 2, False, True),
-    (1500, 3, 1, 80, 80, 16, 4, True, False),
     (3001, 7, 7, 96, 48, 32, 1, False, False),
-    (1216, 1, 1, 16, 16, 16, 1, False, False),
-    (1400, 128, 8, 128, 128, 16, 1, False, False),   # three stages do not fit: one warp per step
+    # long calls of long rows: the streaming kernel
+    (2400, 32, 8, 128, 128, 64, 3, True, False),
+    (3333, 64, 4, 64, 64, 16, 1, True, True),
+    (2500, 16, 4, 256, 64, 16, 2, False, True),
+    (3100, 48, 8, 80, 80, 16, 4, True, False),
+    (4001, 31, 3, 96, 48, 32, 1, False, False),
+    (1500, 64, 8, 128, 64, 16, 1, False, False),
+    (1000, 128, 8, 128, 128, 16, 1, False, False),   # three stages do not fit: one warp per step
 ])
 def test_matches_the_definition(kind, T, H, Hkv, D, rot, bs, axes, norm, interleaved):
     c = make(7 * T + D + rot + kind, T, H, Hkv, D, rot, bs, kind=kind, axes=axes, norm=norm)
@@ -259,12 +262,12 @@ def test_rows_are_quantised_bit_for_bit(T, Hkv, D, bs):
     assert (every[rest] == -1).all()
 
 
-@pytest.mark.parametrize("T", [40, 1300])
-def test_skipped_tokens_of_every_sort(T):
+@pytest.mark.parametrize("T,H", [(40, 8), (1300, 8), (3400, 64)])
+def test_skipped_tokens_of_every_sort(T, H):
     """Padding, bad positions, negative slots and slots past the pool scattered
     over a batch: the others are as if those were not there."""
     kind = pa.KV_FP8_E4M3_ROW
-    make_it = lambda: make(600 + T, T, 8, 2, 64, 64, 16, kind=kind, axes=3, max_pos=300, pad=False)
+    make_it = lambda: make(600 + T, T, H, 2, 64, 64, 16, kind=kind, axes=3, max_pos=300, pad=False)
     c, ok = make_it(), make_it()
     axis = pa.rope_pair_axis((8, 12, 12))
     for i in range(0, T, 10):
@@ -274,7 +277,7 @@ def test_skipped_tokens_of_every_sort(T):
         c["slots"][i + 3] = c["NB"] * 16 + i
         c["pos"][1, i + 4] = -1
     ref = call(ok, axis=axis)
-    marked = torch.full((T, 8, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    marked = torch.full((T, H, 64), 7.0, dtype=torch.bfloat16, device=DEV)
     before, scales = c["cache"].clone(), c["scale"].clone()
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     out = call(c, axis=axis, q_out=marked, status=status)
@@ -293,9 +296,10 @@ def test_skipped_tokens_of_every_sort(T):
     assert torch.equal(flat_s(c["scale"])[dead], flat_s(scales)[dead])
 
 
-def test_many_tokens_in_place_alone_and_without_rotation():
+@pytest.mark.parametrize("T,H,Hkv", [(1999, 8, 2), (2999, 40, 16)])
+def test_many_tokens_in_place_alone_and_without_rotation(T, H, Hkv):
     kind = pa.KV_FP8_E4M3_ROW
-    c, d, e = (make(620, 1999, 8, 2, 128, 128, 16, kind=kind) for _ in range(3))
+    c, d, e = (make(620, T, H, Hkv, 128, 128, 16, kind=kind) for _ in range(3))
     ref = call(c)
     rest = (d["slots"].to(DEV), d["pos"].to(DEV), d["table"].to(DEV))
     q, k, v = parts(d)
@@ -312,7 +316,7 @@ def test_many_tokens_in_place_alone_and_without_rotation():
     codes, s = R.row_codes_fp32(torch.stack([k, v]))
     live = e["slots"] >= 0
     at = e["slots"][live]
-    assert torch.equal(e["cache"].cpu().reshape(2, -1, 2, 128)[:, at], codes[:, live])
+    assert torch.equal(e["cache"].cpu().reshape(2, -1, Hkv, 128)[:, at], codes[:, live])
     assert torch.equal(R.scales_at(e["scale"], at).permute(2, 0, 1), s[:, live].double())
 
 
@@ -366,3 +370,20 @@ def test_e4m3_decoder_agrees_with_the_oracle():
     for i in range(256):
         o = oracle.e4m3_to_double(i)
         assert (o != o and mine[i] != mine[i]) or o == float(mine[i])
+
+
+def test_one_call_and_its_parts_give_the_same_bits():
+    """The streaming kernel on a whole batch, one warp per step on its parts."""
+    c, d = (make(640, 2600, 32, 8, 128, 128, 16, kind=pa.KV_FP8_E4M3_ROW, norm=True) for _ in range(2))
+    ref = call(c)
+    q, k, v = parts(d)
+    pos, slots, table = d["pos"].to(DEV), d["slots"].to(DEV), d["table"].to(DEV)
+    outs = []
+    for a in range(0, 2600, 400):
+        b = a + 400
+        outs.append(pa.rope_and_cache(q[a:b], k[a:b], v[a:b], d["cache"], slots[a:b], pos[a:b], table,
+                                      block_size=16, kv_dtype=d["kind"], kv_scale=d["scale"],
+                                      q_norm=d["qn"], k_norm=d["kn"], norm_eps=1e-5))
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat(outs), ref)
+    assert torch.equal(c["cache"], d["cache"]) and torch.equal(c["scale"], d["scale"])
