@@ -202,7 +202,9 @@ size_t pattn_workspace_bytes(const pattn_ext_t* ext, int num_heads, int num_kv_h
 
 /*
  * The decode KV partition count pattn_varlen_fwd will use for these sizes
- * (ext->num_splits if set, else the library's choice).  Partitions are runs of
+ * (ext->num_splits if set, else the library's choice).  Over a
+ * PATTN_KV_FP8_E4M3_ROW cache the library's own choice is bounded further, by
+ * max(1, sqrt(visible keys / 16) - 1).  Partitions are runs of
  * ceil(n / splits) whole KV blocks over the n blocks a decode row can see,
  * merged by log-sum-exp ("RBLN Attention modes", flash attention; the Triton
  * backend's 16 parallel softmax segments).

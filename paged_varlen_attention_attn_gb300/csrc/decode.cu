@@ -168,20 +168,41 @@ __device__ __forceinline__ void merge_partitions(const Problem& p, int r, int h,
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[k][e] = 0.f;
   }
-#pragma unroll 2
-  for (int sp = 0; sp < S; ++sp) {
+  // AHEAD partitions' loads go out together (the sums are in partition order
+  // whatever AHEAD is).  Row-scaled e4m3, two (the loop unrolled) / four / eight at
+  // a time, one request of 4096 keys in 64 partitions: 32 / 4 heads 59.0 / 37.5 /
+  // 46.8 us (eight spill), 16 / 2 heads 55.9 / 33.4 / 29.3.
+  constexpr int AHEAD = 4;
+#pragma unroll 1
+  for (int sp0 = 0; sp0 < S; sp0 += AHEAD) {
+    float v[AHEAD][NH][PER];
 #pragma unroll
-    for (int k = 0; k < NH; ++k) {
-      const float w = __shfl_sync(0xffffffffu, sp < 32 ? w0[k] : w1[k], sp & 31);
-      const float* src = p.o_part + ((static_cast<int64_t>(r) * p.H + h + k) * S + sp) * D + lane * PER;
-      if constexpr (PER == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-        acc[k][0] += w * v.x; acc[k][1] += w * v.y; acc[k][2] += w * v.z; acc[k][3] += w * v.w;
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-        acc[k][0] += w * v.x; acc[k][1] += w * v.y;
+    for (int u = 0; u < AHEAD; ++u)
+      if (sp0 + u < S) {
+#pragma unroll
+        for (int k = 0; k < NH; ++k) {
+          const float* src = p.o_part +
+                             ((static_cast<int64_t>(r) * p.H + h + k) * S + sp0 + u) * D + lane * PER;
+          if constexpr (PER == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+            v[u][k][0] = x.x; v[u][k][1] = x.y; v[u][k][2] = x.z; v[u][k][3] = x.w;
+          } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+            v[u][k][0] = x.x; v[u][k][1] = x.y;
+          }
+        }
       }
-    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (sp0 + u < S) {
+        const int sp = sp0 + u;
+#pragma unroll
+        for (int k = 0; k < NH; ++k) {
+          const float w = __shfl_sync(0xffffffffu, sp < 32 ? w0[k] : w1[k], sp & 31);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) acc[k][e] += w * v[u][k][e];
+        }
+      }
   }
 #pragma unroll
   for (int k = 0; k < NH; ++k) {

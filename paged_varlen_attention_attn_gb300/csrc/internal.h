@@ -109,6 +109,16 @@ __host__ __device__ constexpr bool kv_is_e4m3(int kv_dtype) {
   return kv_dtype == PATTN_KV_FP8_E4M3 || kv_dtype == PATTN_KV_FP8_E4M3_ROW;
 }
 
+// The partition count of a decode pass over a PATTN_KV_FP8_E4M3_ROW cache: at
+// most sqrt(visible keys / 16) - 1, at least one: the walk over the keys shrinks
+// with the count and the merge grows with it.  Without the bound / with it, heads
+// of 128: 4 requests of 913 keys, 32 / 4 heads 42.6 / 23.2 us (58 / 6 partitions);
+// 1 of 4096, 16 / 2 heads 34.4 / 25.2 (64 / 15); 16 of up to 95, 32 / 8 heads
+// 19.1 / 15.0 (6 / 1); 1 of 61149, 32 / 8 heads 53.9 / 54.9 to 55.9 (64 / 60).
+// Other caches, a count that the caller forces and the 0 of a refused call keep
+// `splits`.
+int row_scaled_splits(int splits, int forced, int kv_dtype, int max_seq_len, int window);
+
 // Number of SMs of the current device (cached per device; 152 if it cannot be
 // asked).
 int current_sms();

@@ -393,6 +393,12 @@ int current_sms() {
   return counts[dev];
 }
 
+int row_scaled_splits(int splits, int forced, int kv_dtype, int max_seq_len, int window) {
+  if (splits < 1 || forced > 0 || kv_dtype != PATTN_KV_FP8_E4M3_ROW) return splits;
+  const int visible = (window > 0) ? std::min(max_seq_len, window) : max_seq_len;
+  return std::max(1, std::min(splits, static_cast<int>(std::sqrt(visible / 16.0)) - 1));
+}
+
 // The cache type and its scales (host only).
 pattn_status_t check_kv_scale(int kv_dtype, const float* kv_scale) {
   if (kv_dtype < PATTN_KV_BF16 || kv_dtype > PATTN_KV_FP8_E4M3_ROW) return PATTN_ERR_UNSUPPORTED;
@@ -566,7 +572,8 @@ pattn_status_t pattn_varlen_fwd(const void* q, const void* kv_cache, const int32
     return diffkv_fwd(q, kv_cache, block_table, seq_lens, query_start_loc, out, scale, num_heads,
                       num_kv_heads, head_size, block_size, window, causal, kv_dtype, ext);
 
-  const int splits = choose_splits(ext, num_kv_heads, block_size, window);
+  const int splits = row_scaled_splits(choose_splits(ext, num_kv_heads, block_size, window),
+                                       ext->num_splits, kv_dtype, ext->max_seq_len, window);
   const WsLayout L = workspace_layout(ext->num_seqs, ext->num_tokens, num_heads, num_kv_heads, head_size,
                                       ext->max_query_len, splits);
   if (ext->workspace_bytes < L.total) return PATTN_ERR_WORKSPACE_TOO_SMALL;

@@ -84,7 +84,9 @@ extern "C" pattn_status_t pattn_decode_fwd_static(
   ext.max_query_len = 1;
   ext.max_seq_len = max_seq_len;
   ext.num_splits = num_splits;
-  const int splits = pattn_decode_splits(&ext, num_heads, num_kv_heads, block_size, window);
+  const int splits = row_scaled_splits(
+      pattn_decode_splits(&ext, num_heads, num_kv_heads, block_size, window), num_splits, kv_dtype,
+      max_seq_len, window);
   if (splits < 1) return PATTN_ERR_INVALID_ARGUMENT;
   const WsLayout L = workspace_layout(num_seqs, num_tokens, num_heads, num_kv_heads, head_size, 1,
                                       splits);

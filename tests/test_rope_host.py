@@ -229,3 +229,12 @@ def test_row_scaled_attention_arguments_are_checked_on_the_host(lib, kw, status)
     if "hv" not in kw:
         assert pa.pattn_decode_fwd_static(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0.1, 4, 2, 64, 16, 0, 1,
                                           pa.KV_FP8_E4M3_ROW, kw["ks"], 2, 2, 3, 8, 40, 0, 0, lib=lib) == status
+
+
+@pytest.mark.parametrize("hq,hkv,bs,splits", [(5, 2, 16, 0), (4, 2, 0, 0), (4, 0, 16, 0), (4, 2, 16, -1)])
+def test_workspace_free_decode_of_row_scales_refuses_what_it_refuses_of_other_caches(lib, hq, hkv, bs, splits):
+    def call(kind):
+        return pa.pattn_decode_fwd_static(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0.1, hq, hkv, 64, bs, 0, 1,
+                                          kind, FAKE if kind else None, 2, 2, 3, 8, 40, splits, 0, lib=lib)
+    assert call(pa.KV_BF16) != 0
+    assert call(pa.KV_FP8_E4M3_ROW) == call(pa.KV_BF16)
