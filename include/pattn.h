@@ -371,6 +371,8 @@ pattn_status_t pattn_reshape_and_cache_diffkv(const void* key, const void* value
  *   code  = e4m3(x / scale), fp32 division, round to nearest even, saturated
  *           at +-448, NaN stays NaN.
  * An infinity (and a magnitude above 448 * 2^60) is stored as the largest code.
+ * Two tokens on one slot of a row-scaled cache can leave the codes of one with
+ * the scale of the other, here and in pattn_rope_and_cache: slots must be distinct.
  *
  *   key, value      [device] bf16 [num_tokens, num_kv_heads, head_size]
  *   kv_cache        [device] e4m3 bytes, the cache of pattn_varlen_fwd

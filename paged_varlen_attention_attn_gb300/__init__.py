@@ -199,13 +199,13 @@ def reshape_and_cache(key, value, kv_cache, slot_mapping, *, block_size, kv_dtyp
                 ("slot_mapping", slot_mapping, (T,), (torch.int64,))):
             if x.shape != shape or x.dtype not in types or x.device != dev or not x.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {types[0]} tensor of shape {shape}")
+        status_at = _status_at(device_status, dev)
         if T == 0:  # (an empty tensor has no address)
             return kv_cache
         st = _call_on(
             dev, load().pattn_reshape_and_cache_rows, key.data_ptr(), value.data_ptr(),
             kv_cache.data_ptr(), kv_scale.data_ptr(), slot_mapping.data_ptr(), T, Hkv, D,
-            int(block_size), NB, None if device_status is None else device_status.data_ptr(),
-            _raw_stream(stream, dev))
+            int(block_size), NB, status_at or None, _raw_stream(stream, dev))
         if st != 0:
             raise PattnError(st, "pattn_reshape_and_cache_rows")
         return kv_cache
@@ -299,6 +299,18 @@ def _rows_of(x, name, dtype, dev):
     return x.data_ptr(), st if T > 1 else H * D, shape
 
 
+def _status_at(status, dev):
+    """Address of a device_status tensor, 0 for None."""
+    if status is None:
+        return 0
+    import torch
+    if (status.device != dev or status.dtype not in (torch.int32, torch.uint32) or
+            status.numel() < 1):
+        raise ValueError("device_status must be an int32 or uint32 tensor of one element on the "
+                         "call's device")
+    return status.data_ptr()
+
+
 def _norm_at(w, name, dtype, dev, D):
     if w.dtype != dtype or w.shape != (D,) or w.device != dev or not w.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} [head_size] tensor")
@@ -370,7 +382,8 @@ def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *,
     if positions is not None:
         pos_shape = positions.shape
         axes = 1 if len(pos_shape) == 1 else pos_shape[0]
-        if (positions.dtype != torch.int64 or not 1 <= len(pos_shape) <= 2 or pos_shape[-1] != T or
+        if (positions.dtype != torch.int64 or not 1 <= len(pos_shape) <= 2 or axes < 1 or
+                pos_shape[-1] != T or
                 positions.device != dev or (T > 1 and positions.stride(-1) != 1)):
             raise ValueError("positions must be int64 [num_tokens] or [axes, num_tokens]")
         if (cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.device != dev or
@@ -386,12 +399,13 @@ def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *,
             axes_at = ctypes.cast(pairs, ctypes.c_void_p).value
     qn_at = 0 if q_norm is None else _norm_at(q_norm, "q_norm", dt, dev, D)
     kn_at = 0 if k_norm is None else _norm_at(k_norm, "k_norm", dt, dev, D)
+    status_at = _status_at(device_status, dev)
     if T == 0:  # (an empty tensor has no address)
         return q_out
     args = _ROPE_PACK.pack(
         _ROPE_PACK.size, q_at, qo_at, k_at, v_at, q_st, qo_st, k_st, v_st, table_at, pos_at, pos_st,
         axes_at, qn_at, kn_at, cache_at, rows_at, scale_at, slots_at,
-        0 if device_status is None else device_status.data_ptr(), _raw_stream(stream, dev),
+        status_at, _raw_stream(stream, dev),
         norm_eps, T, H, Hkv, D, rot, interleaved, axes, max_pos, kv_dtype, block_size, NB)
     st = _call_on(dev, load().pattn_rope_and_cache, args)
     if st != 0:
@@ -411,7 +425,8 @@ def gather_cache(kv_cache, block_table, out_start_loc, *, num_rows, block_size, 
     import torch
     dev = kv_cache.device
     cache_shape = kv_cache.shape
-    if len(cache_shape) != 5 or cache_shape[2] != block_size or not kv_cache.is_contiguous():
+    if (len(cache_shape) != 5 or cache_shape[0] != 2 or cache_shape[2] != block_size or
+            not kv_cache.is_contiguous()):
         raise ValueError("kv_cache must be a contiguous [2, num_blocks, block_size, num_kv_heads, "
                          "head_size] tensor")
     _, NB, _, Hkv, D = cache_shape
@@ -443,14 +458,15 @@ def gather_cache(kv_cache, block_table, out_start_loc, *, num_rows, block_size, 
             raise ValueError(f"key_out and value_out must be contiguous {dt} tensors of shape {shape}")
         outs.append(x)
     key_out, value_out = outs
+    status_at = _status_at(device_status, dev)
     if num_rows == 0 or B == 0:  # (an empty tensor has no address)
         return key_out, value_out
     st = _call_on(
-        dev, load().pattn_gather_cache, kv_cache.data_ptr(), block_table.data_ptr(), starts_at or None, out_start_loc.data_ptr(),
+        dev, load().pattn_gather_cache, kv_cache.data_ptr(), block_table.data_ptr(),
+        starts_at or None, out_start_loc.data_ptr(),
         key_out.data_ptr(), value_out.data_ptr(), B, int(num_rows), mbps, NB, Hkv, D,
         int(block_size), int(kv_dtype),
-        _scale_arg(kv_dtype, kv_scale), None if device_status is None else device_status.data_ptr(),
-        _raw_stream(stream, dev))
+        _scale_arg(kv_dtype, kv_scale), status_at or None, _raw_stream(stream, dev))
     if st != 0:
         raise PattnError(st, "pattn_gather_cache")
     return key_out, value_out

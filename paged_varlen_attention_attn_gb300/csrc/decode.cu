@@ -229,8 +229,9 @@ __device__ __forceinline__ void merge_partitions(const Problem& p, int r, int h,
 // over y_k = x_k + log2 vs_k: the packed f16 weights 2^(y_k - m) keep their
 // range whatever the V scales are, and the normaliser sum_k 2^(x_k - m) =
 // sum_k 2^(y_k - m) / vs_k is summed in fp32 beside them.  8 requests of 120001
-// to 131072 keys, 64 / 8 heads of 128: 334 us, 6.3 TB/s with the scales (93 % of
-// the measured copy bandwidth; 324 us for one scale per tensor).  A third
+// to 131072 keys, 64 / 8 heads of 128: 329 us, 6.4 TB/s with the scales (95 % of
+// the measured copy bandwidth); with L2 flushed first 345 us, 332 for one scale
+// per tensor.  A third
 // producer warp for the scales left the consumers 80 registers, and they spilled.
 template <int D, bool FP8, int NT, int HG, int WPH, bool HALF, bool ROWS>
 __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH, ROWS>::THREADS, WPH > 1 ? 2 : 1)

@@ -159,7 +159,9 @@ extern "C" pattn_status_t pattn_gather_cache(const void* kv_cache, const int32_t
     p.scale[0] = kv_scale[0];
     p.scale[1] = kv_scale[1];
   }
-  if (kv_dtype == PATTN_KV_FP8_E4M3_ROW && !kv_scale) return PATTN_ERR_INVALID_ARGUMENT;
+  if (kv_dtype == PATTN_KV_FP8_E4M3_ROW &&
+      (!kv_scale || (reinterpret_cast<uintptr_t>(kv_scale) & 15)))
+    return PATTN_ERR_INVALID_ARGUMENT;
   if ((reinterpret_cast<uintptr_t>(kv_cache) | reinterpret_cast<uintptr_t>(key_out) |
        reinterpret_cast<uintptr_t>(value_out)) & 15)
     return PATTN_ERR_INVALID_ARGUMENT;

@@ -105,7 +105,7 @@ int test_wait_skip();
 #endif
 
 // Whether the cache holds e4m3 codes (scaled per tensor or per row).
-__host__ __device__ constexpr bool kv_is_e4m3(int kv_dtype) { 
+__host__ __device__ constexpr bool kv_is_e4m3(int kv_dtype) {
   return kv_dtype == PATTN_KV_FP8_E4M3 || kv_dtype == PATTN_KV_FP8_E4M3_ROW;
 }
 

@@ -238,3 +238,45 @@ def test_workspace_free_decode_of_row_scales_refuses_what_it_refuses_of_other_ca
                                           kind, FAKE if kind else None, 2, 2, 3, 8, 40, splits, 0, lib=lib)
     assert call(pa.KV_BF16) != 0
     assert call(pa.KV_FP8_E4M3_ROW) == call(pa.KV_BF16)
+
+
+def _rope_tensors(**kw):
+    T, H, Hkv, D, NB = 4, 4, 2, 64, 3
+    t = dict(q=torch.zeros(T, H, D).bfloat16(), key=torch.zeros(T, Hkv, D).bfloat16(),
+             value=torch.zeros(T, Hkv, D).bfloat16(), kv_cache=torch.zeros(2, NB, 16, Hkv, D).bfloat16(),
+             slot_mapping=torch.arange(T), positions=torch.arange(T), cos_sin=torch.zeros(8, 64))
+    t.update(kw)
+    return t
+
+
+@pytest.mark.parametrize("status", [torch.zeros(1, dtype=torch.int32, device="meta"),
+                                    torch.zeros(1, dtype=torch.int64), torch.zeros(1),
+                                    torch.zeros(0, dtype=torch.int32)])
+def test_a_status_word_elsewhere_or_of_another_type_is_refused(lib, status):
+    t = _rope_tensors()
+    with pytest.raises(ValueError, match="device_status"):
+        pa.rope_and_cache(**t, block_size=16, device_status=status)
+    with pytest.raises(ValueError, match="device_status"):
+        pa.reshape_and_cache(t["key"], t["value"], torch.zeros(2, 3, 16, 2, 64, dtype=torch.uint8),
+                             t["slot_mapping"], block_size=16, kv_dtype=pa.KV_FP8_E4M3_ROW,
+                             kv_scale=torch.zeros(pa.row_scales_shape(3, 16, 2)), device_status=status)
+    with pytest.raises(ValueError, match="device_status"):
+        pa.gather_cache(t["kv_cache"], torch.zeros(1, 2, dtype=torch.int32),
+                        torch.tensor([0, 4], dtype=torch.int32), num_rows=4, block_size=16,
+                        device_status=status)
+
+
+def test_positions_without_an_axis_are_refused(lib):
+    with pytest.raises(ValueError, match="positions"):
+        pa.rope_and_cache(**_rope_tensors(positions=torch.zeros(0, 4, dtype=torch.int64)), block_size=16)
+
+
+def test_read_back_of_half_a_cache_is_refused(lib):
+    with pytest.raises(ValueError, match="kv_cache"):
+        pa.gather_cache(torch.zeros(1, 3, 16, 2, 64).bfloat16(), torch.zeros(1, 2, dtype=torch.int32),
+                        torch.tensor([0, 4], dtype=torch.int32), num_rows=4, block_size=16)
+
+
+def test_read_back_of_misaligned_row_scales_is_refused(lib):
+    assert lib.pattn_gather_cache(FAKE, FAKE, None, FAKE, FAKE, FAKE, 1, 0, 2, 3, 2, 64, 16,
+                                  pa.KV_FP8_E4M3_ROW, FAKE + 4, None, None) == 1
