@@ -123,6 +123,27 @@ def test_partitions(D, splits):
     c.check(c.run(num_splits=splits))
 
 
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("H,Hkv", [(8, 2), (32, 8)])
+@pytest.mark.parametrize("most", [1, 63, 64, 145, 579, 1601, 4096])
+def test_the_chosen_partition_count(most, H, Hkv, window):
+    # from one partition over a few keys to fifteen, and what each merges to by force
+    c = Case(75 + most + window, [(1, most), (1, max(1, most // 3)), (1, 1)], H, Hkv, 128, 16)
+    out = c.run(window=window)
+    c.check(out, window=window)
+    visible = min(most, window) if window else most
+    bound = max(1, int((visible / 16) ** 0.5) - 1)
+    forced = c.run(window=window, num_splits=bound)
+    assert torch.equal(out, forced)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [2, 5, 7, 33, 63, 64])
+def test_merges_of_every_remainder(D, splits):
+    c = Case(78 + D, [(1, 900), (1, 33), (1, 2000)], 8, 4, D, 16)
+    c.check(c.run(num_splits=splits))
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_sinks(D):
     c = Case(80 + D, BATCHES["mixed"], 8, 2, D, 16)
