@@ -550,8 +550,10 @@ cudaError_t launch_kind(RopeParams& p, int sms, cudaStream_t st) {
     while (p.team > 1 && 2 * (2 * RS_WARPS / p.team) <= p.stages) p.team /= 2;
     const int smem = RS_HEAD + p.stages * p.stage_bytes;
     auto kern = rope_stream_kernel<LPR, KIND>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // The limit belongs to the kernel, not to this launch: the same value in every
+    // call, so that no host thread lowers it between another's set and launch.
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               RS_HEAD + RS_RING_BYTES);
     if (e != cudaSuccess) return e;
     kern<<<2 * sms, (RS_WARPS + 1) * 32, smem, st>>>(p);
   } else {
