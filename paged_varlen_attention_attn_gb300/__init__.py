@@ -4,6 +4,10 @@ Argument marshalling only: every step of the computation runs in the CUDA
 kernels of ``libpattn.so`` (built by ``_build.build()``).  There is no CPU or
 PyTorch fallback; if the library is missing, ``load()`` raises.
 
+``stream=`` of a call is the torch stream it runs on (default: the current one);
+an output that the call allocates belongs to that stream, as if it were
+allocated under ``torch.cuda.stream(stream)``.
+
 The names follow the C ABI in ``include/pattn.h``:
 ``pattn_varlen_fwd``, ``pattn_workspace_bytes``, ``pattn_decode_splits``,
 ``pattn_read_device_status``, ``pattn_status_string``, ``pattn_version``.
@@ -277,6 +281,19 @@ def _raw_stream(stream, dev):
     return (_torch_c or _torch())._cuda_getCurrentRawStream(dev.index)
 
 
+def _empty(shape, dtype, dev, stream):
+    """torch.empty from the pool of the stream the call runs on (None: the device's
+    current one), so that the allocator hands the memory to nobody before the call
+    is done with it.  From another stream's pool nothing would order the two."""
+    import torch
+    if stream is None or stream.cuda_stream == _raw_stream(None, dev):
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):  # any object with the handle
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _call_on(dev, fn, *args):
     """fn(*args) with ``dev`` the current device, as the library's launches need."""
     if dev.index == (_torch_c or _torch())._cuda_getDevice():
@@ -348,7 +365,7 @@ def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *,
         q_at, q_st, shape = _rows_of(q, "q", dt, dev)
         T, H, D = shape
         if q_out is None:
-            q_out = torch.empty(shape, dtype=dt, device=dev)
+            q_out = _empty(shape, dt, dev, stream)
         qo_at, qo_st, out_shape = _rows_of(q_out, "q_out", dt, dev)
         if out_shape != shape:
             raise ValueError("q_out must have q's shape")
@@ -453,7 +470,7 @@ def gather_cache(kv_cache, block_table, out_start_loc, *, num_rows, block_size, 
     outs = []
     for x in (key_out, value_out):
         if x is None:
-            x = torch.empty(shape, dtype=dt, device=dev)
+            x = _empty(shape, dt, dev, stream)
         elif x.shape != shape or x.dtype != dt or x.device != dev or not x.is_contiguous():
             raise ValueError(f"key_out and value_out must be contiguous {dt} tensors of shape {shape}")
         outs.append(x)
@@ -496,7 +513,7 @@ def cascade_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scal
         _check_row_scales(kv_scale, kv_cache.shape[1], block_size, num_kv_heads, dev)
     if out is None:
         odt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
-        out = torch.empty((T, num_heads, head_size), dtype=odt, device=dev)
+        out = _empty((T, num_heads, head_size), odt, dev, stream)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     ext = make_ext(num_seqs=seq_lens.shape[0], num_tokens=T,
@@ -663,7 +680,7 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
     T = q.shape[0]
     if out is None:
         odt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
-        out = torch.empty((T, num_heads, head_size_v or head_size), dtype=odt, device=dev)
+        out = _empty((T, num_heads, head_size_v or head_size), odt, dev, stream)
     num_blocks = kv_cache.shape[0] if head_size_v else kv_cache.shape[1]
     if kv_dtype == KV_FP8_E4M3_ROW:
         _check_row_scales(kv_scale, num_blocks, block_size, num_kv_heads, dev)
