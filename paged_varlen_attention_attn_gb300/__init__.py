@@ -525,9 +525,11 @@ def cascade_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scal
                                          common_prefix_len)
     if need == 0:
         raise PattnError(1, "pattn_cascade_workspace_bytes")
-    ws = _workspace(workspace, dev, stream.cuda_stream).get(need, dev)
-    ext.workspace = ws.data_ptr()
-    ext.workspace_bytes = ws.numel()
+    ws = _workspace(workspace, dev, stream.cuda_stream)
+    buf = ws.get(need, dev, stream)
+    ws.used_on(stream.cuda_stream)
+    ext.workspace = buf.data_ptr()
+    ext.workspace_bytes = buf.numel()
     ks = _scale_arg(kv_dtype, kv_scale)
     st = load().pattn_cascade_fwd(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
                                   seq_lens.data_ptr(), query_start_loc.data_ptr(), out.data_ptr(),
@@ -613,21 +615,43 @@ def pattn_version(lib=None):
 
 
 class Workspace:
-    """A torch-allocated device workspace, grown on demand (plumbing only)."""
+    """A torch-allocated device workspace, grown on demand (plumbing only).
+
+    A buffer comes from the pool of the stream whose call needed it, and one that
+    is replaced goes back there, where the next use is ordered behind the calls.
+    A buffer that calls on another stream have used too is not given back before
+    the Workspace is."""
 
     def __init__(self):
         self.buf = None
+        self._stream = None  # whose pool the buffer is from (cudaStream_t)
+        self._held = False   # not to be given back when it is replaced
+        self._replaced = []
 
     def current(self, device):
         """The buffer it has on ``device``, or None."""
         return self.buf if self.buf is not None and self.buf.device == device else None
 
-    def get(self, nbytes, device):
+    def get(self, nbytes, device, stream=None):
+        """A buffer of at least ``nbytes`` for a call on ``stream`` (default: the
+        device's current one)."""
         import torch
         nbytes = max(256, int(nbytes))
-        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(device):
-            self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != device:
+            buf = _empty(nbytes, torch.uint8, device, stream)
+            if self._held:
+                self._replaced.append(self.buf)
+            self.buf, self._held = buf, False
+            self._stream = _raw_stream(stream, device) if device.type == "cuda" else 0
         return self.buf
+
+    def used_on(self, raw_stream):
+        """Notes that a call on a cudaStream_t is about to use the buffer."""
+        if raw_stream != self._stream:
+            self._held = True
 
 
 _default_ws = {}  # (device index, cudaStream_t) -> Workspace
@@ -703,13 +727,17 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
             int(num_kv_heads), int(head_size), int(block_size), int(window), int(causal),
             int(kv_dtype), _scale_arg(kv_dtype, kv_scale), ext)
     # the library itself says when the workspace is missing or too small
-    st = 3 if buf is None else _call_on(dev, run, *args)
+    st = 3
+    if buf is not None:
+        ws.used_on(raw_stream)
+        st = _call_on(dev, run, *args)
     if st != 0:
         need = pattn_workspace_bytes(ext, num_heads, num_kv_heads, head_size, block_size, lib=lib)
         if need == 0:
             raise PattnError(1, "pattn_workspace_bytes")
         if st == 3:
-            buf = ws.get(need, dev)
+            buf = ws.get(need, dev, stream)
+            ws.used_on(raw_stream)
             ext.workspace, ext.workspace_bytes = buf.data_ptr(), buf.numel()
             st = _call_on(dev, run, *args)
     if check and st != 0:

@@ -87,3 +87,35 @@ def test_outputs_belong_to_the_calls_stream(call):
     for x, y in zip(got, call(None)):
         assert owner(y.data_ptr()) == torch.cuda.current_stream().cuda_stream
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("call", [call_forward, call_cascade])
+def test_a_workspace_belongs_to_the_calls_stream_also_when_it_grows(call, own):
+    s = side_stream()
+    kw = {"workspace": pa.Workspace()} if own else {}
+    pa._default_ws.clear()  # (the stream may have served another test)
+    before = 0
+    for reqs in (SMALL, LARGE):
+        got = call(s, reqs, **kw)
+        s.synchronize()
+        ext = pa.forward.last_ext
+        assert owner(ext.workspace) == s.cuda_stream
+        assert ext.workspace_bytes > before
+        before = ext.workspace_bytes
+        assert torch.equal(got[0], call(None, reqs)[0])
+
+
+def test_a_workspace_of_several_streams_keeps_the_buffer_it_replaces():
+    """Its memory is no other tensor's while a call on the second stream may use it."""
+    ws = pa.Workspace()
+    call_forward(None, workspace=ws)
+    a, size = ws.buf.data_ptr(), ws.buf.numel()
+    call_forward(side_stream(), workspace=ws)
+    assert ws.buf.data_ptr() == a
+    call_forward(None, LARGE, workspace=ws)
+    b = ws.buf.data_ptr()
+    assert b != a
+    others = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(8)]
+    assert a not in [x.data_ptr() for x in others]
+    torch.cuda.synchronize()
