@@ -294,6 +294,22 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+_driver = None
+
+
+def _capturing(raw_stream):
+    """Whether a graph is being captured from a cudaStream_t.  (Asked of the driver,
+    which answers for any stream, current or not, in 0.45 us.)"""
+    global _driver
+    if not raw_stream:  # the legacy default stream cannot be captured
+        return False
+    if _driver is None:
+        _driver = ctypes.CDLL("libcuda.so.1")
+        _driver.cuStreamIsCapturing.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int)]
+    status = ctypes.c_int(0)
+    return _driver.cuStreamIsCapturing(raw_stream, status) == 0 and status.value != 0
+
+
 def _call_on(dev, fn, *args):
     """fn(*args) with ``dev`` the current device, as the library's launches need."""
     if dev.index == (_torch_c or _torch())._cuda_getDevice():
@@ -619,8 +635,10 @@ class Workspace:
 
     A buffer comes from the pool of the stream whose call needed it, and one that
     is replaced goes back there, where the next use is ordered behind the calls.
-    A buffer that calls on another stream have used too is not given back before
-    the Workspace is."""
+    A buffer that calls on another stream have used too, or that is part of a
+    captured graph (its replays write to the address that the capture saw), is not
+    given back before the Workspace is: keep an explicit Workspace as long as a
+    graph captured with it."""
 
     def __init__(self):
         self.buf = None
@@ -650,7 +668,7 @@ class Workspace:
 
     def used_on(self, raw_stream):
         """Notes that a call on a cudaStream_t is about to use the buffer."""
-        if raw_stream != self._stream:
+        if not self._held and (raw_stream != self._stream or _capturing(raw_stream)):
             self._held = True
 
 
@@ -659,8 +677,8 @@ _default_ws = {}  # (device index, cudaStream_t) -> Workspace
 
 def _workspace(workspace, dev, raw_stream):
     """The caller's Workspace, or the stream's own: calls on one stream run one
-    after the other and may share scratch, calls on two streams may not.  (Two
-    captured graphs that may run at once need a Workspace each.)"""
+    after the other and may share scratch, calls on two streams may not.  (Nor may
+    two captured graphs that run at once: they need a Workspace each.)"""
     if workspace is not None:
         return workspace
     key = (dev.index, raw_stream)
