@@ -18,6 +18,7 @@ torch (plumbing; the library itself allocates nothing).
 import ctypes
 import os
 import struct
+import threading
 
 from . import _build
 
@@ -672,16 +673,17 @@ class Workspace:
             self._held = True
 
 
-_default_ws = {}  # (device index, cudaStream_t) -> Workspace
+_default_ws = {}  # (device index, cudaStream_t, host thread) -> Workspace
 
 
 def _workspace(workspace, dev, raw_stream):
-    """The caller's Workspace, or the stream's own: calls on one stream run one
-    after the other and may share scratch, calls on two streams may not.  (Nor may
-    two captured graphs that run at once: they need a Workspace each.)"""
+    """The caller's Workspace, or the stream's own: a thread's calls on one stream
+    run one after the other and may share scratch.  Calls on two streams may not,
+    nor two threads' calls on one, whose launches interleave.  (Nor may two captured
+    graphs that run at once: they need a Workspace each.)"""
     if workspace is not None:
         return workspace
-    key = (dev.index, raw_stream)
+    key = (dev.index, raw_stream, threading.get_ident())
     if key not in _default_ws:
         _default_ws[key] = Workspace()
     return _default_ws[key]
@@ -709,7 +711,8 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
     the library never reads device memory on the host.  ``kv_scale``: (k_scale,
     v_scale) of an e4m3 cache, or the row-scale tensor of a KV_FP8_E4M3_ROW cache
     (see ``row_scales_shape``).  ``workspace``: a Workspace (default: one per
-    stream; two graphs that may run at once need one each).  ``timing_events``:
+    stream and host thread; two graphs that may run at once need one each, and a
+    Workspace serves one thread at a time).  ``timing_events``:
     optional 8 raw cudaEvent_t handles (see pattn_ext_t).  ``sinks``: optional
     fp32 [num_heads] device tensor of attention-sink logits.  ``head_size_v``:
     > 0 selects the DiffKV cache layout [num_blocks, block_size, num_kv_heads,

@@ -73,3 +73,30 @@ def test_streamed_rotary_calls_of_two_shapes_from_two_threads():
     assert not refused[0] and not refused[1], (len(refused[0]), len(refused[1]))
     for a, b in want:
         assert torch.equal(a, b)
+
+
+def test_attention_calls_of_two_threads_on_one_stream():
+    """Default workspaces: partitioned decodes and chunks, all on one stream."""
+    from test_row_scaled_attention_gpu import Case
+    cases = [Case(400, [(1, 3000), (1, 2500)], 8, 2, 128, 16),
+             Case(401, [(1, 2800), (140, 300), (1, 900)], 8, 2, 128, 16)]
+    calls = [(c.args(), c.kw(num_splits=8)) for c in cases]
+    want = [pa.forward(*a, **kw) for a, kw in calls]
+    outs = [[torch.empty_like(w) for _ in range(200)] for w in want]
+    torch.cuda.synchronize()
+    start = threading.Barrier(2)
+
+    def work(i):
+        start.wait()
+        for out in outs[i]:
+            pa.forward(*calls[i][0], out=out, **calls[i][1])
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for c, w, got in zip(cases, want, outs):
+        c.check(w)
+        assert all(torch.equal(x, w) for x in got)

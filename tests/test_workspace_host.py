@@ -1,7 +1,10 @@
 """Default and explicit workspaces, without a GPU."""
+import threading
+import time
 import weakref
 
 import pytest
+import torch
 
 import paged_varlen_attention_attn_gb300 as pa
 
@@ -23,3 +26,27 @@ def test_a_buffer_in_a_captured_graph_is_not_given_back(monkeypatch, captured):
     assert (first() is not None) == captured
     del ws
     assert first() is None
+
+
+def test_host_threads_have_default_workspaces_of_their_own():
+    """Two threads' calls on one stream interleave their launches."""
+    device, stream, got = torch.device("cuda", 0), 4096, []
+    work = threading.Event()
+
+    def call():
+        got.append(pa._workspace(None, device, stream))
+        work.wait(30)
+
+    threads = [threading.Thread(target=call) for _ in range(2)]
+    for t in threads:
+        t.start()
+    while len(got) < 2:
+        time.sleep(0.001)
+    mine = [pa._workspace(None, device, stream) for _ in range(2)]
+    work.set()
+    for t in threads:
+        t.join()
+    assert mine[0] is mine[1]
+    assert len({id(w) for w in (got[0], got[1], mine[0])}) == 3
+    own = pa.Workspace()
+    assert pa._workspace(own, device, stream) is own
