@@ -689,6 +689,13 @@ def _workspace(workspace, dev, raw_stream):
     return _default_ws[key]
 
 
+def release_workspaces():
+    """Gives every default workspace back to torch's allocator (each stream and host
+    thread keeps its largest one otherwise).  Not while a graph captured with one
+    may still be replayed."""
+    _default_ws.clear()
+
+
 def _sinks_ptr(sinks, num_heads, device):
     """Device pointer of an fp32 [num_heads] sink tensor (0 for None)."""
     if sinks is None:

@@ -50,3 +50,12 @@ def test_host_threads_have_default_workspaces_of_their_own():
     assert len({id(w) for w in (got[0], got[1], mine[0])}) == 3
     own = pa.Workspace()
     assert pa._workspace(own, device, stream) is own
+
+
+def test_default_workspaces_can_be_released():
+    ws = pa._workspace(None, torch.device("cuda", 0), 4096)
+    buf = weakref.ref(ws.get(1000, "cpu"))
+    del ws
+    assert buf() is not None
+    pa.release_workspaces()
+    assert buf() is None
