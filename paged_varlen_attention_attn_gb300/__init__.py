@@ -86,6 +86,14 @@ def _packer(cls):
     return struct.Struct(fmt + "x" * pad)
 
 
+def _pack(packer, what, *values):
+    """The structure's bytes; sizes that its fields do not hold are invalid."""
+    try:
+        return packer.pack(*values)
+    except (struct.error, OverflowError):
+        raise PattnError(1, what) from None
+
+
 _ROPE_PACK = _packer(RopeArgs)
 _EXT_PACK = _packer(Ext)
 
@@ -436,11 +444,12 @@ def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *,
     status_at = _status_at(device_status, dev)
     if T == 0:  # (an empty tensor has no address)
         return q_out
-    args = _ROPE_PACK.pack(
-        _ROPE_PACK.size, q_at, qo_at, k_at, v_at, q_st, qo_st, k_st, v_st, table_at, pos_at, pos_st,
-        axes_at, qn_at, kn_at, cache_at, rows_at, scale_at, slots_at,
-        status_at, _raw_stream(stream, dev),
-        norm_eps, T, H, Hkv, D, rot, interleaved, axes, max_pos, kv_dtype, block_size, NB)
+    args = _pack(
+        _ROPE_PACK, "pattn_rope_and_cache", _ROPE_PACK.size, q_at, qo_at, k_at, v_at, q_st, qo_st,
+        k_st, v_st, table_at, pos_at, pos_st, axes_at, qn_at, kn_at, cache_at, rows_at, scale_at,
+        slots_at, status_at, _raw_stream(stream, dev),
+        float(norm_eps), T, H, Hkv, D, rot, int(interleaved), axes, max_pos, int(kv_dtype),
+        int(block_size), NB)
     st = _call_on(dev, load().pattn_rope_and_cache, args)
     if st != 0:
         raise PattnError(st, "pattn_rope_and_cache")
@@ -743,11 +752,12 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
         events = (ctypes.c_void_p * 8)(*[int(x) for x in timing_events])
     ws = _workspace(workspace, dev, raw_stream)
     buf = ws.current(dev)
-    ext = Ext.from_buffer_copy(_EXT_PACK.pack(
-        _EXT_PACK.size, seq_lens.shape[0], T, mbps, num_blocks, max_query_len, max_seq_len,
-        num_splits, 0 if buf is None else buf.data_ptr(), 0 if buf is None else buf.numel(),
-        raw_stream, 0 if events is None else ctypes.addressof(events),
-        _sinks_ptr(sinks, num_heads, dev), head_size_v))
+    ext = Ext.from_buffer_copy(_pack(
+        _EXT_PACK, "pattn_varlen_fwd", _EXT_PACK.size, seq_lens.shape[0], T, mbps, num_blocks,
+        int(max_query_len), int(max_seq_len), int(num_splits),
+        0 if buf is None else buf.data_ptr(), 0 if buf is None else buf.numel(), raw_stream,
+        0 if events is None else ctypes.addressof(events), _sinks_ptr(sinks, num_heads, dev),
+        int(head_size_v)))
     ext._events_keepalive = events
     run = (lib or load()).pattn_varlen_fwd
     args = (q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),

@@ -1,0 +1,78 @@
+"""The binding's handling of its arguments, with a library that records its calls
+(no GPU)."""
+import pytest
+import torch
+
+import paged_varlen_attention_attn_gb300 as pa
+
+NEED = 4096
+
+
+class Library:
+    """Answers like libpattn's entry points and keeps what it was called with."""
+
+    def __init__(self):
+        self.calls = []
+
+    def pattn_workspace_bytes(self, *args):
+        self.calls.append(("pattn_workspace_bytes", args))
+        return NEED
+
+    def pattn_varlen_fwd(self, *args):
+        self.calls.append(("pattn_varlen_fwd", args))
+        return 0 if args[-1].workspace_bytes >= NEED else 3
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(pa, "load", lambda path=None: lib)
+    monkeypatch.setattr(pa, "_raw_stream", lambda stream, dev: 0 if stream is None else stream.cuda_stream)
+    monkeypatch.setattr(pa, "_call_on", lambda dev, fn, *args: fn(*args))
+    return lib
+
+
+def _forward(**kw):
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    args = (q, torch.zeros(2, 5, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 3, dtype=torch.int32),
+            torch.ones(2, dtype=torch.int32), torch.tensor([0, 1, 3], dtype=torch.int32))
+    base = dict(scale=1.0, num_heads=4, num_kv_heads=2, head_size=64, block_size=16, max_query_len=2,
+                max_seq_len=40, workspace=pa.Workspace())
+    return pa.forward(*args, **{**base, **kw})
+
+
+@pytest.mark.parametrize("kind", [int, float, torch.tensor, lambda x: torch.tensor(float(x))])
+def test_sizes_may_be_any_number(lib, kind):
+    """As int() takes them: a maximum of a float tensor, a quotient."""
+    _forward(max_query_len=kind(2), max_seq_len=kind(40), num_splits=kind(3), head_size_v=kind(0))
+    ext = lib.calls[-1][1][-1]
+    assert (ext.max_query_len, ext.max_seq_len, ext.num_splits, ext.head_size_v) == (2, 40, 3, 0)
+    assert (ext.num_seqs, ext.num_tokens, ext.max_blocks_per_seq, ext.num_blocks) == (2, 3, 3, 5)
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    with pytest.raises(pa.PattnError) as e:
+        _forward(max_seq_len=1 << 31)
+    assert e.value.status == 1
+
+
+def _rope(lib, **kw):
+    seen = []
+    lib.pattn_rope_and_cache = lambda args: seen.append(pa.RopeArgs.from_buffer_copy(args)) or 0
+    T, H, Hkv, D, NB = 4, 4, 2, 64, 3
+    t = dict(q=torch.zeros(T, H, D).bfloat16(), key=torch.zeros(T, Hkv, D).bfloat16(),
+             value=torch.zeros(T, Hkv, D).bfloat16(), kv_cache=torch.zeros(2, NB, 16, Hkv, D).bfloat16(),
+             slot_mapping=torch.arange(T), positions=torch.arange(T), cos_sin=torch.zeros(8, D),
+             block_size=16)
+    pa.rope_and_cache(**{**t, **kw})
+    return seen[0]
+
+
+def test_rotary_sizes_may_be_any_number(lib):
+    a = _rope(lib, block_size=16.0, norm_eps=1, interleaved=True)
+    assert (a.block_size, a.norm_eps, a.interleaved, a.num_tokens) == (16, 1.0, 1, 4)
+
+
+def test_a_norm_eps_past_fp32_arrives_as_an_infinity(lib):
+    # (which the library refuses, as it does a NaN)
+    assert _rope(lib, norm_eps=1e300).norm_eps == float("inf")
