@@ -222,13 +222,11 @@ def reshape_and_cache(key, value, kv_cache, slot_mapping, *, block_size, kv_dtyp
         if st != 0:
             raise PattnError(st, "pattn_reshape_and_cache_rows")
         return kv_cache
-    if stream is None:
-        stream = torch.cuda.current_stream(key.device)
-    st = pattn_reshape_and_cache(key.data_ptr(), value.data_ptr(), kv_cache.data_ptr(),
-                                 slot_mapping.data_ptr(), key.shape[0], key.shape[1],
-                                 key.shape[2], block_size, kv_cache.shape[1], kv_dtype, kv_scale,
-                                 0 if device_status is None else device_status.data_ptr(),
-                                 stream.cuda_stream)
+    st = _call_on(key.device, pattn_reshape_and_cache, key.data_ptr(), value.data_ptr(),
+                  kv_cache.data_ptr(), slot_mapping.data_ptr(), key.shape[0], key.shape[1],
+                  key.shape[2], block_size, kv_cache.shape[1], kv_dtype, kv_scale,
+                  0 if device_status is None else device_status.data_ptr(),
+                  _raw_stream(stream, key.device))
     if st != 0:
         raise PattnError(st, "pattn_reshape_and_cache")
     return kv_cache
@@ -239,14 +237,12 @@ def reshape_and_cache_diffkv(key, value, kv_cache, slot_mapping, *, block_size,
     """pattn_reshape_and_cache_diffkv on torch tensors: key 16-bit [T, Hkv, dk],
     value [T, Hkv, dv], kv_cache [num_blocks, block_size, Hkv, dk + dv],
     slot_mapping int64 [T].  Raises PattnError."""
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(key.device)
-    st = load().pattn_reshape_and_cache_diffkv(
-        key.data_ptr(), value.data_ptr(), kv_cache.data_ptr(), slot_mapping.data_ptr(),
-        int(key.shape[0]), int(key.shape[1]), int(key.shape[2]), int(value.shape[2]),
-        int(block_size), int(kv_cache.shape[0]), int(kv_dtype),
-        None if device_status is None else device_status.data_ptr(), stream.cuda_stream)
+    st = _call_on(
+        key.device, load().pattn_reshape_and_cache_diffkv, key.data_ptr(), value.data_ptr(),
+        kv_cache.data_ptr(), slot_mapping.data_ptr(), int(key.shape[0]), int(key.shape[1]),
+        int(key.shape[2]), int(value.shape[2]), int(block_size), int(kv_cache.shape[0]),
+        int(kv_dtype), None if device_status is None else device_status.data_ptr(),
+        _raw_stream(stream, key.device))
     if st != 0:
         raise PattnError(st, "pattn_reshape_and_cache_diffkv")
     return kv_cache
@@ -540,28 +536,26 @@ def cascade_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scal
     if out is None:
         odt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
         out = _empty((T, num_heads, head_size), odt, dev, stream)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    raw_stream = _raw_stream(stream, dev)
     ext = make_ext(num_seqs=seq_lens.shape[0], num_tokens=T,
                    max_blocks_per_seq=block_table.shape[1], num_blocks=kv_cache.shape[1],
                    max_query_len=max_query_len, max_seq_len=max_seq_len,
-                   num_splits=num_splits, stream=stream.cuda_stream,
+                   num_splits=num_splits, stream=raw_stream,
                    sinks=_sinks_ptr(sinks, num_heads, dev))
-    need = pattn_cascade_workspace_bytes(ext, num_heads, num_kv_heads, head_size, block_size,
-                                         common_prefix_len)
+    need = _call_on(dev, pattn_cascade_workspace_bytes, ext, num_heads, num_kv_heads, head_size,
+                    block_size, common_prefix_len)
     if need == 0:
         raise PattnError(1, "pattn_cascade_workspace_bytes")
-    ws = _workspace(workspace, dev, stream.cuda_stream)
+    ws = _workspace(workspace, dev, raw_stream)
     buf = ws.get(need, dev, stream)
-    ws.used_on(stream.cuda_stream)
+    ws.used_on(raw_stream)
     ext.workspace = buf.data_ptr()
     ext.workspace_bytes = buf.numel()
-    ks = _scale_arg(kv_dtype, kv_scale)
-    st = load().pattn_cascade_fwd(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
-                                  seq_lens.data_ptr(), query_start_loc.data_ptr(), out.data_ptr(),
-                                  float(scale), int(num_heads), int(num_kv_heads), int(head_size),
-                                  int(block_size), int(window), int(causal), int(kv_dtype), ks,
-                                  int(common_prefix_len), ctypes.byref(ext))
+    st = _call_on(dev, load().pattn_cascade_fwd, q.data_ptr(), kv_cache.data_ptr(),
+                  block_table.data_ptr(), seq_lens.data_ptr(), query_start_loc.data_ptr(),
+                  out.data_ptr(), float(scale), int(num_heads), int(num_kv_heads), int(head_size),
+                  int(block_size), int(window), int(causal), int(kv_dtype),
+                  _scale_arg(kv_dtype, kv_scale), int(common_prefix_len), ctypes.byref(ext))
     if st != 0:
         raise PattnError(st, "pattn_cascade_fwd")
     forward.last_ext = ext
@@ -770,7 +764,8 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
         ws.used_on(raw_stream)
         st = _call_on(dev, run, *args)
     if st != 0:
-        need = pattn_workspace_bytes(ext, num_heads, num_kv_heads, head_size, block_size, lib=lib)
+        need = _call_on(dev, pattn_workspace_bytes, ext, num_heads, num_kv_heads, head_size,
+                        block_size, lib)
         if need == 0:
             raise PattnError(1, "pattn_workspace_bytes")
         if st == 3:

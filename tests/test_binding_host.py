@@ -76,3 +76,58 @@ def test_rotary_sizes_may_be_any_number(lib):
 def test_a_norm_eps_past_fp32_arrives_as_an_infinity(lib):
     # (which the library refuses, as it does a NaN)
     assert _rope(lib, norm_eps=1e300).norm_eps == float("inf")
+
+
+class _Stream:
+    cuda_stream = 0
+
+
+def _row_write(lib):
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    pa.reshape_and_cache(x, x, torch.zeros(2, 5, 16, 2, 64, dtype=torch.bfloat16),
+                         torch.zeros(3, dtype=torch.int64), block_size=16, stream=_Stream())
+
+
+def _diffkv_write(lib):
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    pa.reshape_and_cache_diffkv(x, x, torch.zeros(5, 16, 2, 128, dtype=torch.bfloat16),
+                                torch.zeros(3, dtype=torch.int64), block_size=16, stream=_Stream())
+
+
+def _cascade(lib):
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    pa.cascade_forward(q, torch.zeros(2, 5, 16, 2, 64, dtype=torch.bfloat16),
+                       torch.zeros(2, 3, dtype=torch.int32), torch.ones(2, dtype=torch.int32),
+                       torch.tensor([0, 1, 3], dtype=torch.int32), scale=1.0, num_heads=4,
+                       num_kv_heads=2, head_size=64, block_size=16, common_prefix_len=16,
+                       max_query_len=2, max_seq_len=40, workspace=pa.Workspace(), stream=_Stream())
+
+
+@pytest.mark.parametrize("call,names", [
+    (lambda lib: _forward(stream=_Stream()), ["pattn_workspace_bytes", "pattn_varlen_fwd"]),
+    (_cascade, ["pattn_cascade_workspace_bytes", "pattn_cascade_fwd"]),
+    (_row_write, ["pattn_reshape_and_cache"]),
+    (_diffkv_write, ["pattn_reshape_and_cache_diffkv"])],
+    ids=["forward", "cascade", "row write", "DiffKV write"])
+def test_every_call_runs_with_the_tensors_device_current(lib, monkeypatch, call, names):
+    """Launches, and the sizes that depend on the device's SM count."""
+    current, seen = [], []
+
+    def call_on(dev, fn, *args):
+        current.append(dev)
+        try:
+            return fn(*args)
+        finally:
+            current.pop()
+
+    def entry(name, status):
+        def run(*args):
+            seen.append((name, list(current)))
+            return status
+        return run
+
+    monkeypatch.setattr(pa, "_call_on", call_on)
+    for name in names:
+        setattr(lib, name, entry(name, NEED if name.endswith("_bytes") else 0))
+    call(lib)
+    assert seen == [(name, [torch.device("cpu")]) for name in names]
