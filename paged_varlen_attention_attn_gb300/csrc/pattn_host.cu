@@ -741,7 +741,8 @@ pattn_status_t pattn_cascade_fwd(const void* q, const void* kv_cache, const int3
   pre.bt_stride = ext->max_blocks_per_seq;
   pre.max_q = ext->num_tokens;
   pre.max_s = P;
-  pre.splits = c.splits_pre;
+  // (the layout holds the unbounded counts' partial results)
+  pre.splits = row_scaled_splits(c.splits_pre, ext->num_splits, kv_dtype, pre.max_s, 0);
   pre.hdr = hdr;
   pre.clear_status = 0;
   pre.long_queries = 1;
@@ -770,7 +771,7 @@ pattn_status_t pattn_cascade_fwd(const void* q, const void* kv_cache, const int3
   suf.bt_stride = ext->max_blocks_per_seq;
   suf.max_q = ext->max_query_len;
   suf.max_s = std::max(1, ext->max_seq_len - P);
-  suf.splits = c.splits_suf;
+  suf.splits = row_scaled_splits(c.splits_suf, ext->num_splits, kv_dtype, suf.max_s, 0);
   suf.hdr = hdr;
   suf.clear_status = 0;
   suf.tiles = reinterpret_cast<int2*>(ws + c.suf.tiles_off);
