@@ -433,7 +433,7 @@ def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *,
             pos_st = positions.stride(0)
             if pair_axis is None or len(pair_axis) != rot // 2:
                 raise ValueError("positions of several axes need pair_axis with rot_dim / 2 entries")
-            pairs = ctypes.c_char_p(bytes(pair_axis))
+            pairs = ctypes.c_char_p(bytes(list(pair_axis)))  # (not an array's own bytes)
             axes_at = ctypes.cast(pairs, ctypes.c_void_p).value
     qn_at = 0 if q_norm is None else _norm_at(q_norm, "q_norm", dt, dev, D)
     kn_at = 0 if k_norm is None else _norm_at(k_norm, "k_norm", dt, dev, D)

@@ -1,5 +1,8 @@
 """The binding's handling of its arguments, with a library that records its calls
 (no GPU)."""
+import ctypes
+
+import numpy as np
 import pytest
 import torch
 
@@ -131,3 +134,20 @@ def test_every_call_runs_with_the_tensors_device_current(lib, monkeypatch, call,
         setattr(lib, name, entry(name, NEED if name.endswith("_bytes") else 0))
     call(lib)
     assert seen == [(name, [torch.device("cpu")]) for name in names]
+
+
+@pytest.mark.parametrize("kind", [list, tuple, torch.tensor, np.array, lambda x: np.array(x, np.uint8),
+                                  lambda x: np.array(x, np.int32)])
+def test_pair_axis_may_be_any_sequence(lib, kind):
+    axes = [0] * 10 + [1] * 12 + [2] * 10
+    lib.pattn_rope_and_cache = lambda args: got.append(
+        ctypes.string_at(pa.RopeArgs.from_buffer_copy(args).pair_axis, 32)) or 0
+    got = []
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    pa.rope_and_cache(x, None, None, None, None, torch.zeros(3, 4, dtype=torch.int64),
+                      torch.zeros(8, 64), block_size=16, pair_axis=kind(axes))
+    assert got == [bytes(axes)]
+    for bad in ([0] * 31 + [-1], [0] * 31 + [256], [0] * 31):
+        with pytest.raises(ValueError):
+            pa.rope_and_cache(x, None, None, None, None, torch.zeros(3, 4, dtype=torch.int64),
+                              torch.zeros(8, 64), block_size=16, pair_axis=bad)
