@@ -378,6 +378,8 @@ def rope_and_cache(q, key, value, kv_cache, slot_mapping, positions, cos_sin, *,
     x = q if q is not None else key
     if x is None:
         raise ValueError("rope_and_cache needs q or key")
+    if (key is None and value is not None) or (q is None and q_out is not None):
+        raise ValueError("value goes with key and q_out with q")
     dt = torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
     dev = x.device
     q_at = qo_at = k_at = v_at = q_st = qo_st = k_st = v_st = 0

@@ -151,3 +151,12 @@ def test_pair_axis_may_be_any_sequence(lib, kind):
         with pytest.raises(ValueError):
             pa.rope_and_cache(x, None, None, None, None, torch.zeros(3, 4, dtype=torch.int64),
                               torch.zeros(8, 64), block_size=16, pair_axis=bad)
+
+
+@pytest.mark.parametrize("kw", [dict(key=None), dict(q=None, q_out=torch.zeros(4, 4, 64).bfloat16())])
+def test_half_a_rotary_call_is_refused(lib, kw):
+    # (as the C entry does: the value would not be written, the output not filled)
+    with pytest.raises(ValueError, match="goes with"):
+        _rope(lib, **kw)
+    assert _rope(lib, key=None, value=None).key is None
+    assert _rope(lib, q=None).q is None
