@@ -504,7 +504,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH, ROWS>::THREADS,
     const int key_base = (u_begin + i0) * UNIT;
     // Rows at or past seq_len may hold anything (NaN included): zero this
     // head's rows (only the partition's last unit can have any).
-    // (with row scales also those below the window, in its first unit.)
+    // (with row scales also those below the window, in its first unit: the one
+    // unit zeroed here is either only while a step takes a single unit.)
+    static_assert(!ROWS || U == 1, "a step's first unit is its last");
     if (key_base + nu * UNIT > s || (ROWS && key_base < kmin)) {
       const int u = nu - 1;
       unsigned char* sk = smem + ((i0 + u) % NST) * C::STAGE;
