@@ -1007,7 +1007,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
           const int key_base = (u0 + j) * BLOCK_N;
           const int n_load = min(pages_per_tile, (s - key_base + rows_box - 1) / rows_box);
           const int rows = NK ? min(n_load * rows_box, V_SPLIT) : n_load * rows_box;
-          if (kv == 0) {
+          // One copy of the widening serves both warps where it can: with one for
+          // K and one for V, each fetched anew (one scale per tensor, d 64, 4
+          // chunks of 2048 on 6144 keys, window 1000: 245 us against 221).
+          if constexpr (!ROWS) {
+            widen_e4m3_in_place<D>(ring + st * stage_bytes, 0, rows, lane);
+          } else if (kv == 0) {
             widen_e4m3_in_place<D>(ring + st * stage_bytes, 0, rows, lane);
           } else if (!widen_v(ring + st * stage_bytes, jt, key_base, 0, rows)) {
             ok = 0;
