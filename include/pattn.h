@@ -169,7 +169,9 @@ typedef struct {
  *                   power-of-two scaling, and V tiles are widened to f16
  *                   (exactly) for f16 P V MMAs; at 64 K and V are widened and
  *                   q is scaled per row into f16 (the decode kernel likewise
- *                   per head)
+ *                   per head).  With row scales a prefill V element is the f16
+ *                   product of its code and the row's scale rounded to f16 (2^-11
+ *                   each); the decode kernel puts the scales into the weights
  *   kv_scale        host float[2] {k_scale, v_scale}; required for e4m3, ignored
  *                   for bf16 (may be NULL).  For PATTN_KV_FP8_E4M3_ROW: the
  *                   [device] row scales (layout at PATTN_ROW_SCALE_MIN), 16-B
@@ -204,7 +206,8 @@ size_t pattn_workspace_bytes(const pattn_ext_t* ext, int num_heads, int num_kv_h
  * The decode KV partition count pattn_varlen_fwd will use for these sizes
  * (ext->num_splits if set, else the library's choice).  Over a
  * PATTN_KV_FP8_E4M3_ROW cache the library's own choice is bounded further, by
- * max(1, sqrt(visible keys / 16) - 1).  Partitions are runs of
+ * max(1, sqrt(visible keys / 16) - 1) (in pattn_decode_fwd_static and in each
+ * pass of pattn_cascade_fwd as well).  Partitions are runs of
  * ceil(n / splits) whole KV blocks over the n blocks a decode row can see,
  * merged by log-sum-exp ("RBLN Attention modes", flash attention; the Triton
  * backend's 16 parallel softmax segments).

@@ -145,7 +145,8 @@ pattn_status_t check_call(const void* q, const void* kv_cache, const int32_t* bl
 // gets about 85 % of HBM beside the prefill.  (A sweep of the prefill grid
 // on the mixed workload put the best at 128 of 152 SMs, which these figures
 // reproduce.)  The estimate only balances the two kernels; the result does
-// not depend on it.
+// not depend on it.  A row-scaled e4m3 cache is taken for a tensor-scaled one: its
+// longer tiles and its scales' bytes (4 to a row) are not in the estimate.
 void set_cost_model(Problem& p) {
   p.num_sms = current_sms();
   const bool fp8 = kv_is_e4m3(p.kv_dtype);

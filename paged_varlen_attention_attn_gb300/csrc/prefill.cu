@@ -60,7 +60,9 @@
 // never visited; tiles that straddle an edge are masked per element.  The
 // running max moves lazily: O is rescaled only when a row max grows by more
 // than 2^8, which stays exact because the final normalisation divides by the
-// sum taken against the same reference max.
+// sum taken against the same reference max.  (A row-scaled e4m3 cache's tiles
+// keep the reference until a row's weights sum to ROWS_SUM_LIMIT, near f16's
+// largest value.)
 #include <algorithm>
 
 #include "../../include/pattn.h"

@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(RC_THREADS)
 // token's q, k and v rows and table rows with untiled bulk copies (one for the
 // rows of a packed projection, q, k and v side by side), up to a ring of them
 // ahead.  The bytes in flight then depend on the ring, not on what the warps'
-// registers hold.  Eight consumer warps work in teams of one to eight, a team
-// per token: the smaller, the more rows share a warp's cos, sin and norm
+// registers hold.  Eight consumer warps work in teams of two, four or eight, a
+// team per token: the smaller, the more rows share a warp's cos, sin and norm
 // weights, the larger, the fewer stages the teams hold.
 // 8384 tokens, 64 q and 8 k and v heads of 128, row-scaled e4m3 cache: 56 us,
 // 87 % of the measured copy bandwidth (teams of 8 / 4 / 2 warps 62 / 56.5 / 56).
@@ -537,15 +537,16 @@ cudaError_t launch_kind(RopeParams& p, int sms, cudaStream_t st) {
   // streamed): 64 + 2 x 8 heads of 128, 608 tokens 7.2 / 6.7, 1216 14.4 / 13.9,
   // 8384 77 / 56; 32 + 2 x 8, 1824 tokens 13.2 / 14.5, 2432 17.1 / 16.7, 4864
   // 30.0 / 26.1; 16 + 2 x 2 of 128, 3000 tokens 11.0 / 11.7, 6000 21.0 / 19.3;
-  // of 64, 3000 tokens 8.0 / 9.8, 24000 53 / 58 (a copy's cost shows).  And the
-  // ring has to hold three tokens.
+  // of 64, 3000 tokens 8.0 / 9.8, 24000 53 / 58 (a copy's cost shows).  One count
+  // of bytes for all widths: it keeps 32 heads off the slower side and costs calls
+  // of 64 heads below it half a microsecond.  And the ring has to hold three tokens.
   if (stage >= RS_LEAST_STAGE && p.T * stage >= RS_LEAST_CALL && 3 * stage <= RS_RING_BYTES) {
     p.stage_bytes = static_cast<int>(stage);
     p.packed = p.H > 0 && p.Hkv > 0 && p.key == p.q + p.H * p.D && p.value == p.key + p.Hkv * p.D &&
                p.q_stride == p.k_stride && p.q_stride == p.v_stride;
     p.stages = static_cast<int>(std::min<long long>(RS_STAGES_MAX, RS_RING_BYTES / stage));
-    // the smallest team (one warp, two, ...) that leaves the producer as many
-    // stages as the teams hold
+    // the smallest team that leaves the producer as many stages as the teams hold
+    // (two warps at least: teams of one would need sixteen)
     p.team = RS_WARPS;
     while (p.team > 1 && 2 * (2 * RS_WARPS / p.team) <= p.stages) p.team /= 2;
     const int smem = RS_HEAD + p.stages * p.stage_bytes;
