@@ -560,6 +560,7 @@ def cascade_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scal
                   _scale_arg(kv_dtype, kv_scale), int(common_prefix_len), ctypes.byref(ext))
     if st != 0:
         raise PattnError(st, "pattn_cascade_fwd")
+    ext._workspace_keepalive = buf
     forward.last_ext = ext
     return out
 
@@ -777,5 +778,6 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
             st = _call_on(dev, run, *args)
     if check and st != 0:
         raise PattnError(st, "pattn_varlen_fwd")
+    ext._workspace_keepalive = buf  # (its status word may be read after a larger call)
     forward.last_ext = ext
     return out

@@ -1,6 +1,7 @@
 """The binding's handling of its arguments, with a library that records its calls
 (no GPU)."""
 import ctypes
+import weakref
 
 import numpy as np
 import pytest
@@ -160,3 +161,30 @@ def test_half_a_rotary_call_is_refused(lib, kw):
         _rope(lib, **kw)
     assert _rope(lib, key=None, value=None).key is None
     assert _rope(lib, q=None).q is None
+
+
+@pytest.mark.parametrize("cascade", [False, True])
+def test_a_calls_status_outlives_its_workspace(lib, cascade):
+    """pattn_read_device_status reads and clears a word of the call's own buffer,
+    also when a larger call has replaced it since."""
+    ws, need = pa.Workspace(), [NEED]
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    args = (q, torch.zeros(2, 5, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 3, dtype=torch.int32),
+            torch.ones(2, dtype=torch.int32), torch.tensor([0, 1, 3], dtype=torch.int32))
+    kw = dict(scale=1.0, num_heads=4, num_kv_heads=2, head_size=64, block_size=16, max_query_len=2,
+              max_seq_len=40, workspace=ws)
+    lib.pattn_workspace_bytes = lambda *args: need[0]
+    lib.pattn_varlen_fwd = lambda *args: 0 if args[-1].workspace_bytes >= need[0] else 3
+    lib.pattn_cascade_workspace_bytes = lambda *args: need[0]
+    lib.pattn_cascade_fwd = lambda *args: 0
+    if cascade:
+        pa.cascade_forward(*args, common_prefix_len=16, stream=_Stream(), **kw)
+    else:
+        pa.forward(*args, **kw)
+    ext, buf = pa.forward.last_ext, weakref.ref(ws.buf)
+    need[0] = 2 * NEED
+    pa.forward(*args, **kw)
+    assert ws.buf.numel() >= 2 * NEED and pa.forward.last_ext is not ext
+    assert buf() is not None and buf().data_ptr() == ext.workspace
+    del ext
+    assert buf() is None

@@ -38,6 +38,7 @@ def test_replay_after_the_default_workspace_has_grown(call, warm):
         call(args, kw, out)
     captured = pa.forward.last_ext
     at, size = captured.workspace, captured.workspace_bytes
+    del captured  # (it holds the buffer too)
     with torch.cuda.stream(s):
         big_out = torch.empty_like(big[0])
         call(big, big_kw, big_out)
