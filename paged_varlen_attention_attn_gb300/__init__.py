@@ -173,7 +173,7 @@ def _check_row_scales(scales, num_blocks, block_size, num_kv_heads, device):
     import torch
     if (not isinstance(scales, torch.Tensor) or scales.dtype != torch.float32 or
             scales.device != device or not scales.is_contiguous() or
-            scales.numel() != num_blocks * block_size * num_kv_heads * 2):
+            scales.shape != row_scales_shape(num_blocks, block_size, num_kv_heads)):
         raise ValueError("kv_scale of a KV_FP8_E4M3_ROW cache must be a contiguous fp32 tensor of "
                          "shape row_scales_shape(...) on the cache's device")
 

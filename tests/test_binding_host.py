@@ -188,3 +188,23 @@ def test_a_calls_status_outlives_its_workspace(lib, cascade):
     assert buf() is not None and buf().data_ptr() == ext.workspace
     del ext
     assert buf() is None
+
+
+@pytest.mark.parametrize("shape", [(2, 16, 2, 2), (2, 2, 1, 2, 16), (2, 1, 2, 16, 2), (128,)])
+def test_row_scales_of_another_layout_are_refused(lib, shape):
+    """As many numbers, but not where the kernels read them."""
+    assert torch.Size(shape).numel() == torch.Size(pa.row_scales_shape(2, 16, 2)).numel()
+    scales = torch.ones(shape)
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    cache = torch.zeros(2, 2, 16, 2, 64, dtype=torch.uint8)
+    row = dict(block_size=16, kv_dtype=pa.KV_FP8_E4M3_ROW, kv_scale=scales)
+    slots, bt = torch.arange(3), torch.zeros(1, 2, dtype=torch.int32)
+    qsl, sl = torch.tensor([0, 3], dtype=torch.int32), torch.tensor([3], dtype=torch.int32)
+    att = dict(scale=1.0, num_heads=2, num_kv_heads=2, head_size=64, max_query_len=3, max_seq_len=32, **row)
+    for call in (lambda: pa.reshape_and_cache(x, x, cache, slots, **row),
+                 lambda: pa.rope_and_cache(x, x, x, cache, slots, None, None, **row),
+                 lambda: pa.gather_cache(cache, bt, qsl, num_rows=3, **row),
+                 lambda: pa.forward(x, cache, bt, sl, qsl, **att),
+                 lambda: pa.cascade_forward(x, cache, bt, sl, qsl, common_prefix_len=16, **att)):
+        with pytest.raises(ValueError, match="row_scales_shape"):
+            call()
