@@ -690,9 +690,10 @@ def _workspace(workspace, dev, raw_stream):
     if workspace is not None:
         return workspace
     key = (dev.index, raw_stream, threading.get_ident())
-    if key not in _default_ws:
-        _default_ws[key] = Workspace()
-    return _default_ws[key]
+    ws = _default_ws.get(key)
+    if ws is None:
+        ws = _default_ws[key] = Workspace()
+    return ws
 
 
 def release_workspaces():

@@ -59,3 +59,11 @@ def test_default_workspaces_can_be_released():
     assert buf() is not None
     pa.release_workspaces()
     assert buf() is None
+
+
+def test_a_release_by_another_thread_disturbs_no_call(monkeypatch):
+    class Released(dict):
+        def __contains__(self, key):  # it is there, and gone at the next look
+            return True
+    monkeypatch.setattr(pa, "_default_ws", Released())
+    assert isinstance(pa._workspace(None, torch.device("cuda", 0), 4096), pa.Workspace)
