@@ -492,6 +492,178 @@ pattn_status_t pattn_gather_cache(const void* kv_cache, const int32_t* block_tab
                                   int head_size, int block_size, int kv_dtype,
                                   const float* kv_scale, unsigned* device_status, void* stream);
 
+/*
+ * Attention with keys and values from one shared latent vector a token.
+ *
+ * A model of this kind caches, per token, one row that all heads share: a latent
+ * vector c (latent_size elements) and a rotary key k (rope_size elements).  The
+ * cache is [num_blocks, block_size, latent_size + rope_size], 16-bit
+ * (PATTN_KV_BF16 or PATTN_KV_F16; q, out and the other tensors are of its type),
+ * addressed by block table and slot mapping like the caches above.  The
+ * attention has two forms.  Absorbed: the up-projection of the keys is folded
+ * into q and that of the values into what follows, so every head attends the
+ * cached rows themselves (pattn_latent_fwd; single tokens and short chunks).
+ * Expanded: keys and values are projected up to a pair per head and attended
+ * densely (pattn_latent_expanded_fwd; prompts).  ("[vLLM] other attention
+ * backends" and "RBLN Attention modes" name this attention and its latent cache;
+ * they give no layout, this is the reading taken.)
+ *
+ * Sizes of every entry point below: latent_size a multiple of 128 up to 512,
+ * rope_size a multiple of 16 up to 64, block_size a multiple of 16.  As the
+ * product p . V defines it, a weight of 0 times an infinity or a NaN is NaN: a
+ * non-finite value of a key that the causal mask hides can reach rows of its
+ * request.  Keys at or past seq_len and other requests' keys never do.
+ */
+
+/*
+ * pattn_latent_rope_and_cache -- the cache write of a step's tokens, in one
+ * kernel: for token t the latent is normed if a weight is given,
+ *   c <- c * w / sqrt(mean(c^2) + norm_eps),
+ * the rotary key and the rotary part of every q head are turned pair by pair,
+ *   (a, b) -> (a cos - b sin, b cos + a sin),  cos = cos_sin[positions[t]][i],
+ *   sin = cos_sin[positions[t]][rope_size / 2 + i] for pair i,
+ * and c and the key become the cache row of slot_mapping[t].  fp32 with one
+ * rounding at the end.
+ */
+typedef struct {
+  size_t struct_size;     /* sizeof(pattn_latent_rope_t)                      */
+  const void* q;          /* [device] rotary parts of q: head h of token t at
+                             q + t * q_stride + h * q_head_stride, rope_size
+                             elements; NULL: the cache row only               */
+  void* q_out;            /* [device] likewise; may be q with the same strides,
+                             else must not overlap it                         */
+  const void* latent;     /* [device] token t's at latent + t * latent_stride */
+  const void* k_rope;     /* [device] token t's at k_rope + t * k_rope_stride */
+  void* row_out;          /* [device] optional: the written row densely as well,
+                             token t's at row_out + t * row_out_stride (latent,
+                             then key); may be the rows that latent and k_rope
+                             are the parts of                                 */
+  long long q_stride, q_head_stride, q_out_stride, q_out_head_stride, latent_stride,
+      k_rope_stride, row_out_stride; /* elements, multiples of 8; all buffers 16-B
+                             aligned                                          */
+  const void* latent_norm; /* [device] [latent_size] weight, or NULL          */
+  const float* cos_sin;   /* [device] fp32 [max_position][rope_size], 16-B aligned */
+  const int64_t* positions; /* [device] [num_tokens], or NULL for no rotation.  A
+                             negative one marks padding: nothing of the token
+                             is written                                       */
+  void* kv_cache;         /* [device] the cache, updated                      */
+  const int64_t* slot_mapping; /* [device] [num_tokens]; negative: no cache row.
+                             Slots must be distinct                           */
+  unsigned* device_status; /* [device] optional: a slot past the pool (no row is
+                             written) and a position outside the table (nothing
+                             of the token is) OR bit 1 into it                */
+  void* stream;           /* cudaStream_t; NULL = the legacy default stream   */
+  float norm_eps;         /* finite, >= 0                                     */
+  int num_tokens;
+  int num_heads;
+  int latent_size;
+  int rope_size;
+  int interleaved;        /* 0: pair i is elements (i, i + rope_size / 2);
+                             1: elements (2 i, 2 i + 1)                       */
+  int max_position;       /* rows of cos_sin                                  */
+  int kv_dtype;
+  int block_size;
+  int num_blocks;
+} pattn_latent_rope_t;
+
+/* Returns PATTN_OK once enqueued; argument errors before any CUDA call;
+ * PATTN_ERR_CUDA if the launch fails.  Allocates nothing, never synchronises. */
+pattn_status_t pattn_latent_rope_and_cache(const pattn_latent_rope_t* args);
+
+/*
+ * pattn_gather_latent -- pattn_gather_cache for a cache of latent rows: request
+ * r's keys key_starts[r] (NULL: 0), ... into rows [out_start_loc[r],
+ * out_start_loc[r + 1]) of latent_out [num_rows, latent_size] and rope_out
+ * [num_rows, rope_size] (what an up-projection and the expanded form take).  Rows
+ * outside are left as they are; a key outside its block-table row or a block id
+ * outside the pool zeroes the row and ORs bit 1 into device_status (may be NULL).
+ */
+pattn_status_t pattn_gather_latent(const void* kv_cache, const int32_t* block_table,
+                                   const int32_t* key_starts, const int32_t* out_start_loc,
+                                   void* latent_out, void* rope_out, int num_seqs, int num_rows,
+                                   int max_blocks_per_seq, int num_blocks, int latent_size,
+                                   int rope_size, int block_size, int kv_dtype,
+                                   unsigned* device_status, void* stream);
+
+/*
+ * pattn_latent_fwd -- the absorbed form over the paged cache.
+ *
+ *   out[t][h] = softmax over visible keys k of (scale * q[t][h] . [c_k | key_k]) . c
+ *
+ * with the requests, block table, lengths, causal mask, metadata checks and
+ * status word of pattn_varlen_fwd (row i of request r at position seq_len -
+ * q_len + i).  A request's cached rows are read once for all its rows' heads up
+ * to 64 (row, head) pairs; the keys are cut into equal shares over the GPU, and
+ * requests that several shares touch are merged by log-sum-exp in a fixed order.
+ */
+typedef struct {
+  size_t struct_size;     /* sizeof(pattn_latent_t)                           */
+  const void* q;          /* [device] [num_tokens][num_heads][latent_size +
+                             rope_size], contiguous, 16-B aligned             */
+  const void* kv_cache;   /* [device] 16-B aligned                            */
+  void* out;              /* [device] [num_tokens][num_heads][latent_size], rows
+                             outside the requests are left untouched          */
+  const int32_t* block_table;     /* [device] [num_seqs][max_blocks_per_seq]  */
+  const int32_t* seq_lens;        /* [device] [num_seqs]                      */
+  const int32_t* query_start_loc; /* [device] [num_seqs + 1]                  */
+  void* workspace;        /* [device] 256-B aligned; its status word is read with
+                             pattn_read_device_status                         */
+  size_t workspace_bytes; /* >= pattn_latent_workspace_bytes                  */
+  void* stream;
+  float scale;            /* finite, >= 0                                     */
+  int causal;             /* 1: k <= position; 0: every key < seq_len         */
+  int kv_dtype;
+  int num_seqs, num_tokens, num_heads, latent_size, rope_size, block_size;
+  int max_blocks_per_seq, num_blocks;
+  int max_query_len;      /* >= every q_len                                   */
+} pattn_latent_t;
+
+pattn_status_t pattn_latent_fwd(const pattn_latent_t* args);
+
+/* Workspace bytes pattn_latent_fwd needs (0 if the arguments are invalid). */
+size_t pattn_latent_workspace_bytes(int num_seqs, int num_heads, int latent_size);
+
+/*
+ * pattn_latent_expanded_fwd -- the expanded form over contiguous ragged rows.
+ *
+ *   out[t][h] = softmax over visible keys k of
+ *               scale * (q[t][h][:nope] . k_nope[k][h] + q[t][h][nope:] . k_rope[k])
+ *               . value[k][h]
+ *
+ * Request r has q rows [query_start_loc[r], query_start_loc[r + 1]) and keys
+ * [key_start_loc[r], key_start_loc[r + 1]); with causal its i-th row sees its
+ * first keys - queries + i + 1 keys.  A request with causal and more rows than
+ * keys, or rows or keys outside the tensors, is reported as bad metadata and its
+ * rows are zeroed; a request without keys has rows of zeros.
+ */
+typedef struct {
+  size_t struct_size;     /* sizeof(pattn_latent_expanded_t)                  */
+  const void* q;          /* [device] head h of token t at q + t * q_stride +
+                             h * q_head_stride: nope_size + rope_size elements */
+  const void* k_nope;     /* [device] likewise, nope_size elements            */
+  const void* k_rope;     /* [device] key k's at k_rope + k * k_rope_stride   */
+  const void* value;      /* [device] as k_nope, value_size elements          */
+  void* out;              /* [device] [num_tokens][num_heads][value_size]     */
+  long long q_stride, q_head_stride, k_stride, k_head_stride, k_rope_stride, v_stride,
+      v_head_stride;      /* elements, positive multiples of 8; buffers 16-B aligned */
+  const int32_t* query_start_loc; /* [device] [num_seqs + 1], non-decreasing  */
+  const int32_t* key_start_loc;   /* [device] [num_seqs + 1], non-decreasing  */
+  void* workspace;        /* as in pattn_latent_t                             */
+  size_t workspace_bytes; /* >= pattn_latent_expanded_workspace_bytes         */
+  void* stream;
+  float scale;
+  int causal;
+  int kv_dtype;
+  int num_seqs, num_tokens, num_keys, num_heads;
+  int nope_size, rope_size, value_size; /* 64 or 128, the same for value; rope_size
+                             a multiple of 16 up to 64                        */
+} pattn_latent_expanded_t;
+
+pattn_status_t pattn_latent_expanded_fwd(const pattn_latent_expanded_t* args);
+
+/* Workspace bytes pattn_latent_expanded_fwd needs (0 if the arguments are invalid). */
+size_t pattn_latent_expanded_workspace_bytes(int num_seqs, int num_tokens);
+
 /* A static, human-readable name for a status code. */
 const char* pattn_status_string(int status);
 

@@ -37,7 +37,9 @@ EXPORTS = ("pattn_varlen_fwd", "pattn_workspace_bytes", "pattn_decode_splits",
            "pattn_decode_fwd_static", "pattn_reshape_and_cache",
            "pattn_reshape_and_cache_diffkv", "pattn_cascade_fwd",
            "pattn_cascade_workspace_bytes", "pattn_reshape_and_cache_rows",
-           "pattn_rope_and_cache", "pattn_gather_cache")
+           "pattn_rope_and_cache", "pattn_gather_cache", "pattn_latent_rope_and_cache",
+           "pattn_gather_latent", "pattn_latent_fwd", "pattn_latent_workspace_bytes",
+           "pattn_latent_expanded_fwd", "pattn_latent_expanded_workspace_bytes")
 STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -148,6 +150,18 @@ def load(path=None):
     lib.pattn_rope_and_cache.argtypes = [vp]  # a RopeArgs by reference, or its bytes
     lib.pattn_gather_cache.restype = i
     lib.pattn_gather_cache.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp, vp]
+    lib.pattn_latent_rope_and_cache.restype = i
+    lib.pattn_latent_rope_and_cache.argtypes = [vp]  # each struct by reference, or its bytes
+    lib.pattn_gather_latent.restype = i
+    lib.pattn_gather_latent.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, vp, vp]
+    lib.pattn_latent_fwd.restype = i
+    lib.pattn_latent_fwd.argtypes = [vp]
+    lib.pattn_latent_workspace_bytes.restype = ctypes.c_size_t
+    lib.pattn_latent_workspace_bytes.argtypes = [i, i, i]
+    lib.pattn_latent_expanded_fwd.restype = i
+    lib.pattn_latent_expanded_fwd.argtypes = [vp]
+    lib.pattn_latent_expanded_workspace_bytes.restype = ctypes.c_size_t
+    lib.pattn_latent_expanded_workspace_bytes.argtypes = [i, i]
     if path is None:
         _lib = lib
     return lib
@@ -782,3 +796,7 @@ def forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, num_h
     ext._workspace_keepalive = buf  # (its status word may be read after a larger call)
     forward.last_ext = ext
     return out
+
+
+from .latent import (LatentArgs, LatentExpandedArgs, LatentRopeArgs, gather_latent,  # noqa: E402
+                     latent_expanded_forward, latent_forward, latent_rope_and_cache)

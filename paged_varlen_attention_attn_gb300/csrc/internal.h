@@ -207,6 +207,15 @@ cudaError_t launch_cascade_merge(const float* o_a, const float* lse_a, int chunk
                                  int B, int T, int H, int D, bool half, const float* sinks,
                                  cudaStream_t stream);
 
+// TMA tensor map over 16-bit rows [rows][heads][dim] of any head and row stride
+// (elements, multiples of 8); a box is box_rows rows of one head, 64 elements wide,
+// in the 128-byte-swizzled layout (past the row, the heads or the rows: zeros).
+bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int heads, int rows,
+                     long long head_stride, long long row_stride, int box_rows);
+
+// Checks the sizes and the type of a cache of latent rows (host only).
+pattn_status_t check_latent_sizes(int latent_size, int rope_size, int block_size, int kv_dtype);
+
 // Query rows one prefill CTA covers: two heads x 128 rows when the GQA group
 // size is even, else one head x 256 rows.
 int prefill_rows_per_item(int G);
