@@ -213,6 +213,13 @@ cudaError_t launch_cascade_merge(const float* o_a, const float* lse_a, int chunk
 bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int heads, int rows,
                      long long head_stride, long long row_stride, int box_rows);
 
+// TMA tensor maps over a cache of latent rows [rows][latent + rope] (rows a multiple
+// of 8): the latents as {64, row of 8, 64-element block, 8 rows}, a box all blocks of
+// box_rows rows, which lands as [8 rows][block][8 x 128 bytes]; the rotary parts as
+// {rope, row of 8, 8 rows}, widened to 64 elements with zeros.  128-byte swizzle.
+bool encode_latent_maps(CUtensorMap* latent_map, CUtensorMap* rope_map, const void* cache, bool half,
+                        int latent, int rope, int rows, int box_rows);
+
 // Checks the sizes and the type of a cache of latent rows (host only).
 pattn_status_t check_latent_sizes(int latent_size, int rope_size, int block_size, int kv_dtype);
 

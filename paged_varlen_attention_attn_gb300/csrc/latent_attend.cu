@@ -10,14 +10,21 @@
 // 512 the balance of HBM and tensor cores is near 128 heads.  A CTA holds R = 16,
 // 32 or 64 rows and walks tiles of 64 keys.  One copy of a tile in shared memory
 // feeds both MMAs of tcgen05:
-//   S (64 x 64) = Q K^T, M the rows, K-major from the tile's 64-element column
-//     blocks; M = 64 leaves S's rows on the first 16 lanes of each warp;
-//   O^T (128 dims x R, dc / 128 of them) += V^T P^T, M the dims (the same blocks
+//   S (64 x 64) = Q K^T, M the rows, K-major; M = 64 leaves S's rows on the first
+//     16 lanes of each warp;
+//   O^T (128 dims x R, dc / 128 of them) += V^T P^T, M the dims (the same bytes
 //     read MN-major), N the rows.  O transposed keeps all 128 lanes busy for any R
 //     and takes dc / 128 * R <= 256 TMEM columns (O itself would take all 512).
-// P goes through shared memory as the B operand.  The tile's blocks form a ring of
-// 16 KB pairs of blocks: S consumes them in order, P V frees them in order, so the
-// next tile's copies go out block by block.
+// P goes through shared memory as the B operand.
+//
+// An MMA costs the thread that issues it about 46 cycles however small it is, so S
+// (36 of them for 576 dims, whatever the keys of a tile) wants the largest tile
+// that leaves two in flight beside Q: with tiles of 32 keys and five in the ring a
+// pass over 8 x 125 k keys took 446 us.
+//
+// A tile lies as [8 keys][64-element column block][8 x 128 bytes], so that the rows
+// of a page land with one copy whatever the block size: a copy holds its warp for
+// some 200 ns.  The rotary parts come through a map of their own, from another warp.
 //
 // Work: the batch's (row tile, key tile) grid, row tile after row tile, is cut into
 // equal shares, one per CTA (fewer where a share would be below LEAST_SHARE
@@ -26,7 +33,8 @@
 // single tokens with more than 64 heads, the CTAs of a share work side by side
 // on the row tiles of one token, so HBM is read once for all of them.
 //
-// Six warps: 0-3 softmax and epilogue, 4 TMA, 5 MMA issue.
+// Eight warps: 0-3 softmax and epilogue, 4 TMA of the latents, 5 and 7 issue the MMAs
+// of S and of P V, 6 TMA of Q and the rotary parts.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -38,9 +46,10 @@
 namespace pattn {
 namespace {
 
-constexpr int LA_THREADS = 192;
+constexpr int LA_THREADS = 256;
 constexpr int LA_KEYS = 64;           // keys of a tile
-constexpr int LA_BLK = LA_KEYS * 128; // bytes of a 64-element column block of a tile
+constexpr int LA_ROT = LA_KEYS * 128; // bytes of a tile's rotary parts
+constexpr int LA_LAT = 8 * LA_ROT;    // and of its latents (dc = 512)
 constexpr int PAD = 2;                // a row tile's fixed cost, in key tiles
 constexpr int LEAST_SHARE = 3;        // cost of a CTA's share, in key tiles
 constexpr float LA_RESCALE_LOG2 = 8.f;
@@ -69,7 +78,7 @@ struct LaProblem {
   Cut* cuts;        // [shares + 1]
   float* part_o;    // [grid][2][R][dc]: what a CTA's first and last row tile leave
   float2* part_ml;  // [grid][2][R]: their max (log2 units) and sum
-  double* prefix;   // [B + 1] cost of the requests before
+  float* prefix;    // [B] cost of the requests before (large batches)
   float sl2;
   int B, T, H, dc, dr, bs, mbps, NB, causal, half;
   int R;            // rows of a row tile
@@ -114,64 +123,69 @@ __device__ __forceinline__ int la_key_tiles(const LaProblem& p, int q, int s, in
 // with the position.  (An estimate where rows and tiles do not divide; it only
 // says where the shares are cut.)
 struct Cost {
-  double a, b;
+  float a, b;
   int n;  // row tiles
-  __device__ double upto(double x) const { return x * (a + 0.5 * b * x); }
+  __device__ float upto(float x) const { return x * (a + 0.5f * b * x); }
 };
-__device__ __forceinline__ Cost la_cost(const LaProblem& p, int r) {
-  int t0, q, s;
-  la_request(p, r, t0, q, s);
+__device__ __forceinline__ Cost la_cost(const LaProblem& p, int q, int s) {
   Cost c;
   c.n = la_row_tiles(p, q);
-  c.a = la_key_tiles(p, q, s, 0) + PAD;
-  c.b = c.n > 1 ? static_cast<double>(la_key_tiles(p, q, s, c.n - 1) + PAD - c.a) / (c.n - 1) : 0.;
-  c.a -= 0.5 * c.b;  // (so that n row tiles cost their sum)
+  c.a = static_cast<float>(la_key_tiles(p, q, s, 0) + PAD);
+  c.b = 0.f;
+  if (c.n > 1) {
+    c.b = (static_cast<float>(la_key_tiles(p, q, s, c.n - 1) + PAD) - c.a) / static_cast<float>(c.n - 1);
+    c.a -= 0.5f * c.b;  // (so that n row tiles cost their sum)
+  }
   return c;
 }
 
 // ------------------------------------------------------------------- plan
 
 constexpr int LA_PLAN_THREADS = 1024;
+constexpr int LA_PLAN_BATCH = 4096;  // requests whose costs fit shared memory
 
+// (fp32: the sums say where the shares are cut, and a share is at least LEAST_SHARE
+// tiles, far above a rounding of its border)
 __global__ void __launch_bounds__(LA_PLAN_THREADS)
     latent_plan_kernel(const __grid_constant__ LaProblem p) {
-  __shared__ double warp_sums[32];
-  __shared__ double carry;
+  __shared__ float warp_sums[32];
+  __shared__ float s_prefix[LA_PLAN_BATCH];
   __shared__ unsigned bad;
   grid_dep_trigger();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  if (tid == 0) {
-    carry = 0.;
-    bad = 0u;
-  }
-  __syncthreads();
+  float* prefix = p.B <= LA_PLAN_BATCH ? s_prefix : p.prefix;
+  if (tid == 0) bad = 0u;
+  float total = 0.f;
   for (int base = 0; base < p.B; base += LA_PLAN_THREADS) {
+    __syncthreads();
     const int r = base + tid;
-    double x = 0.;
+    float x = 0.f;
     if (r < p.B) {
       int t0, q, s;
       if (!la_request(p, r, t0, q, s)) bad = PATTN_DEV_BAD_METADATA;
-      const Cost c = la_cost(p, r);
-      x = c.upto(c.n);
+      const Cost c = la_cost(p, q, s);
+      x = c.upto(static_cast<float>(c.n));
     }
-    double incl = x;
+    float incl = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(FULL, incl, o);
+      const float y = __shfl_up_sync(FULL, incl, o);
       if (lane >= o) incl += y;
     }
     if (lane == 31) warp_sums[wid] = incl;
     __syncthreads();
-    double before = carry;
-    for (int w = 0; w < wid; ++w) before += warp_sums[w];
-    if (r < p.B) p.prefix[r] = before + incl - x;
-    __syncthreads();
-    if (tid == LA_PLAN_THREADS - 1) carry = before + incl;
-    __syncthreads();
+    // (every warp sums the warps before it in the same order)
+    float before = lane < wid ? warp_sums[lane] : 0.f, all = warp_sums[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(FULL, before, o);
+      all += __shfl_xor_sync(FULL, all, o);
+    }
+    if (r < p.B) prefix[r] = total + before + incl - x;
+    total += all;
   }
-  const double total = carry;
-  const int shares =
-      max(1, min(p.max_shares, static_cast<int>(min(total / LEAST_SHARE, 1e6))));
+  __syncthreads();
+  const int shares = max(1, min(p.max_shares, static_cast<int>(fminf(total / LEAST_SHARE, 1e6f))));
   if (tid == 0) {
     p.hdr->status = bad;
     p.hdr->shares = shares;
@@ -179,22 +193,22 @@ __global__ void __launch_bounds__(LA_PLAN_THREADS)
   for (int c = tid; c <= shares; c += LA_PLAN_THREADS) {
     Cut cut = {c == shares ? p.B : 0, 0, 0, 0};
     if (c > 0 && c < shares) {
-      const double w = total * c / shares;
+      const float w = total * static_cast<float>(c) / static_cast<float>(shares);
       int lo = 0, hi = p.B;  // the last request that costs begin at or before w
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.prefix[mid] <= w) lo = mid;
+        if (prefix[mid] <= w) lo = mid;
         else hi = mid;
       }
-      const Cost k = la_cost(p, lo);
-      const double v = w - p.prefix[lo];
-      const double x = 2. * v / (k.a + sqrt(fmax(0., k.a * k.a + 2. * k.b * v)));
       int t0, q, s;
       la_request(p, lo, t0, q, s);
+      const Cost k = la_cost(p, q, s);
+      const float v = fmaxf(0.f, w - prefix[lo]);
+      const float x = 2.f * v / (k.a + sqrtf(fmaxf(0.f, k.a * k.a + 2.f * k.b * v)));
       cut.r = lo;
       cut.j = min(static_cast<int>(x), max(0, k.n - 1));
       const int nk = la_key_tiles(p, q, s, cut.j);
-      cut.t = static_cast<int>((x - cut.j) * (nk + PAD));
+      cut.t = static_cast<int>((x - static_cast<float>(cut.j)) * static_cast<float>(nk + PAD));
       if (k.n == 0 || cut.t >= nk) {  // behind the row tile's keys: the next one begins
         cut.t = 0;
         if (++cut.j >= k.n) {
@@ -261,22 +275,21 @@ __device__ __forceinline__ bool la_next(const LaProblem& p, Walk& w, int lane, S
 template <int R>
 struct LaCfg {
   static constexpr int QBLK = R * 128;         // a 64-element column block of Q
-  static constexpr int ND = R == 64 ? 8 : R == 32 ? 10 : 11;  // pairs of blocks in the ring
-  static constexpr int NR = R == 64 ? 2 : 3;   // rotary blocks
+  static constexpr int NST = 2;                // tiles in the ring
+  static constexpr int STAGE = LA_LAT + LA_ROT;
   static constexpr int Q_OFF = 0;
   static constexpr int P_OFF = Q_OFF + 9 * QBLK;
-  static constexpr int D_OFF = P_OFF + R * 128;
-  static constexpr int R_OFF = D_OFF + ND * 2 * LA_BLK;
-  static constexpr int BAR_OFF = R_OFF + NR * LA_BLK;
+  static constexpr int K_OFF = P_OFF + R * 128;
+  static constexpr int BAR_OFF = K_OFF + NST * STAGE;
   static constexpr int SMEM = BAR_OFF + 1024 + 1024;
   static_assert(SMEM <= 232448, "a CTA's shared memory");
-  static_assert(P_OFF % 1024 == 0 && D_OFF % 1024 == 0, "swizzled blocks are 1024-byte aligned");
+  static_assert(P_OFF % 1024 == 0 && K_OFF % 1024 == 0, "swizzled blocks are 1024-byte aligned");
   static constexpr unsigned S_COL = 256;       // two score buffers of 64 columns
 };
 
 struct LaBars {
-  uint64_t d_full[11], d_empty[11], r_full[3], r_empty[3];
-  uint64_t q_full, q_empty, s_full[2], p_full, pv_done, drain;
+  uint64_t k_full[2], k_empty[2];
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, drain[2];
   float alpha[64], l[64];
   unsigned tmem_base;
   int abort_flag;
@@ -329,7 +342,8 @@ __device__ __forceinline__ bool any_of_128(bool ask) {
 template <int R, bool HALF>
 __global__ void __launch_bounds__(LA_THREADS, 1)
     latent_kernel(const __grid_constant__ LaProblem p, const __grid_constant__ CUtensorMap qmap,
-                  const __grid_constant__ CUtensorMap cmap) {
+                  const __grid_constant__ CUtensorMap cmap,
+                  const __grid_constant__ CUtensorMap rmap) {
   using C = LaCfg<R>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -340,25 +354,24 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   grid_dep_trigger();
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::ND; ++i) {
-      mbar_init(&bars->d_full[i], 1);
-      mbar_init(&bars->d_empty[i], 1);
-    }
-    for (int i = 0; i < C::NR; ++i) {
-      mbar_init(&bars->r_full[i], 1);
-      mbar_init(&bars->r_empty[i], 1);
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(&bars->k_full[i], 2);  // the latents' and the rotary parts' bytes
+      mbar_init(&bars->k_empty[i], 1);
     }
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
-    mbar_init(&bars->s_full[0], 1);
-    mbar_init(&bars->s_full[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->s_empty[i], 4);  // read by a softmax warp
+      mbar_init(&bars->drain[i], 1);
+    }
     mbar_init(&bars->p_full, 128);
     mbar_init(&bars->pv_done, 1);
-    mbar_init(&bars->drain, 1);
     bars->abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&cmap);
+    tma_prefetch_desc(&rmap);
   }
   if (warp == 0) {
     tmem_alloc(&bars->tmem_base, 512);
@@ -375,39 +388,44 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   const bool works = share < p.hdr->shares;
   unsigned char* sQ = smem + C::Q_OFF;
   unsigned char* sP = smem + C::P_OFF;
-  unsigned char* sD = smem + C::D_OFF;
-  unsigned char* sR = smem + C::R_OFF;
-  const int nd = p.dc / 128;  // pairs of blocks of a tile
+  unsigned char* sK = smem + C::K_OFF;
+  const int nc = p.dc / 64;  // column blocks of the latents
+  const int nd = p.dc / 128;
 
   if (!works) {
-  } else if (warp == 4) {
+  } else if (warp == 4 || warp == 6) {
     // ---------------------------------------------------------------- TMA
-    // Lane 0 waits for a ring slot and posts its bytes; the copies, one per page
-    // and column block, go out from one lane each.
+    // Warp 4 copies the latents of a tile's pages, warp 6 their rotary parts and Q.
+    // Lane 0 waits for a ring slot and posts its bytes; the copies go out from one
+    // lane each.
+    const bool rot = warp == 6;
     Walk w = la_walk(p, share);
     Seg g;
-    int dpos = 0, rpos = 0, n_seg = 0, ok = 1;
-    const int ppt = LA_KEYS / p.box;  // copies of a block
-    const int my_pg = lane % ppt, my_col = lane / ppt;
+    int pos = 0, n_seg = 0, ok = 1;
+    const int ppt = LA_KEYS / p.box;  // copies of a tile
+    const int page_bytes = rot ? p.box * 128 : p.box * 2 * p.dc;
     while (ok && la_next(p, w, side, g)) {
       if (g.s == 0) continue;
-      if (lane == 0) {
-        if (n_seg > 0 && !mbar_wait(&bars->q_empty, (n_seg - 1) & 1, status, abort_flag)) {
-          ok = 0;
-        } else {
-          mbar_arrive_expect_tx(&bars->q_full, static_cast<unsigned>((2 * nd + 1) * C::QBLK));
-          for (int c = 0; c <= 2 * nd; ++c)
-            tma_load_3d(sQ + c * C::QBLK, &qmap, &bars->q_full, c * 64, 0, static_cast<int>(g.row0));
+      if (rot) {
+        if (lane == 0) {
+          if (n_seg > 0 && !mbar_wait(&bars->q_empty, (n_seg - 1) & 1, status, abort_flag)) {
+            ok = 0;
+          } else {
+            mbar_arrive_expect_tx(&bars->q_full, static_cast<unsigned>((nc + 1) * C::QBLK));
+            for (int c = 0; c <= nc; ++c)
+              tma_load_3d(sQ + c * C::QBLK, &qmap, &bars->q_full, c * 64, 0,
+                          static_cast<int>(g.row0));
+          }
         }
+        ok = __shfl_sync(FULL, ok, 0);
+        if (!ok) break;
+        ++n_seg;
       }
-      ok = __shfl_sync(FULL, ok, 0);
-      if (!ok) break;
-      ++n_seg;
       const int* bt = p.block_table + static_cast<int64_t>(g.r) * p.mbps;
-      // the pool row that page `my_pg` of key tile kt begins at
+      // the pool row that page `lane` of key tile kt begins at
       auto page_row = [&](int kt) {
-        const int key = kt * LA_KEYS + my_pg * p.box;
-        if (kt >= g.k1 || key >= g.s) return 0;
+        const int key = kt * LA_KEYS + lane * p.box;
+        if (lane >= ppt || kt >= g.k1 || key >= g.s) return 0;
         int blk = bt[key / p.bs];
         if (blk < 0 || blk >= p.NB) {
           flag_status(status, PATTN_DEV_BAD_METADATA);
@@ -416,117 +434,118 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         return blk * p.bs + key % p.bs;
       };
       int row_next = page_row(g.k0);
-      for (int kt = g.k0; ok && kt < g.k1; ++kt) {
-        const int row = row_next;
+      for (int kt = g.k0; kt < g.k1; ++kt, ++pos) {
+        const int row = row_next, st = pos % C::NST;
         row_next = page_row(kt + 1);
         const int pages = min(ppt, (g.s - kt * LA_KEYS + p.box - 1) / p.box);
-        const unsigned bytes = static_cast<unsigned>(pages * p.box * 128);
-        for (int d = 0; d <= nd; ++d) {
-          const bool rot = d == nd;  // the rotary block comes last
-          const int pos = rot ? rpos++ : dpos++, n = rot ? C::NR : C::ND, st = pos % n;
-          uint64_t* full = rot ? &bars->r_full[st] : &bars->d_full[st];
-          if (lane == 0) {
-            if (pos >= n && !mbar_wait(rot ? &bars->r_empty[st] : &bars->d_empty[st],
-                                       ((pos / n) - 1) & 1, status, abort_flag))
-              ok = 0;
-            else
-              mbar_arrive_expect_tx(full, rot ? bytes : 2 * bytes);
-          }
-          ok = __shfl_sync(FULL, ok, 0);
-          if (!ok) {
-            --(rot ? rpos : dpos);
-            break;
-          }
-          if (my_col < (rot ? 1 : 2) && my_pg < pages)
-            tma_load_3d((rot ? sR + st * LA_BLK : sD + (2 * st + my_col) * LA_BLK) +
-                            my_pg * p.box * 128,
-                        &cmap, full, (2 * d + my_col) * 64, 0, row);
+        if (lane == 0) {
+          if (pos >= C::NST &&
+              !mbar_wait(&bars->k_empty[st], ((pos / C::NST) - 1) & 1, status, abort_flag))
+            ok = 0;
+          else
+            mbar_arrive_expect_tx(&bars->k_full[st], static_cast<unsigned>(pages * page_bytes));
+        }
+        ok = __shfl_sync(FULL, ok, 0);
+        if (!ok) break;
+        if (lane < pages) {
+          unsigned char* dst = sK + st * C::STAGE + (rot ? LA_LAT : 0) + lane * page_bytes;
+          if (rot)
+            tma_load_3d(dst, &rmap, &bars->k_full[st], 0, 0, row >> 3);
+          else
+            tma_load_4d(dst, &cmap, &bars->k_full[st], 0, 0, 0, row >> 3);
         }
       }
     }
     // A role gave up on a wait: no copy may still be writing shared memory when the
-    // CTA exits.
+    // CTA exits.  (A slot's phase also needs the other producer's bytes; if that one
+    // gave up first, this wait runs out instead.)
     if ((!ok || *abort_flag) && lane == 0) {
-      drain_armed(bars->d_full, C::ND, dpos, -1, status);
-      drain_armed(bars->r_full, C::NR, rpos, -1, status);
+      drain_armed(bars->k_full, C::NST, pos, -1, status);
       if (n_seg > 0) mbar_wait(&bars->q_full, (n_seg - 1) & 1, status, nullptr);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == 5 || warp == 7) {
     // ---------------------------------------------------------------- MMA
+    // An MMA this small costs its issuing thread more than the tensor core, so S and
+    // P V have a thread each.
     if (lane == 0) {
+      const bool scores = warp == 5;
       constexpr unsigned idesc_s = make_idesc_f16(64, LA_KEYS, !HALF, false);
       constexpr unsigned idesc_pv = make_idesc_f16(128, R, !HALF, false) | (1u << 15);  // A MN-major
       const uint64_t q_d = smem_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t p_d = smem_desc_sw128(smem_u32(sP), 16, 1024);
-      const uint64_t k_d = smem_desc_sw128(smem_u32(sD), 16, 1024);
-      const uint64_t r_d = smem_desc_sw128(smem_u32(sR), 16, 1024);
-      const uint64_t v_d = smem_desc_sw128(smem_u32(sD), LA_BLK, 1024);
+      // 8 keys are nc KB apart; of V, 64 dims are 1 KB apart
+      const uint64_t k_d = smem_desc_sw128(smem_u32(sK), 16, nc * 1024);
+      const uint64_t r_d = smem_desc_sw128(smem_u32(sK + LA_LAT), 16, 1024);
+      const uint64_t v_d = smem_desc_sw128(smem_u32(sK), 1024, nc * 1024);
       Walk w = la_walk(p, share);
       Seg g;
-      int tile = 0, n_seg = 0;  // of the CTA so far
+      int n = 0, n_seg = 0;  // tile of the CTA, parts of row tiles
       bool ok = true;
-      // The scores of the CTA's tile n.
-      auto scores = [&](int n) -> bool {
-        const unsigned s_t = tmem + C::S_COL + (n & 1) * 64;
-        for (int d = 0; d < nd; ++d) {
-          const int pos = n * nd + d, st = pos % C::ND;
-          if (!mbar_wait(&bars->d_full[st], (pos / C::ND) & 1, status, abort_flag)) return false;
-          tc_fence_after();
-          const uint64_t qb = q_d + ((2 * d * C::QBLK) >> 4), kb = k_d + ((2 * st * LA_BLK) >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_ss(s_t, qb + (((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4),
-                      kb + (((kk >> 2) * LA_BLK + (kk & 3) * 32) >> 4), idesc_s,
-                      (d > 0 || kk > 0) ? 1u : 0u);
-        }
-        const int st = n % C::NR;
-        if (!mbar_wait(&bars->r_full[st], (n / C::NR) & 1, status, abort_flag)) return false;
-        tc_fence_after();
-        const uint64_t qb = q_d + ((2 * nd * C::QBLK) >> 4), kb = r_d + ((st * LA_BLK) >> 4);
-        for (int kk = 0; kk < p.dr / 16; ++kk)
-          tc_mma_ss(s_t, qb + ((kk * 32) >> 4), kb + ((kk * 32) >> 4), idesc_s, 1u);
-        tc_commit(&bars->r_empty[st]);
-        tc_commit(&bars->s_full[n & 1]);
-        return true;
-      };
       while (ok && la_next(p, w, side, g)) {
         if (g.s == 0) continue;
-        if (!mbar_wait(&bars->q_full, n_seg & 1, status, abort_flag)) break;
+        if (scores && !mbar_wait(&bars->q_full, n_seg & 1, status, abort_flag)) break;
         ++n_seg;
         const int n_tiles = g.k1 - g.k0;
-        for (int i = 0; ok && i <= n_tiles; ++i) {
-          if (i < n_tiles) {
-            if (!scores(tile + i)) {
+        for (int i = 0; i < n_tiles; ++i, ++n) {
+          const int st = n % C::NST;
+          // opaque bases: the offsets of the unrolled MMAs are added at each use
+          if (scores) {
+            if ((n >= 2 &&
+                 !mbar_wait(&bars->s_empty[n & 1], ((n >> 1) - 1) & 1, status, abort_flag)) ||
+                !mbar_wait(&bars->k_full[st], (n / C::NST) & 1, status, abort_flag)) {
               ok = false;
               break;
             }
-            if (i == n_tiles - 1) tc_commit(&bars->q_empty);
-          }
-          if (i == 0) continue;
-          const int n = tile + i - 1;  // P V of the tile before
-          if (!mbar_wait(&bars->p_full, n & 1, status, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          for (int d = 0; d < nd; ++d) {
-            const int st = (n * nd + d) % C::ND;
-            const uint64_t vb = v_d + ((2 * st * LA_BLK) >> 4);
+            tc_fence_after();
+            unsigned s_t = tmem + C::S_COL + (n & 1) * LA_KEYS, more = 0u;
+            uint64_t qb = q_d, kb = k_d + ((st * C::STAGE) >> 4);
+            for (int d = 0; d < nd; ++d) {
+              asm volatile("" : "+r"(s_t), "+l"(qb), "+l"(kb), "+r"(more));
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_ss(s_t, qb + (((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4),
+                          kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s,
+                          kk > 0 ? 1u : more);
+              qb += (2 * C::QBLK) >> 4;
+              kb += 2048 >> 4;
+              more = 1u;
+            }
+            kb = r_d + ((st * C::STAGE) >> 4);
+            asm volatile("" : "+r"(s_t), "+l"(qb), "+l"(kb));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_ss(tmem + d * R, vb + ((kk * 2048) >> 4), p_d + ((kk * 32) >> 4), idesc_pv,
-                        (i > 1 || kk > 0) ? 1u : 0u);
-            tc_commit(&bars->d_empty[st]);
+              if (kk < p.dr / 16)
+                tc_mma_ss(s_t, qb + ((kk * 32) >> 4), kb + ((kk * 32) >> 4), idesc_s, 1u);
+            tc_commit(&bars->s_full[n & 1]);
+            if (i == n_tiles - 1) tc_commit(&bars->q_empty);
+          } else {
+            if (!mbar_wait(&bars->p_full, n & 1, status, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            uint64_t vb = v_d + ((st * C::STAGE) >> 4), pb = p_d;
+            unsigned o_t = tmem, more = i > 0 ? 1u : 0u;
+            for (int kk = 0; kk < LA_KEYS / 16; ++kk) {
+              asm volatile("" : "+r"(o_t), "+l"(vb), "+l"(pb), "+r"(more));
+#pragma unroll
+              for (int d = 0; d < 4; ++d)
+                if (d < nd) tc_mma_ss(o_t + d * R, vb + ((d * 2048) >> 4), pb, idesc_pv, more);
+              vb += (2 * nc * 1024) >> 4;
+              pb += 32 >> 4;
+              more = 1u;
+            }
+            tc_commit(&bars->k_empty[st]);
+            tc_commit(&bars->pv_done);
           }
-          tc_commit(&bars->pv_done);
         }
-        tile += n_tiles;
       }
       // no MMA may still be running when TMEM is released (matters only when a role
       // gave up on a wait)
-      tc_commit(&bars->drain);
-      mbar_wait(&bars->drain, 0, status, nullptr);
+      uint64_t* drain = &bars->drain[scores ? 0 : 1];
+      tc_commit(drain);
+      mbar_wait(drain, 0, status, nullptr);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -567,8 +586,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         float alpha[2] = {1.f, 1.f};
         if (ok && has_rows) {
           tc_fence_after();
-          tc_ld_16x64(lane_base + C::S_COL + (n & 1) * 64, v);
+          tc_ld_16x64(lane_base + C::S_COL + (n & 1) * LA_KEYS, v);
           tc_wait_ld();
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&bars->s_empty[n & 1]);
           if (key0 + LA_KEYS > first_max) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -601,6 +622,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             l[k] += v[e];
           }
         }
+        if (!has_rows && lane == 0) mbar_arrive(&bars->s_empty[n & 1]);
         const bool rescale = any_of_128(ask);
         // P V of the tile before has read P, and O may be rescaled
         if (ok && n > 0 &&
@@ -643,11 +665,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         // slots may hold anything, and 0 * NaN is NaN.
         const int tail = g.s - key0;
         if (tail < LA_KEYS) {
-          for (int e = threadIdx.x; e < (LA_KEYS - tail) * 16 * nd; e += 128) {
-            const int pair = e / (16 * (LA_KEYS - tail)), x = e % (16 * (LA_KEYS - tail));
-            *reinterpret_cast<uint4*>(sD + (2 * ((n * nd + pair) % C::ND) + (x & 1)) * LA_BLK +
-                                      (tail + (x >> 4)) * 128 + ((x >> 1) & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
+          unsigned char* k = sK + (n % C::NST) * C::STAGE;
+          for (int e = threadIdx.x; e < (LA_KEYS - tail) * 8 * nc; e += 128) {
+            const int row = tail + e / (8 * nc), x = e % (8 * nc);
+            *reinterpret_cast<uint4*>(k + ((row >> 3) * nc + (x >> 3)) * 1024 + (row & 7) * 128 +
+                                      (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         fence_proxy_async_smem();
@@ -710,12 +732,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
 
 // --------------------------------------------------------------------- merge
 
-constexpr int LM_WARPS = 8;
+constexpr int LM_ROWS = 8;
 
 // CTA (x, y): rows 8 y .. of the row tile that the CTA x of the attention began and
-// left to the next shares, if it did.  A warp merges a row.
+// left to the next shares, if it did.  A warp merges 128 dims of a row.
 template <bool HALF>
-__global__ void __launch_bounds__(LM_WARPS * 32)
+__global__ void __launch_bounds__(LM_ROWS * 4 * 32)
     latent_merge_kernel(const __grid_constant__ LaProblem p) {
   grid_dep_wait();
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
@@ -723,17 +745,24 @@ __global__ void __launch_bounds__(LM_WARPS * 32)
   if (share + 1 >= shares) return;
   const Cut a = p.cuts[share], b = p.cuts[share + 1];
   if (b.t == 0 || (a.r == b.r && a.j == b.j && a.t > 0)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nd = p.dc / 128;
   int parts = 2;  // shares that hold a part of it
-  while (share + parts < shares) {
-    const Cut c = p.cuts[share + parts];
-    if (c.r != b.r || c.j != b.j || c.t == 0) break;
-    ++parts;
+  for (;;) {
+    const int c = share + parts + lane;
+    bool on = c < shares;
+    if (on) {
+      const Cut k = p.cuts[c];
+      on = k.r == b.r && k.j == b.j && k.t > 0;
+    }
+    const unsigned off = ~__ballot_sync(FULL, on);
+    parts += off ? __ffs(off) - 1 : 32;
+    if (off) break;
   }
   int t0, q, s;
   if (!la_request(p, b.r, t0, q, s)) return;
   const int64_t first = static_cast<int64_t>(p.lanes > 1 ? side : b.j) * p.R;
   const int64_t rows = min(static_cast<int64_t>(p.R), static_cast<int64_t>(q) * p.H - first);
-  const int row = blockIdx.y * LM_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int row = blockIdx.y * LM_ROWS + warp / nd, d = warp % nd;
   if (row >= rows) return;
   // part i's place: the second partial of the first share, the first of the others
   auto at = [&](int i) {
@@ -744,35 +773,23 @@ __global__ void __launch_bounds__(LM_WARPS * 32)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
   const float ref = mx == -INFINITY ? 0.f : mx;
-  float4 acc[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-  const int n4 = p.dc / 128;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < parts; ++i) {
     const float2 ml = p.part_ml[at(i)];
+    const float4 x = *reinterpret_cast<const float4*>(p.part_o + at(i) * p.dc + d * 128 + lane * 4);
     const float wgt = fast_exp2(ml.x - ref);
     l += wgt * ml.y;
-    const float4* o = reinterpret_cast<const float4*>(p.part_o + at(i) * p.dc);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n4) {
-        const float4 x = o[e * 32 + lane];
-        acc[e].x += wgt * x.x;
-        acc[e].y += wgt * x.y;
-        acc[e].z += wgt * x.z;
-        acc[e].w += wgt * x.w;
-      }
+    acc.x += wgt * x.x;
+    acc.y += wgt * x.y;
+    acc.z += wgt * x.z;
+    acc.w += wgt * x.w;
   }
   const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
-  uint16_t* out = p.out + (static_cast<int64_t>(t0) * p.H + first + row) * p.dc;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < n4)
-      reinterpret_cast<uint2*>(out)[e * 32 + lane] =
-          make_uint2(pack2<HALF>(acc[e].x * inv, acc[e].y * inv),
-                     pack2<HALF>(acc[e].z * inv, acc[e].w * inv));
+  uint16_t* out = p.out + (static_cast<int64_t>(t0) * p.H + first + row) * p.dc + d * 128;
+  reinterpret_cast<uint2*>(out)[lane] =
+      make_uint2(pack2<HALF>(acc.x * inv, acc.y * inv), pack2<HALF>(acc.z * inv, acc.w * inv));
 }
 
 // ---------------------------------------------------------------------- host
@@ -793,15 +810,14 @@ LaLayout la_layout(int B, int dc) {
   l.grid = std::min(current_sms(), MAX_SHARES);
   l.cuts = sizeof(LaHeader);
   l.prefix = up(l.cuts + sizeof(Cut) * (l.grid + 1));
-  l.ml = up(l.prefix + sizeof(double) * (static_cast<size_t>(B) + 1));
+  l.ml = up(l.prefix + sizeof(float) * (static_cast<size_t>(B) + 1));
   l.o = up(l.ml + sizeof(float2) * l.grid * 2 * 64);
   l.total = up(l.o + sizeof(float) * l.grid * 2 * 64 * dc);
   return l;
 }
 
 template <int R, bool HALF>
-cudaError_t launch_latent(const LaProblem& p, const CUtensorMap& qmap, const CUtensorMap& cmap,
-                          int grid, cudaStream_t st) {
+cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[3], int grid, cudaStream_t st) {
   using C = LaCfg<R>;
   auto kern = latent_kernel<R, HALF>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -819,19 +835,18 @@ cudaError_t launch_latent(const LaProblem& p, const CUtensorMap& qmap, const CUt
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, p, qmap, cmap);
+  e = cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2]);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), R / LM_WARPS);
-  cfg.blockDim = dim3(LM_WARPS * 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), R / LM_ROWS);
+  cfg.blockDim = dim3(static_cast<unsigned>(LM_ROWS * (p.dc / 128) * 32));
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF>, p);
 }
 
 template <int R>
-cudaError_t launch_latent_rows(const LaProblem& p, const CUtensorMap& qmap, const CUtensorMap& cmap,
-                               int grid, cudaStream_t st) {
-  return p.half ? launch_latent<R, true>(p, qmap, cmap, grid, st)
-                : launch_latent<R, false>(p, qmap, cmap, grid, st);
+cudaError_t launch_latent_rows(const LaProblem& p, const CUtensorMap (&m)[3], int grid, cudaStream_t st) {
+  return p.half ? launch_latent<R, true>(p, m, grid, st)
+                : launch_latent<R, false>(p, m, grid, st);
 }
 
 }  // namespace
@@ -879,7 +894,7 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   unsigned char* ws = static_cast<unsigned char*>(a->workspace);
   p.hdr = reinterpret_cast<LaHeader*>(ws);
   p.cuts = reinterpret_cast<Cut*>(ws + l.cuts);
-  p.prefix = reinterpret_cast<double*>(ws + l.prefix);
+  p.prefix = reinterpret_cast<float*>(ws + l.prefix);
   p.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   p.part_o = reinterpret_cast<float*>(ws + l.o);
   // strictly positive, so that a masked score (-inf) always maps to weight 0; at
@@ -899,18 +914,18 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   const int tiles = (a->num_heads + R - 1) / R;  // row tiles of a token
   p.lanes = a->max_query_len <= 1 && tiles > 1 && tiles <= 8 ? tiles : 1;
   p.max_shares = std::max(1, l.grid / p.lanes);
-  // a copy is a run of rows of one block: 64, 32 or 16
+  // a copy is a run of rows of one block
   p.box = a->block_size % 64 == 0 ? 64 : a->block_size % 32 == 0 ? 32 : 16;
   const int dim = a->latent_size + a->rope_size;
-  CUtensorMap qmap, cmap;
-  if (!encode_rows_map(&qmap, a->q, p.half, dim, 1, a->num_tokens * a->num_heads, dim, dim, R) ||
-      !encode_rows_map(&cmap, a->kv_cache, p.half, dim, 1, a->num_blocks * a->block_size, dim, dim,
-                       p.box))
+  CUtensorMap m[3];
+  if (!encode_rows_map(&m[0], a->q, p.half, dim, 1, a->num_tokens * a->num_heads, dim, dim, R) ||
+      !encode_latent_maps(&m[1], &m[2], a->kv_cache, p.half, a->latent_size, a->rope_size,
+                          a->num_blocks * a->block_size, p.box))
     return PATTN_ERR_CUDA;
   const int grid = p.max_shares * p.lanes;
   cudaStream_t st = static_cast<cudaStream_t>(a->stream);
-  const cudaError_t e = R == 16   ? launch_latent_rows<16>(p, qmap, cmap, grid, st)
-                        : R == 32 ? launch_latent_rows<32>(p, qmap, cmap, grid, st)
-                                  : launch_latent_rows<64>(p, qmap, cmap, grid, st);
+  const cudaError_t e = R == 16   ? launch_latent_rows<16>(p, m, grid, st)
+                        : R == 32 ? launch_latent_rows<32>(p, m, grid, st)
+                                  : launch_latent_rows<64>(p, m, grid, st);
   return e == cudaSuccess ? PATTN_OK : PATTN_ERR_CUDA;
 }

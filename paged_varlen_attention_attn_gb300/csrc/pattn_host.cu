@@ -397,6 +397,31 @@ bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_latent_maps(CUtensorMap* latent_map, CUtensorMap* rope_map, const void* cache, bool half,
+                        int latent, int rope, int rows, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const CUtensorMapDataType dt =
+      half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t row = 2ull * static_cast<cuuint64_t>(latent + rope);
+  const cuuint64_t groups = static_cast<cuuint64_t>(rows / 8);
+  const cuuint32_t box_groups = static_cast<cuuint32_t>(box_rows / 8);
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(latent / 64), groups};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(latent / 64), box_groups};
+  if (enc(latent_map, dt, 4, const_cast<void*>(cache), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  const cuuint64_t rdims[3] = {static_cast<cuuint64_t>(rope), 8, groups};
+  const cuuint64_t rstrides[2] = {row, 8 * row};
+  const cuuint32_t rbox[3] = {64, 8, box_groups};
+  return enc(rope_map, dt, 3, static_cast<char*>(const_cast<void*>(cache)) + 2 * latent, rdims,
+             rstrides, rbox, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int current_sms() {
   static int counts[64] = {0};
   int dev = 0;
