@@ -213,12 +213,14 @@ cudaError_t launch_cascade_merge(const float* o_a, const float* lse_a, int chunk
 bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int heads, int rows,
                      long long head_stride, long long row_stride, int box_rows);
 
-// TMA tensor maps over a cache of latent rows [rows][latent + rope] (rows a multiple
-// of 8): the latents as {64, row of 8, 64-element block, 8 rows}, a box all blocks of
-// box_rows rows, which lands as [8 rows][block][8 x 128 bytes]; the rotary parts as
-// {rope, row of 8, 8 rows}, widened to 64 elements with zeros.  128-byte swizzle.
-bool encode_latent_maps(CUtensorMap* latent_map, CUtensorMap* rope_map, const void* cache, bool half,
-                        int latent, int rope, int rows, int box_rows);
+// TMA tensor maps of the absorbed attention over rows [latent | rope], 128-byte
+// swizzle.  m[0]: q [q_rows] as {64, row, 64-element block}, a box q_box rows of all
+// blocks.  m[1]: the cache [rows] (a multiple of 8) as {64, row of 8, block, 8 rows}, a
+// box all blocks of `box` rows, which lands as [8 rows][block][8 x 128 bytes].  At rope
+// 64 these hold the rotary parts too; otherwise m[2] (the cache) and m[3] (q) do,
+// widened to 64 elements with zeros.
+bool encode_latent_maps(CUtensorMap* m, const void* q, const void* cache, bool half, int latent,
+                        int rope, int q_rows, int q_box, int rows, int box);
 
 // Checks the sizes and the type of a cache of latent rows (host only).
 pattn_status_t check_latent_sizes(int latent_size, int rope_size, int block_size, int kv_dtype);

@@ -24,7 +24,7 @@
 //
 // A tile lies as [8 keys][64-element column block][8 x 128 bytes], so that the rows
 // of a page land with one copy whatever the block size: a copy holds its warp for
-// some 200 ns.  The rotary parts come through a map of their own, from another warp.
+// some 200 ns.
 //
 // Work: the batch's (row tile, key tile) grid, row tile after row tile, is cut into
 // equal shares, one per CTA (fewer where a share would be below LEAST_SHARE
@@ -33,8 +33,8 @@
 // single tokens with more than 64 heads, the CTAs of a share work side by side
 // on the row tiles of one token, so HBM is read once for all of them.
 //
-// Eight warps: 0-3 softmax and epilogue, 4 TMA of the latents, 5 and 7 issue the MMAs
-// of S and of P V, 6 TMA of Q and the rotary parts.
+// Eight warps: 0-3 softmax and epilogue, 4 and 6 TMA of the cache, 5 TMA of Q and the
+// MMAs of S, 7 the MMAs of P V.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -52,6 +52,7 @@ constexpr int LA_ROT = LA_KEYS * 128; // bytes of a tile's rotary parts
 constexpr int LA_LAT = 8 * LA_ROT;    // and of its latents (dc = 512)
 constexpr int PAD = 2;                // a row tile's fixed cost, in key tiles
 constexpr int LEAST_SHARE = 3;        // cost of a CTA's share, in key tiles
+constexpr int LA_AHEAD = 1;           // tiles asked for in L2 before their copies
 constexpr float LA_RESCALE_LOG2 = 8.f;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_SHARES = 1024;
@@ -85,6 +86,7 @@ struct LaProblem {
   int lanes;        // CTAs side by side on a share (1, or the row tiles of a token)
   int max_shares;
   int box;          // cache rows of one copy
+  int fused;        // rotary parts of 64 elements: copied with the latents
 };
 
 // A request's rows and keys; false (and the rows clipped to out) if they are bad.
@@ -325,6 +327,44 @@ __device__ __forceinline__ void tc_ld16(unsigned taddr, float (&v)[16]) {
       : "r"(taddr));
 }
 
+// Asks for a box in L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2,
+                                                int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+
+// 1 in one lane of a converged warp, 0 in the others.
+__device__ __forceinline__ unsigned elect_one() {
+  unsigned r;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r));
+  return r;
+}
+
+// One MMA by the lanes with `lead` (one of a converged warp).
+__device__ __forceinline__ void tc_mma_ss_if(unsigned lead, unsigned d_tmem, uint64_t a_desc,
+                                             uint64_t b_desc, unsigned idesc, unsigned accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
 // Barrier 1 over the softmax threads; whether any of them asked.
 __device__ __forceinline__ bool any_of_128(bool ask) {
   unsigned r;
@@ -343,7 +383,8 @@ template <int R, bool HALF>
 __global__ void __launch_bounds__(LA_THREADS, 1)
     latent_kernel(const __grid_constant__ LaProblem p, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap cmap,
-                  const __grid_constant__ CUtensorMap rmap) {
+                  const __grid_constant__ CUtensorMap rmap,
+                  const __grid_constant__ CUtensorMap qrmap) {
   using C = LaCfg<R>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -371,7 +412,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     fence_mbar_init();
     tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&cmap);
-    tma_prefetch_desc(&rmap);
+    if (!p.fused) {
+      tma_prefetch_desc(&rmap);
+      tma_prefetch_desc(&qrmap);
+    }
   }
   if (warp == 0) {
     tmem_alloc(&bars->tmem_base, 512);
@@ -390,42 +434,31 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   unsigned char* sP = smem + C::P_OFF;
   unsigned char* sK = smem + C::K_OFF;
   const int nc = p.dc / 64;  // column blocks of the latents
+  const int cols = nc + p.fused;  // of a copied row
   const int nd = p.dc / 128;
 
   if (!works) {
   } else if (warp == 4 || warp == 6) {
     // ---------------------------------------------------------------- TMA
-    // Warp 4 copies the latents of a tile's pages, warp 6 their rotary parts and Q.
-    // Lane 0 waits for a ring slot and posts its bytes; the copies go out from one
-    // lane each.
-    const bool rot = warp == 6;
+    // Rotary parts of 64 elements come with the latents, a copy a page, and warps 4 and
+    // 6 take turns at the pages (a copy holds its warp for some 200 ns); others come
+    // through a map that widens them with zeros, copied by warp 6.  Lane 0 waits for
+    // a ring slot and posts its warp's bytes, the copies go out from one lane each.
+    const int half = warp == 6 ? 1 : 0;
+    const bool rot = !p.fused && half;
     Walk w = la_walk(p, share);
     Seg g;
-    int pos = 0, n_seg = 0, ok = 1;
-    const int ppt = LA_KEYS / p.box;  // copies of a tile
-    const int page_bytes = rot ? p.box * 128 : p.box * 2 * p.dc;
+    int pos = 0, ok = 1;
+    const int ppt = LA_KEYS / p.box;  // pages of a tile
+    const int page = p.fused ? half + 2 * lane : lane;  // this lane's
+    const int page_bytes = rot ? p.box * 128 : p.box * 128 * cols;
     while (ok && la_next(p, w, side, g)) {
       if (g.s == 0) continue;
-      if (rot) {
-        if (lane == 0) {
-          if (n_seg > 0 && !mbar_wait(&bars->q_empty, (n_seg - 1) & 1, status, abort_flag)) {
-            ok = 0;
-          } else {
-            mbar_arrive_expect_tx(&bars->q_full, static_cast<unsigned>((nc + 1) * C::QBLK));
-            for (int c = 0; c <= nc; ++c)
-              tma_load_3d(sQ + c * C::QBLK, &qmap, &bars->q_full, c * 64, 0,
-                          static_cast<int>(g.row0));
-          }
-        }
-        ok = __shfl_sync(FULL, ok, 0);
-        if (!ok) break;
-        ++n_seg;
-      }
       const int* bt = p.block_table + static_cast<int64_t>(g.r) * p.mbps;
-      // the pool row that page `lane` of key tile kt begins at
+      // the pool row that the lane's page of key tile kt begins at, -1 for none
       auto page_row = [&](int kt) {
-        const int key = kt * LA_KEYS + lane * p.box;
-        if (lane >= ppt || kt >= g.k1 || key >= g.s) return 0;
+        const int key = kt * LA_KEYS + page * p.box;
+        if (page >= ppt || kt >= g.k1 || key >= g.s) return -1;
         int blk = bt[key / p.bs];
         if (blk < 0 || blk >= p.NB) {
           flag_status(status, PATTN_DEV_BAD_METADATA);
@@ -433,27 +466,44 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         }
         return blk * p.bs + key % p.bs;
       };
-      int row_next = page_row(g.k0);
+      // Tiles past the ring are asked for in L2: two tiles in flight do not cover the
+      // latency of HBM.
+      int rows[LA_AHEAD + 1];
+      auto ask = [&](int row) {
+        if (row < 0) return;
+        if (rot) tma_prefetch_3d(&rmap, 0, 0, row >> 3);
+        else tma_prefetch_4d(&cmap, 0, 0, 0, row >> 3);
+      };
+#pragma unroll
+      for (int e = 0; e <= LA_AHEAD; ++e) {
+        rows[e] = page_row(g.k0 + e);
+        if (e > 0) ask(rows[e]);
+      }
       for (int kt = g.k0; kt < g.k1; ++kt, ++pos) {
-        const int row = row_next, st = pos % C::NST;
-        row_next = page_row(kt + 1);
-        const int pages = min(ppt, (g.s - kt * LA_KEYS + p.box - 1) / p.box);
+        const int row = rows[0], st = pos % C::NST;
+#pragma unroll
+        for (int e = 0; e < LA_AHEAD; ++e) rows[e] = rows[e + 1];
+        rows[LA_AHEAD] = page_row(kt + 1 + LA_AHEAD);
+        const int copies = __popc(__ballot_sync(FULL, row >= 0));
         if (lane == 0) {
           if (pos >= C::NST &&
               !mbar_wait(&bars->k_empty[st], ((pos / C::NST) - 1) & 1, status, abort_flag))
             ok = 0;
+          else if (copies > 0)
+            mbar_arrive_expect_tx(&bars->k_full[st], static_cast<unsigned>(copies * page_bytes));
           else
-            mbar_arrive_expect_tx(&bars->k_full[st], static_cast<unsigned>(pages * page_bytes));
+            mbar_arrive(&bars->k_full[st]);
         }
         ok = __shfl_sync(FULL, ok, 0);
         if (!ok) break;
-        if (lane < pages) {
-          unsigned char* dst = sK + st * C::STAGE + (rot ? LA_LAT : 0) + lane * page_bytes;
+        if (row >= 0) {
+          unsigned char* dst = sK + st * C::STAGE + (rot ? LA_LAT : 0) + page * page_bytes;
           if (rot)
             tma_load_3d(dst, &rmap, &bars->k_full[st], 0, 0, row >> 3);
           else
             tma_load_4d(dst, &cmap, &bars->k_full[st], 0, 0, 0, row >> 3);
         }
+        ask(rows[LA_AHEAD]);
       }
     }
     // A role gave up on a wait: no copy may still be writing shared memory when the
@@ -461,92 +511,113 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     // gave up first, this wait runs out instead.)
     if ((!ok || *abort_flag) && lane == 0) {
       drain_armed(bars->k_full, C::NST, pos, -1, status);
-      if (n_seg > 0) mbar_wait(&bars->q_full, (n_seg - 1) & 1, status, nullptr);
     }
     __syncwarp();
   } else if (warp == 5 || warp == 7) {
     // ---------------------------------------------------------------- MMA
-    // An MMA this small costs its issuing thread more than the tensor core, so S and
-    // P V have a thread each.
-    if (lane == 0) {
-      const bool scores = warp == 5;
-      constexpr unsigned idesc_s = make_idesc_f16(64, LA_KEYS, !HALF, false);
-      constexpr unsigned idesc_pv = make_idesc_f16(128, R, !HALF, false) | (1u << 15);  // A MN-major
-      const uint64_t q_d = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t p_d = smem_desc_sw128(smem_u32(sP), 16, 1024);
-      // 8 keys are nc KB apart; of V, 64 dims are 1 KB apart
-      const uint64_t k_d = smem_desc_sw128(smem_u32(sK), 16, nc * 1024);
-      const uint64_t r_d = smem_desc_sw128(smem_u32(sK + LA_LAT), 16, 1024);
-      const uint64_t v_d = smem_desc_sw128(smem_u32(sK), 1024, nc * 1024);
-      Walk w = la_walk(p, share);
-      Seg g;
-      int n = 0, n_seg = 0;  // tile of the CTA, parts of row tiles
-      bool ok = true;
-      while (ok && la_next(p, w, side, g)) {
-        if (g.s == 0) continue;
-        if (scores && !mbar_wait(&bars->q_full, n_seg & 1, status, abort_flag)) break;
+    // S and P V have a warp each.  The whole warp walks, with every value that the
+    // descriptors are made of the same in all lanes and known to be (reductions over
+    // the warp), and the elected lane issues: an MMA of S then takes 34 cycles (M 64, N
+    // 64; its operands take 32 to read).  With lane 0 in place of the elected one it
+    // took 54, from a branch for one lane 50 to 71.
+    const bool scores = warp == 5;
+    const unsigned lead = elect_one();
+    constexpr unsigned idesc_s = make_idesc_f16(64, LA_KEYS, !HALF, false);
+    constexpr unsigned idesc_pv = make_idesc_f16(128, R, !HALF, false) | (1u << 15);  // A MN-major
+    const unsigned t_base = __reduce_max_sync(FULL, tmem);
+    const uint64_t q_d = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t p_d = smem_desc_sw128(smem_u32(sP), 16, 1024);
+    // 8 keys are `cols` KB apart; of V, 64 dims are 1 KB apart
+    const uint64_t k_d = smem_desc_sw128(smem_u32(sK), 16, cols * 1024);
+    const uint64_t r_d = smem_desc_sw128(smem_u32(sK + (p.fused ? nc * 1024 : LA_LAT)), 16,
+                                         p.fused ? cols * 1024 : 1024);
+    const uint64_t v_d = smem_desc_sw128(smem_u32(sK), 1024, cols * 1024);
+    Walk w = la_walk(p, share);
+    Seg g;
+    int n = 0, n_seg = 0;  // tile of the CTA, parts of row tiles
+    bool ok = true;
+    while (ok && __reduce_max_sync(FULL, static_cast<unsigned>(la_next(p, w, side, g)))) {
+      const int n_tiles = static_cast<int>(
+          __reduce_max_sync(FULL, g.s == 0 ? 0u : static_cast<unsigned>(g.k1 - g.k0)));
+      if (n_tiles == 0) continue;
+      if (scores) {
+        // Q, once the scores of the part before are done
+        if (n_seg > 0 &&
+            !__all_sync(FULL, mbar_wait(&bars->q_empty, (n_seg - 1) & 1, status, abort_flag)))
+          break;
+        if (lead) {
+          mbar_arrive_expect_tx(&bars->q_full, static_cast<unsigned>((nc + 1) * C::QBLK));
+          tma_load_3d(sQ, &qmap, &bars->q_full, 0, static_cast<int>(g.row0), 0);
+          if (!p.fused)
+            tma_load_3d(sQ + nc * C::QBLK, &qrmap, &bars->q_full, 0, static_cast<int>(g.row0), 0);
+        }
         ++n_seg;
-        const int n_tiles = g.k1 - g.k0;
-        for (int i = 0; i < n_tiles; ++i, ++n) {
-          const int st = n % C::NST;
-          // opaque bases: the offsets of the unrolled MMAs are added at each use
-          if (scores) {
-            if ((n >= 2 &&
-                 !mbar_wait(&bars->s_empty[n & 1], ((n >> 1) - 1) & 1, status, abort_flag)) ||
-                !mbar_wait(&bars->k_full[st], (n / C::NST) & 1, status, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            unsigned s_t = tmem + C::S_COL + (n & 1) * LA_KEYS, more = 0u;
-            uint64_t qb = q_d, kb = k_d + ((st * C::STAGE) >> 4);
-            for (int d = 0; d < nd; ++d) {
-              asm volatile("" : "+r"(s_t), "+l"(qb), "+l"(kb), "+r"(more));
+        if (!__all_sync(FULL, mbar_wait(&bars->q_full, (n_seg - 1) & 1, status, abort_flag))) break;
+      }
+      for (int i = 0; i < n_tiles; ++i, ++n) {
+        const int st = n % C::NST;
+        if (scores) {
+          bool there = n < 2 || mbar_wait(&bars->s_empty[n & 1], ((n >> 1) - 1) & 1, status,
+                                          abort_flag);
+          there = there && mbar_wait(&bars->k_full[st], (n / C::NST) & 1, status, abort_flag);
+          if (!__all_sync(FULL, there)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const unsigned s_t = t_base + C::S_COL + (n & 1) * LA_KEYS;
+          uint64_t qb = q_d, kb = k_d + ((st * C::STAGE) >> 4);
+          for (int d = 0; d < nd; ++d) {
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_ss(s_t, qb + (((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4),
-                          kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s,
-                          kk > 0 ? 1u : more);
-              qb += (2 * C::QBLK) >> 4;
-              kb += 2048 >> 4;
-              more = 1u;
-            }
-            kb = r_d + ((st * C::STAGE) >> 4);
-            asm volatile("" : "+r"(s_t), "+l"(qb), "+l"(kb));
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_ss_if(lead, s_t, qb + (((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4),
+                           kb + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc_s,
+                           (kk > 0 || d > 0) ? 1u : 0u);
+            qb += (2 * C::QBLK) >> 4;
+            kb += 2048 >> 4;
+          }
+          kb = r_d + ((st * C::STAGE) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (kk < p.dr / 16)
-                tc_mma_ss(s_t, qb + ((kk * 32) >> 4), kb + ((kk * 32) >> 4), idesc_s, 1u);
+          for (int kk = 0; kk < 4; ++kk)
+            if (kk < p.dr / 16)
+              tc_mma_ss_if(lead, s_t, qb + ((kk * 32) >> 4), kb + ((kk * 32) >> 4), idesc_s, 1u);
+          if (lead) {
             tc_commit(&bars->s_full[n & 1]);
             if (i == n_tiles - 1) tc_commit(&bars->q_empty);
-          } else {
-            if (!mbar_wait(&bars->p_full, n & 1, status, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            uint64_t vb = v_d + ((st * C::STAGE) >> 4), pb = p_d;
-            unsigned o_t = tmem, more = i > 0 ? 1u : 0u;
-            for (int kk = 0; kk < LA_KEYS / 16; ++kk) {
-              asm volatile("" : "+r"(o_t), "+l"(vb), "+l"(pb), "+r"(more));
+          }
+        } else {
+          if (!__all_sync(FULL, mbar_wait(&bars->p_full, n & 1, status, abort_flag))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint64_t vb = v_d + ((st * C::STAGE) >> 4), pb = p_d;
+          for (int kk = 0; kk < LA_KEYS / 16; ++kk) {
 #pragma unroll
-              for (int d = 0; d < 4; ++d)
-                if (d < nd) tc_mma_ss(o_t + d * R, vb + ((d * 2048) >> 4), pb, idesc_pv, more);
-              vb += (2 * nc * 1024) >> 4;
-              pb += 32 >> 4;
-              more = 1u;
-            }
+            for (int d = 0; d < 4; ++d)
+              if (d < nd)
+                tc_mma_ss_if(lead, t_base + d * R, vb + ((d * 2048) >> 4), pb, idesc_pv,
+                             (i > 0 || kk > 0) ? 1u : 0u);
+            vb += (2 * cols * 1024) >> 4;
+            pb += 32 >> 4;
+          }
+          if (lead) {
             tc_commit(&bars->k_empty[st]);
             tc_commit(&bars->pv_done);
           }
         }
       }
-      // no MMA may still be running when TMEM is released (matters only when a role
-      // gave up on a wait)
+    }
+    // no MMA may still be running when TMEM is released (matters only when a role gave
+    // up on a wait)
+    if (lead) {
       uint64_t* drain = &bars->drain[scores ? 0 : 1];
       tc_commit(drain);
       mbar_wait(drain, 0, status, nullptr);
+      // (nor may Q's copy be in flight)
+      if (n_seg > 0) mbar_wait(&bars->q_full, (n_seg - 1) & 1, status, nullptr);
     }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax
     // Warp w's TMEM lanes 32 w .. + 15 hold rows 16 w .. + 15 of S; a thread has two
@@ -668,7 +739,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           unsigned char* k = sK + (n % C::NST) * C::STAGE;
           for (int e = threadIdx.x; e < (LA_KEYS - tail) * 8 * nc; e += 128) {
             const int row = tail + e / (8 * nc), x = e % (8 * nc);
-            *reinterpret_cast<uint4*>(k + ((row >> 3) * nc + (x >> 3)) * 1024 + (row & 7) * 128 +
+            *reinterpret_cast<uint4*>(k + ((row >> 3) * cols + (x >> 3)) * 1024 + (row & 7) * 128 +
                                       (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
@@ -817,7 +888,7 @@ LaLayout la_layout(int B, int dc) {
 }
 
 template <int R, bool HALF>
-cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[3], int grid, cudaStream_t st) {
+cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[4], int grid, cudaStream_t st) {
   using C = LaCfg<R>;
   auto kern = latent_kernel<R, HALF>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -835,7 +906,7 @@ cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[3], int gri
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2]);
+  e = cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2], m[3]);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(grid), R / LM_ROWS);
   cfg.blockDim = dim3(static_cast<unsigned>(LM_ROWS * (p.dc / 128) * 32));
@@ -844,7 +915,7 @@ cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[3], int gri
 }
 
 template <int R>
-cudaError_t launch_latent_rows(const LaProblem& p, const CUtensorMap (&m)[3], int grid, cudaStream_t st) {
+cudaError_t launch_latent_rows(const LaProblem& p, const CUtensorMap (&m)[4], int grid, cudaStream_t st) {
   return p.half ? launch_latent<R, true>(p, m, grid, st)
                 : launch_latent<R, false>(p, m, grid, st);
 }
@@ -914,13 +985,12 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   const int tiles = (a->num_heads + R - 1) / R;  // row tiles of a token
   p.lanes = a->max_query_len <= 1 && tiles > 1 && tiles <= 8 ? tiles : 1;
   p.max_shares = std::max(1, l.grid / p.lanes);
-  // a copy is a run of rows of one block
-  p.box = a->block_size % 64 == 0 ? 64 : a->block_size % 32 == 0 ? 32 : 16;
-  const int dim = a->latent_size + a->rope_size;
-  CUtensorMap m[3];
-  if (!encode_rows_map(&m[0], a->q, p.half, dim, 1, a->num_tokens * a->num_heads, dim, dim, R) ||
-      !encode_latent_maps(&m[1], &m[2], a->kv_cache, p.half, a->latent_size, a->rope_size,
-                          a->num_blocks * a->block_size, p.box))
+  // a copy is a run of rows of one block, and there are two at least for the two warps
+  p.box = a->block_size % 32 == 0 ? 32 : 16;
+  p.fused = a->rope_size == 64;
+  CUtensorMap m[4];
+  if (!encode_latent_maps(m, a->q, a->kv_cache, p.half, a->latent_size, a->rope_size,
+                          a->num_tokens * a->num_heads, R, a->num_blocks * a->block_size, p.box))
     return PATTN_ERR_CUDA;
   const int grid = p.max_shares * p.lanes;
   cudaStream_t st = static_cast<cudaStream_t>(a->stream);

@@ -397,29 +397,41 @@ bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_latent_maps(CUtensorMap* latent_map, CUtensorMap* rope_map, const void* cache, bool half,
-                        int latent, int rope, int rows, int box_rows) {
+bool encode_latent_maps(CUtensorMap* m, const void* q, const void* cache, bool half, int latent,
+                        int rope, int q_rows, int q_box, int rows, int box) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const CUtensorMapDataType dt =
       half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const cuuint64_t row = 2ull * static_cast<cuuint64_t>(latent + rope);
   const cuuint64_t groups = static_cast<cuuint64_t>(rows / 8);
-  const cuuint32_t box_groups = static_cast<cuuint32_t>(box_rows / 8);
+  const cuuint32_t cols = static_cast<cuuint32_t>(latent / 64 + (rope == 64 ? 1 : 0));
+  const cuuint32_t qb = static_cast<cuuint32_t>(q_box), gb = static_cast<cuuint32_t>(box / 8);
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(latent / 64), groups};
-  const cuuint64_t strides[3] = {row, 128, 8 * row};
-  const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(latent / 64), box_groups};
-  if (enc(latent_map, dt, 4, const_cast<void*>(cache), dims, strides, box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
-  const cuuint64_t rdims[3] = {static_cast<cuuint64_t>(rope), 8, groups};
-  const cuuint64_t rstrides[2] = {row, 8 * row};
-  const cuuint32_t rbox[3] = {64, 8, box_groups};
-  return enc(rope_map, dt, 3, static_cast<char*>(const_cast<void*>(cache)) + 2 * latent, rdims,
-             rstrides, rbox, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&](CUtensorMap* map, const void* base, cuuint32_t rank, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* bx) {
+    return enc(map, dt, rank, const_cast<void*>(base), dims, strides, bx, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t qd[3] = {64, static_cast<cuuint64_t>(q_rows), cols}, qs[2] = {row, 128};
+  const cuuint32_t qx[3] = {64, qb, cols};
+  const cuuint64_t cd[4] = {64, 8, cols, groups}, cs[3] = {row, 128, 8 * row};
+  const cuuint32_t cx[4] = {64, 8, cols, gb};
+  if (!encode(&m[0], q, 3, qd, qs, qx) || !encode(&m[1], cache, 4, cd, cs, cx)) return false;
+  if (rope == 64) {
+    m[2] = m[1];
+    m[3] = m[0];
+    return true;
+  }
+  const char* tail = static_cast<const char*>(cache) + 2 * latent;
+  const cuuint64_t rd[3] = {static_cast<cuuint64_t>(rope), 8, groups}, rs[2] = {row, 8 * row};
+  const cuuint32_t rx[3] = {64, 8, gb};
+  const cuuint64_t td[3] = {static_cast<cuuint64_t>(rope), static_cast<cuuint64_t>(q_rows), 1};
+  const cuuint32_t tx[3] = {64, qb, 1};
+  return encode(&m[2], tail, 3, rd, rs, rx) &&
+         encode(&m[3], static_cast<const char*>(q) + 2 * latent, 3, td, qs, tx);
 }
 
 int current_sms() {
