@@ -57,9 +57,11 @@ constexpr float LA_RESCALE_LOG2 = 8.f;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_SHARES = 1024;
 
-// Where a share begins: key tile t of row tile j of request r.
-struct Cut {
-  int r, j, t, pad;
+// Where a share begins: key tile t of row tile j of request r, with the request as
+// la_request gives it (so that a CTA's first copies wait for one load less).
+struct __align__(16) Cut {
+  int r, j, t, known;
+  int t0, q, s, pad;
 };
 
 struct LaHeader {
@@ -77,7 +79,7 @@ struct LaProblem {
   uint16_t* out;
   LaHeader* hdr;
   Cut* cuts;        // [shares + 1]
-  float* part_o;    // [grid][2][R][dc]: what a CTA's first and last row tile leave
+  float* part_o;    // [grid][2][R / 4][dc][4]: what a CTA's first and last row tile leave
   float2* part_ml;  // [grid][2][R]: their max (log2 units) and sum
   float* prefix;    // [B] cost of the requests before (large batches)
   float sl2;
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(LA_PLAN_THREADS)
     p.hdr->shares = shares;
   }
   for (int c = tid; c <= shares; c += LA_PLAN_THREADS) {
-    Cut cut = {c == shares ? p.B : 0, 0, 0, 0};
+    Cut cut = {c == shares ? p.B : 0, 0, 0, 0, 0, 0, 0, 0};
     if (c > 0 && c < shares) {
       const float w = total * static_cast<float>(c) / static_cast<float>(shares);
       int lo = 0, hi = p.B;  // the last request that costs begin at or before w
@@ -218,6 +220,10 @@ __global__ void __launch_bounds__(LA_PLAN_THREADS)
           ++cut.r;
         }
       }
+      cut.known = cut.r == lo;
+      cut.t0 = t0;
+      cut.q = q;
+      cut.s = s;
     }
     p.cuts[c] = cut;
   }
@@ -238,8 +244,13 @@ struct Walk {
   Cut at, end;
 };
 
+__device__ __forceinline__ Cut la_cut(const LaProblem& p, int share) {
+  const int4* c = reinterpret_cast<const int4*>(p.cuts + share);
+  const int4 a = c[0], b = c[1];
+  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
 __device__ __forceinline__ Walk la_walk(const LaProblem& p, int share) {
-  return {p.cuts[share], p.cuts[share + 1]};
+  return {la_cut(p, share), la_cut(p, share + 1)};
 }
 
 // The next part, or false.  lane: which row tile of a token (lanes > 1).
@@ -248,9 +259,15 @@ __device__ __forceinline__ bool la_next(const LaProblem& p, Walk& w, int lane, S
     if (w.at.r >= p.B) return false;
     if (w.at.r == w.end.r && w.at.j == w.end.j && w.at.t >= w.end.t) return false;
     if (w.at.r > w.end.r || (w.at.r == w.end.r && w.at.j > w.end.j)) return false;
-    la_request(p, w.at.r, g.t0, g.q, g.s);
+    if (!w.at.known) {
+      la_request(p, w.at.r, w.at.t0, w.at.q, w.at.s);
+      w.at.known = 1;
+    }
+    g.t0 = w.at.t0;
+    g.q = w.at.q;
+    g.s = w.at.s;
     if (w.at.j >= la_row_tiles(p, g.q)) {
-      w.at = {w.at.r + 1, 0, 0, 0};
+      w.at = {w.at.r + 1, 0, 0, 0, 0, 0, 0, 0};
       continue;
     }
     g.r = w.at.r;
@@ -429,6 +446,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   grid_dep_wait();  // the plan kernel's cuts
 
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
+  // (the cuts are there for every share; one past the last is not looked at)
   const bool works = share < p.hdr->shares;
   unsigned char* sQ = smem + C::Q_OFF;
   unsigned char* sP = smem + C::P_OFF;
@@ -769,25 +787,40 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         ok = false;
       if (any_of_128(!ok)) break;  // (all four warps, so that none waits for another)
       tc_fence_after();
-      float* po = p.part_o + part * R * p.dc;
-      for (int d = 0; d < nd; ++d) {
-        const int dim = d * 128 + warp * 32 + lane;
+      // Lane: a dim of the block; columns: the rows.
+      if (!whole) {
+        float4* po = reinterpret_cast<float4*>(p.part_o) + part * (R / 4) * p.dc + warp * 32 + lane;
+        for (int d = 0; d < nd; ++d, po += 128)
 #pragma unroll
-        for (int c = 0; c < R; c += 16) {
-          if (c >= g.rows) break;
-          float o[16];
-          tc_ld16(lane_base + d * R + c, o);
-          tc_wait_ld();
+          for (int c = 0; c < R; c += 16) {
+            if (c >= g.rows) break;
+            float o[16];
+            tc_ld16(lane_base + d * R + c, o);
+            tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (c + e >= g.rows) break;
-            if (whole)
-              out[static_cast<int64_t>(c + e) * p.dc + dim] =
-                  static_cast<uint16_t>(pack2<HALF>(o[e] * bars->l[c + e], 0.f));
-            else
-              po[(c + e) * p.dc + dim] = o[e];
+            for (int e = 0; e < 16; e += 4)
+              po[static_cast<int64_t>((c + e) / 4) * p.dc] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
-        }
+      } else {
+        // neighbouring lanes swap rows, so that each writes two dims of one row
+        const int odd = lane & 1;
+        uint16_t* ob = out + warp * 32 + (lane & ~1) + static_cast<int64_t>(odd) * p.dc;
+        for (int d = 0; d < nd; ++d, ob += 128)
+#pragma unroll
+          for (int c = 0; c < R; c += 16) {
+            if (c >= g.rows) break;
+            float o[16];
+            tc_ld16(lane_base + d * R + c, o);
+            tc_wait_ld();
+            uint16_t* row = ob + static_cast<int64_t>(c) * p.dc;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2, row += 2 * p.dc) {
+              const float x = o[e] * bars->l[c + e], y = o[e + 1] * bars->l[c + e + 1];
+              const float got = __shfl_xor_sync(FULL, odd ? x : y, 1);
+              if (c + e + odd < g.rows)
+                *reinterpret_cast<unsigned*>(row) = odd ? pack2<HALF>(got, y) : pack2<HALF>(x, got);
+            }
+          }
       }
       tc_fence_before();
     }
@@ -803,64 +836,74 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
 
 // --------------------------------------------------------------------- merge
 
-constexpr int LM_ROWS = 8;
-
-// CTA (x, y): rows 8 y .. of the row tile that the CTA x of the attention began and
-// left to the next shares, if it did.  A warp merges 128 dims of a row.
+// CTA (x, y): rows 4 y .. of the row tile that the CTA x of the attention began and
+// left to the next shares, if it did.  A thread merges a dim of the four rows.
 template <bool HALF>
-__global__ void __launch_bounds__(LM_ROWS * 4 * 32)
-    latent_merge_kernel(const __grid_constant__ LaProblem p) {
+__global__ void __launch_bounds__(512) latent_merge_kernel(const __grid_constant__ LaProblem p) {
   grid_dep_wait();
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
   const int shares = p.hdr->shares;
+  const Cut a = la_cut(p, share), b = la_cut(p, share + 1);
   if (share + 1 >= shares) return;
-  const Cut a = p.cuts[share], b = p.cuts[share + 1];
   if (b.t == 0 || (a.r == b.r && a.j == b.j && a.t > 0)) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nd = p.dc / 128;
+  // (a cut inside a row tile knows its request, which is not a bad one)
+  const int64_t first = static_cast<int64_t>(p.lanes > 1 ? side : b.j) * p.R;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.R),
+                                        static_cast<int64_t>(b.q) * p.H - first));
+  const int row = blockIdx.y * 4, lane = threadIdx.x & 31, dim = threadIdx.x;
+  if (row >= rows) return;
   int parts = 2;  // shares that hold a part of it
   for (;;) {
     const int c = share + parts + lane;
     bool on = c < shares;
     if (on) {
-      const Cut k = p.cuts[c];
-      on = k.r == b.r && k.j == b.j && k.t > 0;
+      const int4 k = *reinterpret_cast<const int4*>(p.cuts + c);
+      on = k.x == b.r && k.y == b.j && k.z > 0;
     }
     const unsigned off = ~__ballot_sync(FULL, on);
     parts += off ? __ffs(off) - 1 : 32;
     if (off) break;
   }
-  int t0, q, s;
-  if (!la_request(p, b.r, t0, q, s)) return;
-  const int64_t first = static_cast<int64_t>(p.lanes > 1 ? side : b.j) * p.R;
-  const int64_t rows = min(static_cast<int64_t>(p.R), static_cast<int64_t>(q) * p.H - first);
-  const int row = blockIdx.y * LM_ROWS + warp / nd, d = warp % nd;
-  if (row >= rows) return;
   // part i's place: the second partial of the first share, the first of the others
   auto at = [&](int i) {
-    return (static_cast<int64_t>((share + i) * p.lanes + side) * 2 + (i == 0 ? 1 : 0)) * p.R + row;
+    return static_cast<int64_t>((share + i) * p.lanes + side) * 2 + (i == 0 ? 1 : 0);
   };
-  float mx = -INFINITY;
-  for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, p.part_ml[at(i)].x);
+  float mx[4], l[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+  for (int e = 0; e < 4; ++e) mx[e] = -INFINITY;
+  for (int i = lane; i < parts; i += 32)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], p.part_ml[at(i) * p.R + row + e].x);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(FULL, mx[e], o));
+    if (mx[e] == -INFINITY) mx[e] = 0.f;
+  }
 #pragma unroll 8
   for (int i = 0; i < parts; ++i) {
-    const float2 ml = p.part_ml[at(i)];
-    const float4 x = *reinterpret_cast<const float4*>(p.part_o + at(i) * p.dc + d * 128 + lane * 4);
-    const float wgt = fast_exp2(ml.x - ref);
-    l += wgt * ml.y;
-    acc.x += wgt * x.x;
-    acc.y += wgt * x.y;
-    acc.z += wgt * x.z;
-    acc.w += wgt * x.w;
+    const float4* ml = reinterpret_cast<const float4*>(p.part_ml + at(i) * p.R + row);
+    const float4 ml0 = ml[0], ml1 = ml[1];
+    const float4 x = reinterpret_cast<const float4*>(
+        p.part_o)[(at(i) * (p.R / 4) + blockIdx.y) * p.dc + dim];
+    const float w[4] = {fast_exp2(ml0.x - mx[0]), fast_exp2(ml0.z - mx[1]),
+                        fast_exp2(ml1.x - mx[2]), fast_exp2(ml1.z - mx[3])};
+    l[0] += w[0] * ml0.y;
+    l[1] += w[1] * ml0.w;
+    l[2] += w[2] * ml1.y;
+    l[3] += w[3] * ml1.w;
+    acc[0] += w[0] * x.x;
+    acc[1] += w[1] * x.y;
+    acc[2] += w[2] * x.z;
+    acc[3] += w[3] * x.w;
   }
-  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
-  uint16_t* out = p.out + (static_cast<int64_t>(t0) * p.H + first + row) * p.dc + d * 128;
-  reinterpret_cast<uint2*>(out)[lane] =
-      make_uint2(pack2<HALF>(acc.x * inv, acc.y * inv), pack2<HALF>(acc.z * inv, acc.w * inv));
+  uint16_t* out = p.out + (static_cast<int64_t>(b.t0) * p.H + first + row) * p.dc + dim;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (row + e < rows) {
+      const float inv = l[e] > 0.f ? 1.f / l[e] : l[e] == 0.f ? 0.f : NAN;
+      out[static_cast<int64_t>(e) * p.dc] = static_cast<uint16_t>(pack2<HALF>(acc[e] * inv, 0.f));
+    }
 }
 
 // ---------------------------------------------------------------------- host
@@ -908,8 +951,8 @@ cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[4], int gri
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2], m[3]);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), R / LM_ROWS);
-  cfg.blockDim = dim3(static_cast<unsigned>(LM_ROWS * (p.dc / 128) * 32));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), R / 4);
+  cfg.blockDim = dim3(static_cast<unsigned>(p.dc));
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF>, p);
 }
