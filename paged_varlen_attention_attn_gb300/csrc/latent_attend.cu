@@ -66,7 +66,7 @@ struct __align__(16) Cut {
 
 struct LaHeader {
   unsigned status;
-  int shares;  // written by the plan kernel
+  int shares;  // written by the attention's first CTA, for the merge
   int pad[62];
 };
 static_assert(sizeof(LaHeader) == 256 && offsetof(LaHeader, status) == offsetof(WsHeader, status),
@@ -81,10 +81,9 @@ struct LaProblem {
   Cut* cuts;        // [shares + 1]
   float* part_o;    // [grid][2][R / 4][dc][4]: what a CTA's first and last row tile leave
   float2* part_ml;  // [grid][2][R]: their max (log2 units) and sum
-  float* prefix;    // [B] cost of the requests before (large batches)
   float sl2;
   int B, T, H, dc, dr, bs, mbps, NB, causal, half;
-  int R;            // rows of a row tile
+  int R, r_shift;   // rows of a row tile, a power of two
   int lanes;        // CTAs side by side on a share (1, or the row tiles of a token)
   int max_shares;
   int box;          // cache rows of one copy
@@ -107,18 +106,19 @@ __device__ __forceinline__ bool la_request(const LaProblem& p, int r, int& t0, i
   return false;
 }
 
+// (A call has fewer than 2^31 (token, head) rows.)
 __device__ __forceinline__ int la_row_tiles(const LaProblem& p, int q) {
   if (p.lanes > 1) return q > 0 ? 1 : 0;  // (a lane's own)
-  return static_cast<int>((static_cast<int64_t>(q) * p.H + p.R - 1) / p.R);
+  return static_cast<int>((static_cast<unsigned>(q) * static_cast<unsigned>(p.H) + p.R - 1) >> p.r_shift);
 }
 
 // Key tiles of row tile j (a bad request's counts one, in which nothing is done).
 __device__ __forceinline__ int la_key_tiles(const LaProblem& p, int q, int s, int j) {
   if (s == 0) return 1;
   int keys = s;
-  if (p.causal && p.lanes == 1) {
-    const int64_t last = (static_cast<int64_t>(j) + 1) * p.R - 1;
-    keys = s - q + static_cast<int>(min(static_cast<int64_t>(q - 1), last / p.H)) + 1;
+  if (p.causal && q > 1) {
+    const unsigned last = (static_cast<unsigned>(j + 1) << p.r_shift) - 1;
+    keys = s - q + min(q - 1, static_cast<int>(last / static_cast<unsigned>(p.H))) + 1;
   }
   return (keys + LA_KEYS - 1) / LA_KEYS;
 }
@@ -129,7 +129,6 @@ __device__ __forceinline__ int la_key_tiles(const LaProblem& p, int q, int s, in
 struct Cost {
   float a, b;
   int n;  // row tiles
-  __device__ float upto(float x) const { return x * (a + 0.5f * b * x); }
 };
 __device__ __forceinline__ Cost la_cost(const LaProblem& p, int q, int s) {
   Cost c;
@@ -142,91 +141,136 @@ __device__ __forceinline__ Cost la_cost(const LaProblem& p, int q, int s) {
   }
   return c;
 }
+__device__ __forceinline__ unsigned long long la_total(const LaProblem& p, int q, int s) {
+  const Cost c = la_cost(p, q, s);
+  const float n = static_cast<float>(c.n);
+  return static_cast<unsigned long long>(rintf(n * (c.a + 0.5f * c.b * n)));
+}
 
 // ------------------------------------------------------------------- plan
 
-constexpr int LA_PLAN_THREADS = 1024;
-constexpr int LA_PLAN_BATCH = 4096;  // requests whose costs fit shared memory
-
-// (fp32: the sums say where the shares are cut, and a share is at least LEAST_SHARE
-// tiles, far above a rounding of its border)
-__global__ void __launch_bounds__(LA_PLAN_THREADS)
-    latent_plan_kernel(const __grid_constant__ LaProblem p) {
-  __shared__ float warp_sums[32];
-  __shared__ float s_prefix[LA_PLAN_BATCH];
-  __shared__ unsigned bad;
+// The status word, cleared before anything of the call can set it.
+__global__ void latent_clear_kernel(LaHeader* hdr) {
   grid_dep_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  float* prefix = p.B <= LA_PLAN_BATCH ? s_prefix : p.prefix;
-  if (tid == 0) bad = 0u;
-  float total = 0.f;
-  for (int base = 0; base < p.B; base += LA_PLAN_THREADS) {
-    __syncthreads();
-    const int r = base + tid;
-    float x = 0.f;
-    if (r < p.B) {
-      int t0, q, s;
-      if (!la_request(p, r, t0, q, s)) bad = PATTN_DEV_BAD_METADATA;
-      const Cost c = la_cost(p, q, s);
-      x = c.upto(static_cast<float>(c.n));
-    }
-    float incl = x;
+  if (threadIdx.x == 0) hdr->status = 0u;
+}
+
+// The sum of x over the CTA's threads before this one, and over all of them.
+__device__ __forceinline__ unsigned long long sum_before(unsigned long long x,
+                                                         unsigned long long* warp_sums,
+                                                         unsigned long long& all) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  unsigned long long incl = x;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float y = __shfl_up_sync(FULL, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warp_sums[wid] = incl;
-    __syncthreads();
-    // (every warp sums the warps before it in the same order)
-    float before = lane < wid ? warp_sums[lane] : 0.f, all = warp_sums[lane];
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(FULL, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // (the sums of the last use have been read)
+  if (lane == 31) warp_sums[wid] = incl;
+  __syncthreads();
+  unsigned long long before = 0ull;
+  all = 0ull;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      before += __shfl_xor_sync(FULL, before, o);
-      all += __shfl_xor_sync(FULL, all, o);
+  for (int w = 0; w < LA_THREADS / 32; ++w) {
+    const unsigned long long y = warp_sums[w];
+    if (w < wid) before += y;
+    all += y;
+  }
+  return before + incl - x;
+}
+
+// Where weight w of request r falls, v past the request's begin.
+__device__ __forceinline__ Cut la_place(const LaProblem& p, int r, int t0, int q, int s, float v) {
+  const Cost k = la_cost(p, q, s);
+  const float x = 2.f * v / (k.a + sqrtf(fmaxf(0.f, k.a * k.a + 2.f * k.b * v)));
+  Cut cut = {r, min(static_cast<int>(x), k.n - 1), 0, 1, t0, q, s, 0};
+  const int nk = la_key_tiles(p, q, s, cut.j);
+  cut.t = static_cast<int>((x - static_cast<float>(cut.j)) * static_cast<float>(nk + PAD));
+  if (cut.t >= nk) {  // behind the row tile's keys: the next one begins
+    cut.t = 0;
+    if (++cut.j >= k.n) cut = {r + 1, 0, 0, 0, 0, 0, 0, 0};
+  }
+  return cut;
+}
+
+// Cuts the batch into shares: every CTA sums the requests' costs (integers, so that all
+// agree) and finds the two cuts of its share; the first one leaves all of them for the
+// merge.  In the CTAs themselves because a kernel of its own before them, and the load
+// of what it found, put 6 us before the first copy.
+__device__ __forceinline__ void la_plan(const LaProblem& p, int share, unsigned long long* warp_sums,
+                                        Cut* mine, int* shares_out) {
+  const int tid = threadIdx.x;
+  int t0_0 = 0, q_0 = 0, s_0 = 0;  // request tid, for both passes
+  unsigned long long x_0 = 0ull, sum = 0ull, total;
+  bool bad = false;
+  for (int r = tid; r < p.B; r += LA_THREADS) {
+    int t0, q, s;
+    bad |= !la_request(p, r, t0, q, s);
+    const unsigned long long x = la_total(p, q, s);
+    sum += x;
+    if (r == tid) {
+      t0_0 = t0;
+      q_0 = q;
+      s_0 = s;
+      x_0 = x;
     }
-    if (r < p.B) prefix[r] = total + before + incl - x;
-    total += all;
+  }
+  unsigned long long before = sum_before(sum, warp_sums, total);
+  const int shares = static_cast<int>(
+      max(1ull, min(static_cast<unsigned long long>(p.max_shares), total / LEAST_SHARE)));
+  const bool first = blockIdx.x == 0;
+  if (tid == 0) {
+    *shares_out = shares;
+    mine[0] = {0, 0, 0, 0, 0, 0, 0, 0};
+    mine[1] = {p.B, 0, 0, 0, 0, 0, 0, 0};
   }
   __syncthreads();
-  const int shares = max(1, min(p.max_shares, static_cast<int>(fminf(total / LEAST_SHARE, 1e6f))));
-  if (tid == 0) {
-    p.hdr->status = bad;
-    p.hdr->shares = shares;
+  if (first) {
+    grid_dep_wait();  // (the status word is clear, and the last call's merge done)
+    if (bad) flag_status(&p.hdr->status, PATTN_DEV_BAD_METADATA);
+    if (tid == 0) {
+      p.hdr->shares = shares;
+      p.cuts[0] = {0, 0, 0, 0, 0, 0, 0, 0};
+      p.cuts[shares] = {p.B, 0, 0, 0, 0, 0, 0, 0};
+    }
   }
-  for (int c = tid; c <= shares; c += LA_PLAN_THREADS) {
-    Cut cut = {c == shares ? p.B : 0, 0, 0, 0, 0, 0, 0, 0};
-    if (c > 0 && c < shares) {
-      const float w = total * static_cast<float>(c) / static_cast<float>(shares);
-      int lo = 0, hi = p.B;  // the last request that costs begin at or before w
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= w) lo = mid;
-        else hi = mid;
+  // Pass 2: the request that weight total * c / shares falls into.
+  auto weight = [&](int c) { return total * static_cast<unsigned>(c) / static_cast<unsigned>(shares); };
+  unsigned long long done = 0ull;
+  for (int base = 0; base < p.B; base += LA_THREADS) {
+    const int r = base + tid;
+    int t0 = t0_0, q = q_0, s = s_0;
+    unsigned long long x = x_0, all;
+    if (base > 0) {
+      x = 0ull;
+      if (r < p.B) {
+        la_request(p, r, t0, q, s);
+        x = la_total(p, q, s);
       }
-      int t0, q, s;
-      la_request(p, lo, t0, q, s);
-      const Cost k = la_cost(p, q, s);
-      const float v = fmaxf(0.f, w - prefix[lo]);
-      const float x = 2.f * v / (k.a + sqrtf(fmaxf(0.f, k.a * k.a + 2.f * k.b * v)));
-      cut.r = lo;
-      cut.j = min(static_cast<int>(x), max(0, k.n - 1));
-      const int nk = la_key_tiles(p, q, s, cut.j);
-      cut.t = static_cast<int>((x - static_cast<float>(cut.j)) * static_cast<float>(nk + PAD));
-      if (k.n == 0 || cut.t >= nk) {  // behind the row tile's keys: the next one begins
-        cut.t = 0;
-        if (++cut.j >= k.n) {
-          cut.j = 0;
-          ++cut.r;
+    }
+    if (p.B > LA_THREADS) before = sum_before(x, warp_sums, all) + done;
+    if (x > 0ull) {
+      if (first) {
+        for (int c = max(1, static_cast<int>(before * shares / total)); c < shares; ++c) {
+          const unsigned long long w = weight(c);
+          if (w >= before + x) break;
+          if (w < before) continue;
+          p.cuts[c] = la_place(p, r, t0, q, s, static_cast<float>(w - before));
         }
       }
-      cut.known = cut.r == lo;
-      cut.t0 = t0;
-      cut.q = q;
-      cut.s = s;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = share + e;
+        if (c < 1 || c >= shares) continue;
+        const unsigned long long w = weight(c);
+        if (w >= before && w < before + x)
+          mine[e] = la_place(p, r, t0, q, s, static_cast<float>(w - before));
+      }
     }
-    p.cuts[c] = cut;
+    if (p.B > LA_THREADS) done += all;
   }
+  __syncthreads();
 }
 
 // ------------------------------------------------------------------ the walk
@@ -249,10 +293,6 @@ __device__ __forceinline__ Cut la_cut(const LaProblem& p, int share) {
   const int4 a = c[0], b = c[1];
   return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
-__device__ __forceinline__ Walk la_walk(const LaProblem& p, int share) {
-  return {la_cut(p, share), la_cut(p, share + 1)};
-}
-
 // The next part, or false.  lane: which row tile of a token (lanes > 1).
 __device__ __forceinline__ bool la_next(const LaProblem& p, Walk& w, int lane, Seg& g) {
   for (;;) {
@@ -310,6 +350,9 @@ struct LaBars {
   uint64_t k_full[2], k_empty[2];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, drain[2];
   float alpha[64], l[64];
+  Cut cuts[2];
+  unsigned long long sums[LA_THREADS / 32];
+  int shares;
   unsigned tmem_base;
   int abort_flag;
 };
@@ -443,11 +486,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   tc_fence_after();
   const unsigned tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
-  grid_dep_wait();  // the plan kernel's cuts
-
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
-  // (the cuts are there for every share; one past the last is not looked at)
-  const bool works = share < p.hdr->shares;
+  la_plan(p, share, bars->sums, bars->cuts, &bars->shares);
+  grid_dep_wait();  // (before the status word can be set)
+  const bool works = share < bars->shares;
   unsigned char* sQ = smem + C::Q_OFF;
   unsigned char* sP = smem + C::P_OFF;
   unsigned char* sK = smem + C::K_OFF;
@@ -464,7 +506,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     // a ring slot and posts its warp's bytes, the copies go out from one lane each.
     const int half = warp == 6 ? 1 : 0;
     const bool rot = !p.fused && half;
-    Walk w = la_walk(p, share);
+    Walk w = {bars->cuts[0], bars->cuts[1]};
     Seg g;
     int pos = 0, ok = 1;
     const int ppt = LA_KEYS / p.box;  // pages of a tile
@@ -550,7 +592,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     const uint64_t r_d = smem_desc_sw128(smem_u32(sK + (p.fused ? nc * 1024 : LA_LAT)), 16,
                                          p.fused ? cols * 1024 : 1024);
     const uint64_t v_d = smem_desc_sw128(smem_u32(sK), 1024, cols * 1024);
-    Walk w = la_walk(p, share);
+    Walk w = {bars->cuts[0], bars->cuts[1]};
     Seg g;
     int n = 0, n_seg = 0;  // tile of the CTA, parts of row tiles
     bool ok = true;
@@ -646,7 +688,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     const float sl2 = p.sl2;
     int tile = 0;
     bool ok = true;
-    Walk w = la_walk(p, share);
+    Walk w = {bars->cuts[0], bars->cuts[1]};
     Seg g;
     while (la_next(p, w, side, g)) {
       uint16_t* out = p.out + g.row0 * p.dc;
@@ -657,12 +699,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       }
       // row i of the tile sees keys below kmax
       int kmax[2] = {g.s, g.s}, first_max = g.s;
-      if (p.causal) {
-        const int64_t in_req = g.row0 - static_cast<int64_t>(g.t0) * p.H;
-        first_max = g.s - g.q + static_cast<int>(in_req / p.H) + 1;
+      if (p.causal && g.q > 1) {
+        const unsigned in_req = static_cast<unsigned>(g.row0 - static_cast<int64_t>(g.t0) * p.H);
+        const unsigned H = static_cast<unsigned>(p.H);
+        first_max = g.s - g.q + static_cast<int>(in_req / H) + 1;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          kmax[e] = min(g.s, g.s - g.q + static_cast<int>((in_req + ra + 8 * e) / p.H) + 1);
+          kmax[e] = min(g.s, g.s - g.q + static_cast<int>((in_req + ra + 8 * e) / H) + 1);
       }
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       const int n_tiles = g.k1 - g.k0;
@@ -915,16 +958,15 @@ int la_rows(int max_q, int H) {
 }
 
 struct LaLayout {
-  size_t cuts, prefix, ml, o, total;
+  size_t cuts, ml, o, total;
   int grid;
 };
-LaLayout la_layout(int B, int dc) {
+LaLayout la_layout(int dc) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   LaLayout l;
   l.grid = std::min(current_sms(), MAX_SHARES);
   l.cuts = sizeof(LaHeader);
-  l.prefix = up(l.cuts + sizeof(Cut) * (l.grid + 1));
-  l.ml = up(l.prefix + sizeof(float) * (static_cast<size_t>(B) + 1));
+  l.ml = up(l.cuts + sizeof(Cut) * (l.grid + 1));
   l.o = up(l.ml + sizeof(float2) * l.grid * 2 * 64);
   l.total = up(l.o + sizeof(float) * l.grid * 2 * 64 * dc);
   return l;
@@ -936,7 +978,7 @@ cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[4], int gri
   auto kern = latent_kernel<R, HALF>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  latent_plan_kernel<<<1, LA_PLAN_THREADS, 0, st>>>(p);
+  latent_clear_kernel<<<1, 32, 0, st>>>(p.hdr);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -972,7 +1014,7 @@ extern "C" size_t pattn_latent_workspace_bytes(int num_seqs, int num_heads, int 
   if (num_seqs < 0 || num_heads <= 0 || latent_size <= 0 || latent_size % 128 != 0 ||
       latent_size > 512)
     return 0;
-  return la_layout(num_seqs, latent_size).total;
+  return la_layout(latent_size).total;
 }
 
 extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
@@ -995,7 +1037,7 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   if (static_cast<long long>(a->num_tokens) * a->num_heads > 0x7fffff00LL ||
       static_cast<long long>(a->num_blocks) * a->block_size > 0x7fffff00LL)
     return PATTN_ERR_UNSUPPORTED;
-  const LaLayout l = la_layout(a->num_seqs, a->latent_size);
+  const LaLayout l = la_layout(a->latent_size);
   if (a->workspace_bytes < l.total) return PATTN_ERR_WORKSPACE_TOO_SMALL;
   if (a->num_seqs == 0 || a->num_tokens == 0) return PATTN_OK;
   if (a->num_blocks == 0 || a->max_blocks_per_seq == 0) return PATTN_ERR_INVALID_ARGUMENT;
@@ -1008,7 +1050,6 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   unsigned char* ws = static_cast<unsigned char*>(a->workspace);
   p.hdr = reinterpret_cast<LaHeader*>(ws);
   p.cuts = reinterpret_cast<Cut*>(ws + l.cuts);
-  p.prefix = reinterpret_cast<float*>(ws + l.prefix);
   p.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   p.part_o = reinterpret_cast<float*>(ws + l.o);
   // strictly positive, so that a masked score (-inf) always maps to weight 0; at
@@ -1025,6 +1066,7 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   p.causal = a->causal;
   p.half = a->kv_dtype == PATTN_KV_F16;
   p.R = R;
+  p.r_shift = R == 16 ? 4 : R == 32 ? 5 : 6;
   const int tiles = (a->num_heads + R - 1) / R;  // row tiles of a token
   p.lanes = a->max_query_len <= 1 && tiles > 1 && tiles <= 8 ? tiles : 1;
   p.max_shares = std::max(1, l.grid / p.lanes);
