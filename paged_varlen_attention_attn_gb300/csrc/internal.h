@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pattn.h"
 
 namespace pattn {
@@ -221,6 +223,15 @@ bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int
 // widened to 64 elements with zeros.
 bool encode_latent_maps(CUtensorMap* m, const void* q, const void* cache, bool half, int latent,
                         int rope, int q_rows, int q_box, int rows, int box);
+
+// Raises a kernel's dynamic shared memory limit to `bytes` on the current device, once:
+// `ready` holds a bit per device.  (The call costs as much as a launch; the value is
+// the same in every call, so no host thread lowers it between another's set and
+// launch.)  `again`: whatever `ready` says, for a launch that was refused because the
+// limit went with a context that is no longer current.  With threads > 0 also checks that the kernel has at least `regs` registers
+// over them (a setmaxnreg split that asked for more would wait forever).
+cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<unsigned long long>& ready,
+                                bool again, int threads = 0, int regs = 0);
 
 // Checks the sizes and the type of a cache of latent rows (host only).
 pattn_status_t check_latent_sizes(int latent_size, int rope_size, int block_size, int kv_dtype);

@@ -36,6 +36,7 @@
 // Eight warps: 0-3 softmax and epilogue, 4 and 6 TMA of the cache, 5 TMA of Q and the
 // MMAs of S, 7 the MMAs of P V.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 
@@ -65,7 +66,7 @@ struct __align__(16) Cut {
 };
 
 struct LaHeader {
-  unsigned status;
+  unsigned status;  // written by the merge: the CTAs' own words together
   int shares;  // written by the attention's first CTA, for the merge
   int pad[62];
 };
@@ -78,6 +79,7 @@ struct LaProblem {
   const int* qsl;
   uint16_t* out;
   LaHeader* hdr;
+  unsigned* cta_status;  // [grid]
   Cut* cuts;        // [shares + 1]
   float* part_o;    // [grid][2][R / 4][dc][4]: what a CTA's first and last row tile leave
   float2* part_ml;  // [grid][2][R]: their max (log2 units) and sum
@@ -149,12 +151,6 @@ __device__ __forceinline__ unsigned long long la_total(const LaProblem& p, int q
 
 // ------------------------------------------------------------------- plan
 
-// The status word, cleared before anything of the call can set it.
-__global__ void latent_clear_kernel(LaHeader* hdr) {
-  grid_dep_trigger();
-  if (threadIdx.x == 0) hdr->status = 0u;
-}
-
 // The sum of x over the CTA's threads before this one, and over all of them.
 __device__ __forceinline__ unsigned long long sum_before(unsigned long long x,
                                                          unsigned long long* warp_sums,
@@ -199,7 +195,7 @@ __device__ __forceinline__ Cut la_place(const LaProblem& p, int r, int t0, int q
 // merge.  In the CTAs themselves because a kernel of its own before them, and the load
 // of what it found, put 6 us before the first copy.
 __device__ __forceinline__ void la_plan(const LaProblem& p, int share, unsigned long long* warp_sums,
-                                        Cut* mine, int* shares_out) {
+                                        Cut* mine, int* shares_out, unsigned* status) {
   const int tid = threadIdx.x;
   int t0_0 = 0, q_0 = 0, s_0 = 0;  // request tid, for both passes
   unsigned long long x_0 = 0ull, sum = 0ull, total;
@@ -227,8 +223,7 @@ __device__ __forceinline__ void la_plan(const LaProblem& p, int share, unsigned 
   }
   __syncthreads();
   if (first) {
-    grid_dep_wait();  // (the status word is clear, and the last call's merge done)
-    if (bad) flag_status(&p.hdr->status, PATTN_DEV_BAD_METADATA);
+    if (bad) flag_status(status, PATTN_DEV_BAD_METADATA);
     if (tid == 0) {
       p.hdr->shares = shares;
       p.cuts[0] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -288,11 +283,6 @@ struct Walk {
   Cut at, end;
 };
 
-__device__ __forceinline__ Cut la_cut(const LaProblem& p, int share) {
-  const int4* c = reinterpret_cast<const int4*>(p.cuts + share);
-  const int4 a = c[0], b = c[1];
-  return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-}
 // The next part, or false.  lane: which row tile of a token (lanes > 1).
 __device__ __forceinline__ bool la_next(const LaProblem& p, Walk& w, int lane, Seg& g) {
   for (;;) {
@@ -353,6 +343,7 @@ struct LaBars {
   Cut cuts[2];
   unsigned long long sums[LA_THREADS / 32];
   int shares;
+  unsigned status;  // of this CTA
   unsigned tmem_base;
   int abort_flag;
 };
@@ -450,7 +441,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   LaBars* bars = reinterpret_cast<LaBars*>(smem + C::BAR_OFF);
-  unsigned* status = &p.hdr->status;
+  unsigned* status = &bars->status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_trigger();
 
@@ -469,6 +460,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     mbar_init(&bars->p_full, 128);
     mbar_init(&bars->pv_done, 1);
     bars->abort_flag = 0;
+    bars->status = 0u;
     fence_mbar_init();
     tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&cmap);
@@ -487,8 +479,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   const unsigned tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
-  la_plan(p, share, bars->sums, bars->cuts, &bars->shares);
-  grid_dep_wait();  // (before the status word can be set)
+  la_plan(p, share, bars->sums, bars->cuts, &bars->shares, status);
   const bool works = share < bars->shares;
   unsigned char* sQ = smem + C::Q_OFF;
   unsigned char* sP = smem + C::P_OFF;
@@ -871,6 +862,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) p.cta_status[blockIdx.x] = bars->status;
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -879,74 +871,105 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
 
 // --------------------------------------------------------------------- merge
 
-// CTA (x, y): rows 4 y .. of the row tile that the CTA x of the attention began and
-// left to the next shares, if it did.  A thread merges a dim of the four rows.
-template <bool HALF>
+// CTA (x, y): rows 4 G y .. of the row tile that the CTA x of the attention began and
+// left to the next shares, if it did.  A thread merges a dim of the 4 G rows, U parts
+// at a time with their loads in flight together.  Bound by latency: many row tiles in
+// two parts each take G 4, U 2 (64 requests on 128 heads: 22 us with G 1 and a pass
+// for the max, about 7 so), few in many parts G 1, U 8.
+template <bool HALF, int G, int U>
 __global__ void __launch_bounds__(512) latent_merge_kernel(const __grid_constant__ LaProblem p) {
   grid_dep_wait();
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
+  const int lane = threadIdx.x & 31, dim = threadIdx.x;
+  if (blockIdx.x + 1 == gridDim.x && blockIdx.y == 0 && threadIdx.x < 32) {
+    unsigned any = 0u;
+    for (unsigned i = lane; i < gridDim.x; i += 32) any |= p.cta_status[i];
+    any = __reduce_or_sync(FULL, any);
+    if (lane == 0) p.hdr->status = any;
+  }
   const int shares = p.hdr->shares;
-  const Cut a = la_cut(p, share), b = la_cut(p, share + 1);
+  // lane i: the cut i shares on
+  const int4* cuts = reinterpret_cast<const int4*>(p.cuts);
+  const int mine = min(share + lane, p.max_shares);
+  const int4 c = cuts[2 * mine], c1 = cuts[2 * mine + 1];
   if (share + 1 >= shares) return;
-  if (b.t == 0 || (a.r == b.r && a.j == b.j && a.t > 0)) return;
+  const int4 a = {__shfl_sync(FULL, c.x, 0), __shfl_sync(FULL, c.y, 0), __shfl_sync(FULL, c.z, 0), 0};
+  const int4 b = {__shfl_sync(FULL, c.x, 1), __shfl_sync(FULL, c.y, 1), __shfl_sync(FULL, c.z, 1), 0};
+  const int t0 = __shfl_sync(FULL, c1.x, 1), q = __shfl_sync(FULL, c1.y, 1);
+  if (b.z == 0 || (a.x == b.x && a.y == b.y && a.z > 0)) return;
   // (a cut inside a row tile knows its request, which is not a bad one)
-  const int64_t first = static_cast<int64_t>(p.lanes > 1 ? side : b.j) * p.R;
+  const int64_t first = static_cast<int64_t>(p.lanes > 1 ? side : b.y) * p.R;
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.R),
-                                        static_cast<int64_t>(b.q) * p.H - first));
-  const int row = blockIdx.y * 4, lane = threadIdx.x & 31, dim = threadIdx.x;
-  if (row >= rows) return;
-  int parts = 2;  // shares that hold a part of it
-  for (;;) {
-    const int c = share + parts + lane;
-    bool on = c < shares;
-    if (on) {
-      const int4 k = *reinterpret_cast<const int4*>(p.cuts + c);
-      on = k.x == b.r && k.y == b.j && k.z > 0;
-    }
-    const unsigned off = ~__ballot_sync(FULL, on);
-    parts += off ? __ffs(off) - 1 : 32;
-    if (off) break;
-  }
-  // part i's place: the second partial of the first share, the first of the others
-  auto at = [&](int i) {
-    return static_cast<int64_t>((share + i) * p.lanes + side) * 2 + (i == 0 ? 1 : 0);
+                                        static_cast<int64_t>(q) * p.H - first));
+  const int row0 = blockIdx.y * 4 * G;
+  if (row0 >= rows) return;
+  // shares that hold a part of it: the cuts behind this share that lie inside it
+  auto inside = [&](int i, const int4& k) {
+    return i < shares && k.x == b.x && k.y == b.y && k.z > 0;
   };
-  float mx[4], l[4] = {0.f, 0.f, 0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) mx[e] = -INFINITY;
-  for (int i = lane; i < parts; i += 32)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], p.part_ml[at(i) * p.R + row + e].x);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(FULL, mx[e], o));
-    if (mx[e] == -INFINITY) mx[e] = 0.f;
+  unsigned off = ~(__ballot_sync(FULL, inside(share + lane, c)) | 3u);
+  int parts = off ? __ffs(off) - 1 : 32;
+  while (!off) {
+    const int i = min(share + parts + lane, p.max_shares);
+    off = ~__ballot_sync(FULL, share + parts + lane < shares && inside(i, cuts[2 * i]));
+    parts += off ? __ffs(off) - 1 : 32;
   }
-#pragma unroll 8
-  for (int i = 0; i < parts; ++i) {
-    const float4* ml = reinterpret_cast<const float4*>(p.part_ml + at(i) * p.R + row);
-    const float4 ml0 = ml[0], ml1 = ml[1];
-    const float4 x = reinterpret_cast<const float4*>(
-        p.part_o)[(at(i) * (p.R / 4) + blockIdx.y) * p.dc + dim];
-    const float w[4] = {fast_exp2(ml0.x - mx[0]), fast_exp2(ml0.z - mx[1]),
-                        fast_exp2(ml1.x - mx[2]), fast_exp2(ml1.z - mx[3])};
-    l[0] += w[0] * ml0.y;
-    l[1] += w[1] * ml0.w;
-    l[2] += w[2] * ml1.y;
-    l[3] += w[3] * ml1.w;
-    acc[0] += w[0] * x.x;
-    acc[1] += w[1] * x.y;
-    acc[2] += w[2] * x.z;
-    acc[3] += w[3] * x.w;
-  }
-  uint16_t* out = p.out + (static_cast<int64_t>(b.t0) * p.H + first + row) * p.dc + dim;
+  float mx[G][4], l[G][4], acc[G][4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (row + e < rows) {
-      const float inv = l[e] > 0.f ? 1.f / l[e] : l[e] == 0.f ? 0.f : NAN;
-      out[static_cast<int64_t>(e) * p.dc] = static_cast<uint16_t>(pack2<HALF>(acc[e] * inv, 0.f));
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      mx[g][e] = -INFINITY;
+      l[g][e] = acc[g][e] = 0.f;
     }
+  for (int i0 = 0; i0 < parts; i0 += U) {
+    float4 x[G][U], ml[G][U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // part i's place: the second partial of the first share, the first of the others
+      const int i = min(i0 + u, parts - 1);
+      const int64_t at = static_cast<int64_t>((share + i) * p.lanes + side) * 2 + (i == 0 ? 1 : 0);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float4* s = reinterpret_cast<const float4*>(p.part_ml + at * p.R + row0 + 4 * g);
+        ml[g][u][0] = s[0];
+        ml[g][u][1] = s[1];
+        x[g][u] = reinterpret_cast<const float4*>(
+            p.part_o)[(at * (p.R / 4) + blockIdx.y * G + g) * p.dc + dim];
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        auto of = [&](const float4& v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; };
+        float top = mx[g][e];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u < parts) top = fmaxf(top, of(ml[g][u][e >> 1], 2 * (e & 1)));
+        const float ref = top == -INFINITY ? 0.f : top, was = fast_exp2(mx[g][e] - ref);
+        l[g][e] *= was;
+        acc[g][e] *= was;
+        mx[g][e] = top;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u < parts) {
+            const float w = fast_exp2(of(ml[g][u][e >> 1], 2 * (e & 1)) - ref);
+            l[g][e] += w * of(ml[g][u][e >> 1], 2 * (e & 1) + 1);
+            acc[g][e] += w * of(x[g][u], e);
+          }
+      }
+  }
+  uint16_t* out = p.out + (static_cast<int64_t>(t0) * p.H + first + row0) * p.dc + dim;
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (row0 + 4 * g + e < rows) {
+        const float s = l[g][e], inv = s > 0.f ? 1.f / s : s == 0.f ? 0.f : NAN;
+        out[static_cast<int64_t>(4 * g + e) * p.dc] =
+            static_cast<uint16_t>(pack2<HALF>(acc[g][e] * inv, 0.f));
+      }
 }
 
 // ---------------------------------------------------------------------- host
@@ -958,14 +981,15 @@ int la_rows(int max_q, int H) {
 }
 
 struct LaLayout {
-  size_t cuts, ml, o, total;
+  size_t status, cuts, ml, o, total;
   int grid;
 };
 LaLayout la_layout(int dc) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   LaLayout l;
   l.grid = std::min(current_sms(), MAX_SHARES);
-  l.cuts = sizeof(LaHeader);
+  l.status = sizeof(LaHeader);
+  l.cuts = up(l.status + sizeof(unsigned) * l.grid);
   l.ml = up(l.cuts + sizeof(Cut) * (l.grid + 1));
   l.o = up(l.ml + sizeof(float2) * l.grid * 2 * 64);
   l.total = up(l.o + sizeof(float) * l.grid * 2 * 64 * dc);
@@ -976,27 +1000,29 @@ template <int R, bool HALF>
 cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[4], int grid, cudaStream_t st) {
   using C = LaCfg<R>;
   auto kern = latent_kernel<R, HALF>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
-  latent_clear_kernel<<<1, 32, 0, st>>>(p.hdr);
-  e = cudaGetLastError();
+  static std::atomic<unsigned long long> ready{0};  // devices whose limit is set
+  cudaError_t e = cudaErrorInvalidValue;
+  for (int again = 0; again < 2 && e == cudaErrorInvalidValue; ++again) {
+    e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::SMEM, ready, again);
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(grid), LA_THREADS, C::SMEM, st>>>(p, m[0], m[1], m[2], m[3]);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(LA_THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2], m[3]);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), R / 4);
   cfg.blockDim = dim3(static_cast<unsigned>(p.dc));
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF>, p);
+  // a quarter as many row tiles as SMs and more: most of them in two parts
+  const bool many = static_cast<long long>(p.B) * p.lanes * 4 >= grid;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), many ? R / 16 : R / 4);
+  return many ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, 4, 2>, p)
+              : cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, 1, 8>, p);
 }
 
 template <int R>
@@ -1049,6 +1075,7 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   p.out = static_cast<uint16_t*>(a->out);
   unsigned char* ws = static_cast<unsigned char*>(a->workspace);
   p.hdr = reinterpret_cast<LaHeader*>(ws);
+  p.cta_status = reinterpret_cast<unsigned*>(ws + l.status);
   p.cuts = reinterpret_cast<Cut*>(ws + l.cuts);
   p.part_ml = reinterpret_cast<float2*>(ws + l.ml);
   p.part_o = reinterpret_cast<float*>(ws + l.o);

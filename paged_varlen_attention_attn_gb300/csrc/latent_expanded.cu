@@ -25,6 +25,7 @@
 // Twelve warps: 0-3 and 4-7 softmax and epilogue of the two sub-tiles, 8 TMA of Q
 // and K, 9 and 11 MMA issuers, 10 TMA of V.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 
@@ -756,16 +757,9 @@ template <int NB, bool HALF>
 cudaError_t launch_expanded(const ExProblem& p, const CUtensorMap (&m)[4], cudaStream_t st) {
   using C = ExCfg<NB>;
   auto kern = expanded_kernel<NB, HALF>;
-  cudaFuncAttributes fa;
-  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  // the register split must fit in what the CTA is launched with
-  if (static_cast<long long>(fa.numRegs) * EX_THREADS < EX_REGS_TOTAL)
-    return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
+  static std::atomic<unsigned long long> ready{0};  // devices whose limit is set
   expanded_plan_kernel<<<1, EX_PLAN_THREADS, 0, st>>>(p);
-  e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -778,7 +772,16 @@ cudaError_t launch_expanded(const ExProblem& p, const CUtensorMap (&m)[4], cudaS
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2], m[3]);
+  e = cudaErrorInvalidValue;
+  for (int again = 0; again < 2 && e == cudaErrorInvalidValue; ++again) {
+    // (with the limit: the register split must fit in what the CTA is launched with)
+    e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::SMEM, ready, again, EX_THREADS,
+                            EX_REGS_TOTAL);
+    if (e != cudaSuccess) return e;
+    e = cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2], m[3]);
+    if (e == cudaErrorInvalidValue) cudaGetLastError();
+  }
+  return e;
 }
 
 }  // namespace

@@ -434,6 +434,24 @@ bool encode_latent_maps(CUtensorMap* m, const void* q, const void* cache, bool h
          encode(&m[3], static_cast<const char*>(q) + 2 * latent, 3, td, qs, tx);
 }
 
+cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<unsigned long long>& ready,
+                                bool again, int threads, int regs) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!again && (ready.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  if (threads > 0) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    if (static_cast<long long>(attr.numRegs) * threads < regs) return cudaErrorInvalidConfiguration;
+  }
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 int current_sms() {
   static int counts[64] = {0};
   int dev = 0;

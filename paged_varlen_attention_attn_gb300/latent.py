@@ -213,9 +213,25 @@ def gather_latent(kv_cache, block_table, out_start_loc, *, num_rows, latent_size
     return latent_out, rope_out
 
 
-def _run(name, pack, args, need, workspace, dev, stream):
-    """The call with a workspace of ``need`` bytes: args(address, bytes, raw stream).
-    Returns an Ext for pattn_read_device_status."""
+_sizes = {}  # workspace bytes by (name, device index, sizes)
+
+
+def _workspace_bytes(name, dev, *sizes):
+    key = (name, dev.index, sizes)
+    need = _sizes.get(key)
+    if need is None:
+        need = _call_on(dev, getattr(load(), name), *sizes)
+        if need == 0:
+            raise PattnError(1, name)
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        _sizes[key] = need
+    return need
+
+
+def _scratch(workspace, need, dev, stream):
+    """(address, bytes, raw stream, Ext for pattn_read_device_status) of a call's
+    workspace of at least ``need`` bytes."""
     raw = _raw_stream(stream, dev)
     ws = _workspace(workspace, dev, raw)
     buf = ws.current(dev)
@@ -223,13 +239,12 @@ def _run(name, pack, args, need, workspace, dev, stream):
         buf = ws.get(need, dev, stream)
     ws.used_on(raw)
     at, size = buf.data_ptr(), buf.numel()
-    st = _call_on(dev, getattr(load(), name), _pack(pack, name, pack.size, *args(at, size, raw)))
-    if st != 0:
-        raise PattnError(st, name)
-    ext = Ext.from_buffer_copy(_pack(_EXT_PACK, name, _EXT_PACK.size, 0, 0, 0, 0, 0, 0, 0, at, size,
-                                     raw, 0, 0, 0))
-    ext._workspace_keepalive = buf  # (its status word may be read after a larger call)
-    return ext
+    ext = getattr(ws, "_ext", None)
+    if ext is None or ext.workspace != at or (ext.stream or 0) != raw:
+        ext = ws._ext = Ext.from_buffer_copy(_pack(_EXT_PACK, "workspace", _EXT_PACK.size, 0, 0, 0, 0,
+                                                   0, 0, 0, at, size, raw, 0, 0, 0))
+        ext._workspace_keepalive = buf  # (its status word may be read after a larger call)
+    return at, size, raw, ext
 
 
 def latent_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, latent_size,
@@ -261,19 +276,19 @@ def latent_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale
     if out is None:
         out = _empty((T, H, latent_size), dt, dev, stream)
     out_at = _index(out, "out", dt, (T, H, latent_size), dev)
-    lib = load()
-    need = _call_on(dev, lib.pattn_latent_workspace_bytes, B, H, int(latent_size))
-    if need == 0 or row <= latent_size:
-        raise PattnError(1, "pattn_latent_workspace_bytes")
     if T == 0 or B == 0:  # (an empty tensor has no address)
         return out
-    latent_forward.last_ext = _run(
-        "pattn_latent_fwd", _ATTEND_PACK,
-        lambda at, size, raw: (q.data_ptr(), kv_cache.data_ptr(), out_at, bt_at, sl_at, qsl_at, at,
-                               size, raw, float(scale), int(causal), int(kv_dtype), B, T, H,
-                               int(latent_size), row - int(latent_size), int(block_size), mbps, NB,
-                               int(max_query_len)),
-        need, workspace, dev, stream)
+    latent_size = int(latent_size)
+    need = _workspace_bytes("pattn_latent_workspace_bytes", dev, B, H, latent_size)
+    at, size, raw, ext = _scratch(workspace, need, dev, stream)
+    args = _pack(_ATTEND_PACK, "pattn_latent_fwd", _ATTEND_PACK.size, q.data_ptr(),
+                 kv_cache.data_ptr(), out_at, bt_at, sl_at, qsl_at, at, size, raw, float(scale),
+                 int(causal), int(kv_dtype), B, T, H, latent_size, row - latent_size,
+                 int(block_size), mbps, NB, int(max_query_len))
+    st = _call_on(dev, load().pattn_latent_fwd, args)
+    if st != 0:
+        raise PattnError(st, "pattn_latent_fwd")
+    latent_forward.last_ext = ext
     return out
 
 
@@ -311,14 +326,16 @@ def latent_expanded_forward(q, k_nope, k_rope, value, query_start_loc, key_start
     out_at = _index(out, "out", dt, (T, H, dv), dev)
     if T == 0 or B <= 0:  # (an empty tensor has no address)
         return out
-    need = load().pattn_latent_expanded_workspace_bytes(B, T)
     if K == 0:  # (likewise: no key is read)
         k_at = v_at = r_at = q_at
         k_st, k_sh, v_st, v_sh, r_st = H * dn, dn, H * dv, dv, dr
-    latent_expanded_forward.last_ext = _run(
-        "pattn_latent_expanded_fwd", _EXPANDED_PACK,
-        lambda at, size, raw: (q_at, k_at, r_at, v_at, out_at, q_st, q_sh, k_st, k_sh, r_st, v_st,
-                               v_sh, qsl_at, ksl_at, at, size, raw, float(scale), int(causal),
-                               int(kv_dtype), B, T, K, H, dn, dr, dv),
-        need, workspace, dev, stream)
+    need = load().pattn_latent_expanded_workspace_bytes(B, T)
+    at, size, raw, ext = _scratch(workspace, need, dev, stream)
+    args = _pack(_EXPANDED_PACK, "pattn_latent_expanded_fwd", _EXPANDED_PACK.size, q_at, k_at, r_at,
+                 v_at, out_at, q_st, q_sh, k_st, k_sh, r_st, v_st, v_sh, qsl_at, ksl_at, at, size,
+                 raw, float(scale), int(causal), int(kv_dtype), B, T, K, H, dn, dr, dv)
+    st = _call_on(dev, load().pattn_latent_expanded_fwd, args)
+    if st != 0:
+        raise PattnError(st, "pattn_latent_expanded_fwd")
+    latent_expanded_forward.last_ext = ext
     return out
