@@ -210,8 +210,10 @@ cudaError_t launch_cascade_merge(const float* o_a, const float* lse_a, int chunk
                                  cudaStream_t stream);
 
 // TMA tensor map over 16-bit rows [rows][heads][dim] of any head and row stride
-// (elements, multiples of 8); a box is box_rows rows of one head, 64 elements wide,
-// in the 128-byte-swizzled layout (past the row, the heads or the rows: zeros).
+// (elements, multiples of 8), as {64, row, 64-element block, head}; a box is box_rows
+// rows of one head, all blocks, which lands as [block][row][128 bytes], 128-byte
+// swizzled (past the rows: zeros).  dim: a multiple of 64, or less than 64 and widened
+// to it with zeros.
 bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int heads, int rows,
                      long long head_stride, long long row_stride, int box_rows);
 

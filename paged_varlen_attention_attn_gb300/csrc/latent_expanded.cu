@@ -42,6 +42,7 @@ constexpr int EX_REGS_TOTAL = 2 * 128 * EX_SOFTMAX_REGS + 128 * EX_OTHER_REGS;
 constexpr int EX_ROWS = 256;  // query rows of an item
 constexpr int EX_RING = 4;    // item ring
 constexpr int EX_HALF = 64;   // keys of a V stage
+constexpr int EX_VAHEAD = 3;  // V stages asked for in L2 before their copies
 constexpr float EX_RESCALE_LOG2 = 8.f;
 constexpr float EX_SUM_LIMIT = 256.f;  // 2^EX_RESCALE_LOG2
 constexpr unsigned FULL = 0xffffffffu;
@@ -291,7 +292,8 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     expanded_kernel(const __grid_constant__ ExProblem p, const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap rmap,
-                    const __grid_constant__ CUtensorMap vmap) {
+                    const __grid_constant__ CUtensorMap vmap,
+                    const __grid_constant__ CUtensorMap qrmap) {
   using C = ExCfg<NB>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -328,6 +330,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&rmap);
     tma_prefetch_desc(&vmap);
+    tma_prefetch_desc(&qrmap);
   }
   if (warp == 0) {
     tmem_alloc(&bars->tmem_base, 512);
@@ -394,10 +397,9 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           if (u.n == 0) continue;
           mbar_arrive_expect_tx(&bars->q_full[X], C::TILE);
           ++(X ? q_arms1 : q_arms0);
-#pragma unroll
-          for (int c = 0; c < C::KB; ++c)
-            tma_load_3d(sQ + X * C::TILE + c * C::BLK, &qmap, &bars->q_full[X], c * 64, it.h,
-                        it.t0 + u.i0);
+          tma_load_4d(sQ + X * C::TILE, &qmap, &bars->q_full[X], 0, it.t0 + u.i0, 0, it.h);
+          tma_load_4d(sQ + X * C::TILE + NB * C::BLK, &qrmap, &bars->q_full[X], 0, it.t0 + u.i0, 0,
+                      it.h);
         }
         for (int j = 0; j < n; ++j, ++jg) {
           const int st = jg % C::KST;
@@ -409,10 +411,8 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           mbar_arrive_expect_tx(&bars->k_full[st], C::TILE);
           armed_end = jg + 1;
           const int row = it.k0 + j * BLOCK_N;
-#pragma unroll
-          for (int c = 0; c < NB; ++c)
-            tma_load_3d(sK + st * C::TILE + c * C::BLK, &kmap, &bars->k_full[st], c * 64, it.h, row);
-          tma_load_3d(sK + st * C::TILE + NB * C::BLK, &rmap, &bars->k_full[st], 0, 0, row);
+          tma_load_4d(sK + st * C::TILE, &kmap, &bars->k_full[st], 0, row, 0, it.h);
+          tma_load_4d(sK + st * C::TILE + NB * C::BLK, &rmap, &bars->k_full[st], 0, row, 0, 0);
         }
         if (!ok) break;
         ++n_worked;
@@ -447,10 +447,10 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           }
           mbar_arrive_expect_tx(&bars->v_full[st], C::VSTAGE);
           armed_end = jg + 1;
-#pragma unroll
-          for (int c = 0; c < NB; ++c)
-            tma_load_3d(sV + st * C::VSTAGE + c * C::VBLK, &vmap, &bars->v_full[st], c * 64, it.h,
-                        it.k0 + j * EX_HALF);
+          const int row = it.k0 + j * EX_HALF;
+          tma_load_4d(sV + st * C::VSTAGE, &vmap, &bars->v_full[st], 0, row, 0, it.h);
+          // V has one tile in shared memory: the next one waits in L2
+          if (j + EX_VAHEAD < 2 * n) tma_prefetch_4d(&vmap, 0, row + EX_VAHEAD * EX_HALF, 0, it.h);
         }
       }
       if (!ok || *abort_flag) drain_armed(bars->v_full, C::VST, armed_end, -1, status);
@@ -754,7 +754,7 @@ ExLayout ex_layout(int B, int T) {
 }
 
 template <int NB, bool HALF>
-cudaError_t launch_expanded(const ExProblem& p, const CUtensorMap (&m)[4], cudaStream_t st) {
+cudaError_t launch_expanded(const ExProblem& p, const CUtensorMap (&m)[5], cudaStream_t st) {
   using C = ExCfg<NB>;
   auto kern = expanded_kernel<NB, HALF>;
   static std::atomic<unsigned long long> ready{0};  // devices whose limit is set
@@ -778,7 +778,7 @@ cudaError_t launch_expanded(const ExProblem& p, const CUtensorMap (&m)[4], cudaS
     e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::SMEM, ready, again, EX_THREADS,
                             EX_REGS_TOTAL);
     if (e != cudaSuccess) return e;
-    e = cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2], m[3]);
+    e = cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2], m[3], m[4]);
     if (e == cudaErrorInvalidValue) cudaGetLastError();
   }
   return e;
@@ -834,15 +834,17 @@ extern "C" pattn_status_t pattn_latent_expanded_fwd(const pattn_latent_expanded_
   p.sl2 = fmaxf(a->scale * LOG2E, 1e-30f);
   const bool half = a->kv_dtype == PATTN_KV_F16;
   const int H = a->num_heads, keys = std::max(1, a->num_keys);
-  CUtensorMap m[4];
-  if (!encode_rows_map(&m[0], a->q, half, a->nope_size + a->rope_size, H, a->num_tokens,
-                       a->q_head_stride, a->q_stride, BLOCK_M) ||
-      !encode_rows_map(&m[1], a->k_nope, half, a->nope_size, H, keys, a->k_head_stride, a->k_stride,
+  const int dn = a->nope_size, dr = a->rope_size;
+  const uint16_t* q_rope = static_cast<const uint16_t*>(a->q) + dn;
+  CUtensorMap m[5];
+  if (!encode_rows_map(&m[0], a->q, half, dn, H, a->num_tokens, a->q_head_stride, a->q_stride,
+                       BLOCK_M) ||
+      !encode_rows_map(&m[1], a->k_nope, half, dn, H, keys, a->k_head_stride, a->k_stride, BLOCK_N) ||
+      !encode_rows_map(&m[2], a->k_rope, half, dr, 1, keys, a->k_rope_stride, a->k_rope_stride,
                        BLOCK_N) ||
-      !encode_rows_map(&m[2], a->k_rope, half, a->rope_size, 1, keys, a->k_rope_stride,
-                       a->k_rope_stride, BLOCK_N) ||
-      !encode_rows_map(&m[3], a->value, half, a->value_size, H, keys, a->v_head_stride, a->v_stride,
-                       EX_HALF))
+      !encode_rows_map(&m[3], a->value, half, dn, H, keys, a->v_head_stride, a->v_stride, EX_HALF) ||
+      !encode_rows_map(&m[4], q_rope, half, dr, H, a->num_tokens, a->q_head_stride, a->q_stride,
+                       BLOCK_M))
     return PATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(a->stream);
   const cudaError_t e = a->nope_size == 128

@@ -385,13 +385,15 @@ bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int
                      long long head_stride, long long row_stride, int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
-                        static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[2] = {2ull * static_cast<cuuint64_t>(head_stride),
-                           2ull * static_cast<cuuint64_t>(row_stride)};
-  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+  const cuuint32_t blocks = static_cast<cuuint32_t>(std::max(1, dim / 64));
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(std::min(dim, 64)),
+                              static_cast<cuuint64_t>(rows), blocks,
+                              static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[3] = {2ull * static_cast<cuuint64_t>(row_stride), 128,
+                                 2ull * static_cast<cuuint64_t>(head_stride)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), blocks, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
