@@ -368,6 +368,39 @@ __device__ __forceinline__ void tc_mma_ss_f8(unsigned d_tmem, uint64_t a_desc, u
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// 1 in one lane of a converged warp, 0 in the others.
+__device__ __forceinline__ unsigned elect_one() {
+  unsigned r;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r));
+  return r;
+}
+// One MMA by the lane with `lead` of a converged warp (see elect_one): operands that
+// are the same in all lanes, and known to be, cost the issue a third less than from a
+// branch for one thread.
+__device__ __forceinline__ void tc_mma_ss_if(unsigned lead, unsigned d_tmem, uint64_t a_desc,
+                                             uint64_t b_desc, unsigned idesc, unsigned accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts_if(unsigned lead, unsigned d_tmem, unsigned a_tmem,
+                                             uint64_t b_desc, unsigned idesc, unsigned accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
 // One MMA, A from tensor memory, B from a shared memory descriptor.
 __device__ __forceinline__ void tc_mma_ts(unsigned d_tmem, unsigned a_tmem, uint64_t b_desc,
                                           unsigned idesc, unsigned accumulate) {

@@ -378,29 +378,6 @@ __device__ __forceinline__ void tc_ld16(unsigned taddr, float (&v)[16]) {
       : "r"(taddr));
 }
 
-// 1 in one lane of a converged warp, 0 in the others.
-__device__ __forceinline__ unsigned elect_one() {
-  unsigned r;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "elect.sync _|q, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r));
-  return r;
-}
-
-// One MMA by the lanes with `lead` (one of a converged warp).
-__device__ __forceinline__ void tc_mma_ss_if(unsigned lead, unsigned d_tmem, uint64_t a_desc,
-                                             uint64_t b_desc, unsigned idesc, unsigned accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-
 // Barrier 1 over the softmax threads; whether any of them asked.
 __device__ __forceinline__ bool any_of_128(bool ask) {
   unsigned r;

@@ -9,21 +9,27 @@
 // keys - queries + i.
 //
 // Bound by the tensor cores: 2 (dn + dr + dv) flops per pair and head, and each
-// key tile is read once per 256 rows.  Per 128 x 128 tile, S = Q K^T (dn + dr
-// deep) and O += P V are tcgen05 MMAs.  As in the paged prefill kernel of this
-// library, a persistent CTA owns two 128-row sub-tiles of one head that share
-// the key tiles and take turns on the tensor core, P stays in TMEM, the softmax
-// is online with a lazy reference max, and two threads issue the MMAs.  What
-// differs is the shared memory: Q takes (dn + 64) x 256 x 2 bytes, 96 KB at dn =
-// 128, and a whole K tile 48 KB.  Two K tiles and one V tile are left room for, so
-// V moves in halves of 64 keys: the half that both sub-tiles have used is
-// refilled while the other one is still read.
+// key tile is read once per 256 rows.  A persistent CTA owns two 128-row sub-tiles of
+// one head and walks their key tiles; S = Q K^T (dn + dr deep) and O += P V are
+// tcgen05 MMAs, P stays in TMEM, the softmax is online with a lazy reference max.
+//
+// Shared memory decides the shape.  Q takes (dn + 64) x 256 x 2 bytes, 96 KB at dn =
+// 128, and with tiles of 128 keys (48 KB of K, 32 KB of V) the two sub-tiles taking
+// turns on the tensor core, as in the paged prefill kernel of this library, a tile has
+// to stay while both use it and too little is left for the copies behind it: 1990 us
+// for 8 prompts of 1024 to 8192, 32 heads, whatever the rings were cut into.  So
+// tiles are 64 keys, each sub-tile has two score buffers in TMEM (4 x 64 columns beside
+// the 2 x dv of O), and both sub-tiles' MMAs on a tile follow each other at once: S_A,
+// S_B of tile j + 1, then P V_A, P V_B of tile j, from a warp each.  K and V then have
+// three stages, and the softmax of a tile runs under the MMAs of its neighbours.  The
+// price is S at N 64, which reads operands for 48 cycles an MMA against 32 of the
+// tensor core.
 //
 // Rotary parts shorter than 64 are widened with zeros by TMA (a box that reaches
 // past the row), so S is always a whole number of 64-element column blocks.
 //
 // Twelve warps: 0-3 and 4-7 softmax and epilogue of the two sub-tiles, 8 TMA of Q
-// and K, 9 and 11 MMA issuers, 10 TMA of V.
+// and K, 9 the MMAs of S, 10 TMA of V, 11 the MMAs of P V.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -41,8 +47,7 @@ constexpr int EX_SOFTMAX_REGS = 216, EX_OTHER_REGS = 72;  // setmaxnreg split
 constexpr int EX_REGS_TOTAL = 2 * 128 * EX_SOFTMAX_REGS + 128 * EX_OTHER_REGS;
 constexpr int EX_ROWS = 256;  // query rows of an item
 constexpr int EX_RING = 4;    // item ring
-constexpr int EX_HALF = 64;   // keys of a V stage
-constexpr int EX_VAHEAD = 3;  // V stages asked for in L2 before their copies
+constexpr int EX_KEYS = 64;   // keys of a tile
 constexpr float EX_RESCALE_LOG2 = 8.f;
 constexpr float EX_SUM_LIMIT = 256.f;  // 2^EX_RESCALE_LOG2
 constexpr unsigned FULL = 0xffffffffu;
@@ -72,26 +77,27 @@ template <int NB>
 struct ExCfg {
   static constexpr int DV = 64 * NB;
   static constexpr int KB = NB + 1;  // column blocks of q and k
-  static constexpr int BLK = BLOCK_M * 128;
-  static constexpr int TILE = KB * BLK;              // a Q or K tile
-  static constexpr int KST = 2;
-  static constexpr int VBLK = EX_HALF * 128;
-  static constexpr int VSTAGE = NB * VBLK;           // 64 keys of V
-  static constexpr int VST = NB == 2 ? 2 : 4;
-  static constexpr int Q_OFF = 0;
-  static constexpr int K_OFF = 2 * TILE;
-  static constexpr int V_OFF = K_OFF + KST * TILE;
-  static constexpr int BAR_OFF = V_OFF + VST * VSTAGE;
+  static constexpr int QBLK = BLOCK_M * 128;
+  static constexpr int QTILE = KB * QBLK;
+  static constexpr int BLK = EX_KEYS * 128;
+  static constexpr int KTILE = KB * BLK;
+  static constexpr int VTILE = NB * BLK;
+  static constexpr int ST = NB == 2 ? 3 : 4;  // stages of K and of V
+  static constexpr int K_OFF = 2 * QTILE;
+  static constexpr int V_OFF = K_OFF + ST * KTILE;
+  static constexpr int BAR_OFF = V_OFF + ST * VTILE;
   static constexpr int SMEM = BAR_OFF + 512 + 1024;
   static_assert(SMEM <= 232448 && SMEM > 118784, "one CTA fills an SM");
-  __device__ static constexpr unsigned s_col(int X) { return X ? 128u : 0u; }
+  // TMEM columns of sub-tile X's score buffer b (P takes its lower half) and output
+  __device__ static constexpr unsigned s_col(int X, int b) { return X * 128u + b * EX_KEYS; }
   __device__ static constexpr unsigned o_col(int X) { return X ? 384u : 256u; }
 };
 
 struct ExBars {
-  uint64_t q_full[2], k_full[2], k_empty[2], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], o_final[2], tok[2];
-  uint64_t q_empty, drain;
+  uint64_t q_full[2], q_empty, k_full[4], k_empty[4], v_full[4], v_empty[4];
+  // by sub-tile and score buffer: scores there, P V of the weights in it done
+  uint64_t s_full[2][2], pv_done[2][2];
+  uint64_t p_full[2], drain[2];
   uint64_t ring_full[EX_RING], ring_empty[EX_RING];
   int ring[EX_RING];
   unsigned tmem_base;
@@ -120,7 +126,7 @@ __device__ __forceinline__ void ex_clip(const ExProblem& p, int& t0, int& q) {
 
 __device__ __forceinline__ int ex_tiles_seen(const ExProblem& p, int q, int s, int row_end) {
   const int hi = p.causal ? min(s, s - q + row_end) : s;
-  return (hi + BLOCK_N - 1) / BLOCK_N;
+  return (hi + EX_KEYS - 1) / EX_KEYS;
 }
 
 constexpr int EX_BUCKETS = 2048;
@@ -305,21 +311,21 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
-      mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 2);  // both issuers release a stage
-      mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], BLOCK_M);
-      mbar_init(&bars->o_final[i], 1);
-      mbar_init(&bars->tok[i], 1);
+      mbar_init(&bars->drain[i], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars->s_full[i][b], 1);
+        mbar_init(&bars->pv_done[i][b], 1);
+      }
     }
-    for (int i = 0; i < C::VST; ++i) {
+    for (int i = 0; i < C::ST; ++i) {
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_empty[i], 1);
       mbar_init(&bars->v_full[i], 1);
-      mbar_init(&bars->v_empty[i], 2);
+      mbar_init(&bars->v_empty[i], 1);
     }
-    mbar_init(&bars->q_empty, 2);
-    mbar_init(&bars->drain, 2);
-    // the item ring: posted by warp 8; taken by warp 10, the two issuers and
-    // each softmax warp
+    mbar_init(&bars->q_empty, 1);
+    // the item ring: posted by warp 8; taken by warps 9 to 11 and each softmax warp
     for (int i = 0; i < EX_RING; ++i) {
       mbar_init(&bars->ring_full[i], 1);
       mbar_init(&bars->ring_empty[i], 3 + 8);
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   };
   auto release = [&](int k) { mbar_arrive(&bars->ring_empty[k % EX_RING]); };
 
-  unsigned char* sQ = smem + C::Q_OFF;
+  unsigned char* sQ = smem;
   unsigned char* sK = smem + C::K_OFF;
   unsigned char* sV = smem + C::V_OFF;
 
@@ -395,24 +401,24 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         for (int X = 0; X < 2; ++X) {
           const ExSub& u = X ? b : a;
           if (u.n == 0) continue;
-          mbar_arrive_expect_tx(&bars->q_full[X], C::TILE);
+          mbar_arrive_expect_tx(&bars->q_full[X], C::QTILE);
           ++(X ? q_arms1 : q_arms0);
-          tma_load_4d(sQ + X * C::TILE, &qmap, &bars->q_full[X], 0, it.t0 + u.i0, 0, it.h);
-          tma_load_4d(sQ + X * C::TILE + NB * C::BLK, &qrmap, &bars->q_full[X], 0, it.t0 + u.i0, 0,
-                      it.h);
+          tma_load_4d(sQ + X * C::QTILE, &qmap, &bars->q_full[X], 0, it.t0 + u.i0, 0, it.h);
+          tma_load_4d(sQ + X * C::QTILE + NB * C::QBLK, &qrmap, &bars->q_full[X], 0, it.t0 + u.i0,
+                      0, it.h);
         }
         for (int j = 0; j < n; ++j, ++jg) {
-          const int st = jg % C::KST;
-          if (jg >= C::KST &&
-              !mbar_wait(&bars->k_empty[st], ((jg / C::KST) - 1) & 1, status, abort_flag)) {
+          const int st = jg % C::ST;
+          if (jg >= C::ST &&
+              !mbar_wait(&bars->k_empty[st], ((jg / C::ST) - 1) & 1, status, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&bars->k_full[st], C::TILE);
+          mbar_arrive_expect_tx(&bars->k_full[st], C::KTILE);
           armed_end = jg + 1;
-          const int row = it.k0 + j * BLOCK_N;
-          tma_load_4d(sK + st * C::TILE, &kmap, &bars->k_full[st], 0, row, 0, it.h);
-          tma_load_4d(sK + st * C::TILE + NB * C::BLK, &rmap, &bars->k_full[st], 0, row, 0, 0);
+          const int row = it.k0 + j * EX_KEYS;
+          tma_load_4d(sK + st * C::KTILE, &kmap, &bars->k_full[st], 0, row, 0, it.h);
+          tma_load_4d(sK + st * C::KTILE + NB * C::BLK, &rmap, &bars->k_full[st], 0, row, 0, 0);
         }
         if (!ok) break;
         ++n_worked;
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       // A role gave up on a wait: no copy may still be writing shared memory when
       // the CTA exits.
       if (!ok || idx < 0 || *abort_flag) {
-        drain_armed(bars->k_full, C::KST, armed_end, -1, status);
+        drain_armed(bars->k_full, C::ST, armed_end, -1, status);
         if (q_arms0 > 0) mbar_wait(&bars->q_full[0], (q_arms0 - 1) & 1, status, nullptr);
         if (q_arms1 > 0) mbar_wait(&bars->q_full[1], (q_arms1 - 1) & 1, status, nullptr);
       }
@@ -438,128 +444,128 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         const ExItem it = ex_load_item(p, idx, n_items);
         if (!it.live) break;
         const int n = max(ex_sub(p, it, 0).n, ex_sub(p, it, 1).n);
-        for (int j = 0; j < 2 * n; ++j, ++jg) {
-          const int st = jg % C::VST;
-          if (jg >= C::VST &&
-              !mbar_wait(&bars->v_empty[st], ((jg / C::VST) - 1) & 1, status, abort_flag)) {
+        for (int j = 0; j < n; ++j, ++jg) {
+          const int st = jg % C::ST;
+          if (jg >= C::ST &&
+              !mbar_wait(&bars->v_empty[st], ((jg / C::ST) - 1) & 1, status, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&bars->v_full[st], C::VSTAGE);
+          mbar_arrive_expect_tx(&bars->v_full[st], C::VTILE);
           armed_end = jg + 1;
-          const int row = it.k0 + j * EX_HALF;
-          tma_load_4d(sV + st * C::VSTAGE, &vmap, &bars->v_full[st], 0, row, 0, it.h);
-          // V has one tile in shared memory: the next one waits in L2
-          if (j + EX_VAHEAD < 2 * n) tma_prefetch_4d(&vmap, 0, row + EX_VAHEAD * EX_HALF, 0, it.h);
+          tma_load_4d(sV + st * C::VTILE, &vmap, &bars->v_full[st], 0, it.k0 + j * EX_KEYS, 0, it.h);
         }
       }
-      if (!ok || *abort_flag) drain_armed(bars->v_full, C::VST, armed_end, -1, status);
-    } else if ((warp == 9 || warp == 11) && lane == 0) {
-      // -------------------------------------------------------- MMA issuers
-      // Warp 9 issues sub-tile A's MMAs, warp 11 B's, in turns handed over through
-      // tok[]: an MMA holds its issuing thread for about as long as it runs, so
-      // each waits for its operands and commits while the other one issues.
-      const int X = warp == 11 ? 1 : 0;
-      constexpr unsigned idesc_s = make_idesc_f16(BLOCK_M, BLOCK_N, !HALF, false);
+      if (!ok || *abort_flag) drain_armed(bars->v_full, C::ST, armed_end, -1, status);
+    } else if (warp == 9 || warp == 11) {
+      // ---------------------------------------------------------------- MMAs
+      // The whole warp walks, with what the descriptors are made of known to be the
+      // same in all lanes, and the elected lane issues.
+      const bool scores = warp == 9;
+      const unsigned lead = elect_one();
+      constexpr unsigned idesc_s = make_idesc_f16(BLOCK_M, EX_KEYS, !HALF, false);
       constexpr unsigned idesc_pv = make_idesc_f16(BLOCK_M, C::DV, !HALF, true);
-      const uint64_t q_d = smem_desc_sw128(smem_u32(sQ + X * C::TILE), 16, 1024);
+      const unsigned t_base = __reduce_max_sync(FULL, tmem);
+      const uint64_t q_d = smem_desc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t k_d = smem_desc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t v_d = smem_desc_sw128(smem_u32(sV), C::VBLK, 1024);
-      int jg = 0, pv_tot = 0, q_tot = 0;
-      unsigned turn = 0;
+      const uint64_t v_d = smem_desc_sw128(smem_u32(sV), C::BLK, 1024);
+      int jg = 0;                  // key tiles so far (ring position)
+      int cnt0 = 0, cnt1 = 0;      // of sub-tile X (its score buffer and phase)
+      int q_tot0 = 0, q_tot1 = 0;  // Q tiles of sub-tile X
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int idx = take(k);
-        if (idx < 0) break;
-        release(k);
+        if (!__all_sync(FULL, idx >= 0)) break;
+        if (lane == 0) release(k);
         const ExItem it = ex_load_item(p, idx, n_items);
-        if (!it.live) break;
-        const ExSub u = ex_sub(p, it, X);
-        const int n = max(u.n, ex_sub(p, it, 1 - X).n);
-        if (n == 0) continue;
-        for (int j = 0; j <= n; ++j, ++turn) {
-          const int jj = jg + j;
-          const bool do_pv = j >= 1 && j - 1 < u.n, do_s = j < u.n;
-          const int st = jj % C::KST;
-          const int vp = 2 * (jj - 1);  // V ring position of the previous tile's first half
-          if (do_pv && !(mbar_wait(&bars->p_full[X], pv_tot & 1, status, abort_flag) &&
-                         mbar_wait(&bars->v_full[vp % C::VST], (vp / C::VST) & 1, status,
-                                   abort_flag))) {
+        if (!__any_sync(FULL, it.live)) break;
+        const int na = static_cast<int>(__reduce_max_sync(FULL, static_cast<unsigned>(ex_sub(p, it, 0).n)));
+        const int nb = static_cast<int>(__reduce_max_sync(FULL, static_cast<unsigned>(ex_sub(p, it, 1).n)));
+        const int n = max(na, nb);
+        for (int j = 0; ok && j < n; ++j, ++jg) {
+          const int st = jg % C::ST;
+          const unsigned ph = (jg / C::ST) & 1;
+          if (!__all_sync(FULL, mbar_wait(scores ? &bars->k_full[st] : &bars->v_full[st], ph, status,
+                                          abort_flag))) {
             ok = false;
             break;
           }
-          if (do_s) {
-            if (!mbar_wait(&bars->k_full[st], (jj / C::KST) & 1, status, abort_flag) ||
-                (j == 0 && !mbar_wait(&bars->q_full[X], q_tot & 1, status, abort_flag))) {
+          // V rows at or past the request's keys become zero: they may hold anything, and
+          // 0 * NaN is NaN.
+          const int rows = it.s - j * EX_KEYS;
+          if (!scores && rows < EX_KEYS) {
+            for (int e = lane; e < (EX_KEYS - rows) * 8 * NB; e += 32) {
+              const int r = rows + e / (8 * NB), x = e % (8 * NB);
+              *reinterpret_cast<uint4*>(sV + st * C::VTILE + (x >> 3) * C::BLK + r * 128 +
+                                        (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int X = 0; X < 2; ++X) {
+            if (j >= (X ? nb : na)) continue;
+            int& cnt = X ? cnt1 : cnt0;
+            int& q_tot = X ? q_tot1 : q_tot0;
+            const int b = cnt & 1;
+            bool there = true;
+            if (scores) {
+              // the buffer's last weights are used, and Q is there
+              if (cnt >= 2)
+                there = mbar_wait(&bars->pv_done[X][b], ((cnt >> 1) - 1) & 1, status, abort_flag);
+              if (j == 0) {
+                there = there && mbar_wait(&bars->q_full[X], q_tot & 1, status, abort_flag);
+                ++q_tot;
+              }
+            } else {
+              there = mbar_wait(&bars->p_full[X], cnt & 1, status, abort_flag);
+            }
+            if (!__all_sync(FULL, there)) {
               ok = false;
               break;
             }
-            if (j == 0) ++q_tot;
-          }
-          // A's turn t follows B's turn t - 1, B's turn t follows A's turn t
-          if ((X == 1 || turn > 0) &&
-              !mbar_wait(&bars->tok[X], (X ? turn : turn - 1) & 1, status, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          // opaque base addresses: their per-MMA offsets are added at each use
-          // instead of being hoisted out of the loops as live registers
-          uint64_t qb = q_d;
-          unsigned s_t = tmem + C::s_col(X), o_t = tmem + C::o_col(X);
-          asm volatile("" : "+l"(qb), "+r"(s_t), "+r"(o_t));
-          const uint64_t kb = k_d + ((st * C::TILE) >> 4);
-          if (do_pv) {
+            tc_fence_after();
+            const unsigned s_t = t_base + X * 128u + b * EX_KEYS;
+            if (scores) {
+              const uint64_t qb = q_d + ((X * C::QTILE) >> 4), kb = k_d + ((st * C::KTILE) >> 4);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              if (hf && !mbar_wait(&bars->v_full[(vp + 1) % C::VST], ((vp + 1) / C::VST) & 1, status,
-                                   abort_flag)) {
-                ok = false;
-                break;
-              }
-              const uint64_t vb = v_d + ((((vp + hf) % C::VST) * C::VSTAGE) >> 4);
+              for (int kk = 0; kk < 4 * C::KB; ++kk)
+                tc_mma_ss_if(lead, s_t, qb + (((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4),
+                             kb + (((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4), idesc_s,
+                             kk > 0 ? 1u : 0u);
+              if (lead) tc_commit(&bars->s_full[X][b]);
+            } else {
+              const uint64_t vb = v_d + ((st * C::VTILE) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_ts(o_t, s_t + (hf * 4 + kk) * 8, vb + ((kk * 2048) >> 4), idesc_pv,
-                          (j > 1 || hf > 0 || kk > 0) ? 1u : 0u);
-              if (hf == 0) tc_commit(&bars->v_empty[vp % C::VST]);
+              for (int kk = 0; kk < EX_KEYS / 16; ++kk)
+                tc_mma_ts_if(lead, t_base + C::o_col(X), s_t + kk * 8, vb + ((kk * 2048) >> 4),
+                             idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+              if (lead) tc_commit(&bars->pv_done[X][b]);
             }
-            if (!ok) break;
+            ++cnt;
           }
-          if (do_s) {
-#pragma unroll
-            for (int kk = 0; kk < 4 * C::KB; ++kk) {
-              const unsigned off = ((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4;
-              tc_mma_ss(s_t, qb + off, kb + off, idesc_s, kk > 0 ? 1u : 0u);
-            }
+          if (!ok) break;
+          if (lead) {
+            tc_commit(scores ? &bars->k_empty[st] : &bars->v_empty[st]);
+            if (scores && j == n - 1) tc_commit(&bars->q_empty);
           }
-          mbar_arrive(&bars->tok[1 - X]);  // the other issuer's turn
-          if (do_pv) ++pv_tot;
-          // commits, while the other issuer's MMAs run; both release every stage
-          if (do_s) tc_commit(&bars->s_full[X]);
-          if (do_pv && j == u.n) tc_commit(&bars->o_final[X]);
-          if (j >= 1) {
-            if (!do_pv) tc_commit(&bars->v_empty[vp % C::VST]);
-            tc_commit(&bars->v_empty[(vp + 1) % C::VST]);
-          }
-          if (j < n) tc_commit(&bars->k_empty[st]);
-          if (j == n - 1) tc_commit(&bars->q_empty);
         }
-        jg += n;
       }
       // no MMA may still be running when TMEM is released
-      tc_commit(&bars->drain);
-      mbar_wait(&bars->drain, 0, status, nullptr);
+      if (lead) {
+        tc_commit(&bars->drain[scores ? 0 : 1]);
+        mbar_wait(&bars->drain[scores ? 0 : 1], 0, status, nullptr);
+      }
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EX_SOFTMAX_REGS));
     // ------------------------------------------------------------ softmax
     const int X = warp >> 2, row = threadIdx.x & 127;
     const unsigned lane_base = tmem + (static_cast<unsigned>((warp & 3) * 32) << 16);
-    const unsigned s_t = lane_base + C::s_col(X), o_t = lane_base + C::o_col(X);
+    const unsigned o_t = lane_base + C::o_col(X);
     const float sl2 = p.sl2;
-    unsigned s_ph = 0, o_ph = 0;
-    int jg = 0;  // key tiles of the items so far (ring position)
+    int cnt = 0;  // key tiles of this sub-tile so far (score buffer and phase)
     bool ok = true;
     for (int k = 0;; ++k) {
       const int idx = take(k);
@@ -568,25 +574,21 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       const ExItem it = ex_load_item(p, idx, n_items);
       if (!it.live) break;
       const ExSub u = ex_sub(p, it, X);
-      const int n_other = ex_sub(p, it, 1 - X).n;
       const int i = u.i0 + row, s = it.s;
       const bool row_ok = i < it.q;
       // row i sees keys below kmax; a tile past `edge` needs the mask
       const int kmax = p.causal ? min(s, s - it.q + i + 1) : s;
-      const int edge = min(s, p.causal ? s - it.q + u.i0 + 1 : s) - BLOCK_N;
-      // V rows at or past the request's keys are zeroed by the first sub-tile whose
-      // P V reads them (they may hold anything, and 0 * NaN is NaN)
-      const int tail = (s - 1) / BLOCK_N;
-      const bool zeroes = s > 0 && s % BLOCK_N != 0 && tail < u.n && (X == 0 || tail >= n_other);
+      const int edge = min(s, p.causal ? s - it.q + u.i0 + 1 : s) - EX_KEYS;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < u.n; ++j) {
-        if (!__all_sync(FULL, mbar_wait(&bars->s_full[X], s_ph, status, abort_flag))) {
+      for (int j = 0; j < u.n; ++j, ++cnt) {
+        const int b = cnt & 1;
+        if (!__all_sync(FULL, mbar_wait(&bars->s_full[X][b], (cnt >> 1) & 1, status, abort_flag))) {
           ok = false;
           break;
         }
-        s_ph ^= 1;
         tc_fence_after();
-        const int key0 = j * BLOCK_N, lim = kmax - key0;
+        const unsigned s_t = lane_base + C::s_col(X, b);
+        const int key0 = j * EX_KEYS, lim = kmax - key0;
         const bool masked = key0 > edge;
         // Common case: the reference stays; the weights against it are computed in
         // registers, and if any exceeded 2^EX_RESCALE_LOG2 their sum did too and
@@ -594,47 +596,47 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         bool slow = m_run == -INFINITY;
         float ps = 0.f;
         if (!__any_sync(FULL, slow)) {
-          float sv[BLOCK_N];
+          float sv[EX_KEYS];
 #pragma unroll
-          for (int g = 0; g < BLOCK_N / 32; ++g)
+          for (int g = 0; g < EX_KEYS / 32; ++g)
             tc_ld32(s_t + g * 32, *reinterpret_cast<float(*)[32]>(&sv[g * 32]));
           tc_wait_ld();
           if (masked) {
 #pragma unroll
-            for (int q = 0; q < BLOCK_N; ++q) sv[q] = q < lim ? sv[q] : -INFINITY;
+            for (int q = 0; q < EX_KEYS; ++q) sv[q] = q < lim ? sv[q] : -INFINITY;
           }
-          unsigned pk[BLOCK_N / 2];
+          unsigned pk[EX_KEYS / 2];
 #pragma unroll
-          for (int g = 0; g < BLOCK_N / 32; ++g)
+          for (int g = 0; g < EX_KEYS / 32; ++g)
             ps += ex_weights<HALF>(*reinterpret_cast<const float(*)[32]>(&sv[g * 32]), sl2, m_run,
                                    *reinterpret_cast<unsigned(*)[16]>(&pk[g * 16]));
           slow = !(ps <= EX_SUM_LIMIT);
           if (!__any_sync(FULL, slow)) {
 #pragma unroll
-            for (int g = 0; g < BLOCK_N / 32; ++g)
+            for (int g = 0; g < EX_KEYS / 32; ++g)
               tc_st16u(s_t + g * 16, *reinterpret_cast<const unsigned(*)[16]>(&pk[g * 16]));
           }
         }
         if (__any_sync(FULL, slow)) {
-          float sv[BLOCK_N];  // the scores again: nothing was stored over them
+          float sv[EX_KEYS];  // the scores again: nothing was stored over them
 #pragma unroll
-          for (int g = 0; g < BLOCK_N / 32; ++g)
+          for (int g = 0; g < EX_KEYS / 32; ++g)
             tc_ld32(s_t + g * 32, *reinterpret_cast<float(*)[32]>(&sv[g * 32]));
           tc_wait_ld();
           if (masked) {
 #pragma unroll
-            for (int q = 0; q < BLOCK_N; ++q) sv[q] = q < lim ? sv[q] : -INFINITY;
+            for (int q = 0; q < EX_KEYS; ++q) sv[q] = q < lim ? sv[q] : -INFINITY;
           }
           float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-          for (int q = 4; q < BLOCK_N - 4; q += 8) {
+          for (int q = 4; q < EX_KEYS - 4; q += 8) {
             m4[0] = max3(m4[0], sv[q + 0], sv[q + 1]);
             m4[1] = max3(m4[1], sv[q + 2], sv[q + 3]);
             m4[2] = max3(m4[2], sv[q + 4], sv[q + 5]);
             m4[3] = max3(m4[3], sv[q + 6], sv[q + 7]);
           }
-          m4[0] = max3(m4[0], sv[BLOCK_N - 4], sv[BLOCK_N - 3]);
-          m4[1] = max3(m4[1], sv[BLOCK_N - 2], sv[BLOCK_N - 1]);
+          m4[0] = max3(m4[0], sv[EX_KEYS - 4], sv[EX_KEYS - 3]);
+          m4[1] = max3(m4[1], sv[EX_KEYS - 2], sv[EX_KEYS - 1]);
           const float mx = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
           const float mx_s = mx == -INFINITY ? -INFINITY : mx * sl2;
           // the reference moves only where a row max grows by more than
@@ -650,15 +652,20 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           const float ref = m_run == -INFINITY ? 0.f : m_run;
           ps = 0.f;
 #pragma unroll
-          for (int g = 0; g < BLOCK_N / 32; ++g) {
+          for (int g = 0; g < EX_KEYS / 32; ++g) {
             unsigned pk[16];
             ps += ex_weights<HALF>(*reinterpret_cast<const float(*)[32]>(&sv[g * 32]), sl2, ref, pk);
             tc_st16u(s_t + g * 16, pk);
           }
-          // O is rescaled last, once the score registers are free.  P V of the
-          // previous tile is complete: the commit that announced these scores
-          // was issued after it.
+          // O is rescaled last, once the score registers are free and P V of the
+          // previous tile is in it.
           if (__any_sync(FULL, need_o)) {
+            if (!__all_sync(FULL, mbar_wait(&bars->pv_done[X][b ^ 1], ((cnt - 1) >> 1) & 1, status,
+                                            abort_flag))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
             const float a = need_o ? alpha : 1.f;
 #pragma unroll
             for (int q = 0; q < C::DV / 32; ++q) {
@@ -673,37 +680,17 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         }
         l_run += ps;
         tc_wait_st();
-        if (zeroes && j == tail) {
-          const int vp = 2 * (jg + j);
-          for (int hf = 0; hf < 2; ++hf) {
-            if (!__all_sync(FULL, mbar_wait(&bars->v_full[(vp + hf) % C::VST],
-                                            ((vp + hf) / C::VST) & 1, status, abort_flag))) {
-              ok = false;
-              break;
-            }
-          }
-          if (!ok) break;
-          if (row >= s - key0) {
-            unsigned char* v = sV + ((vp + row / EX_HALF) % C::VST) * C::VSTAGE + (row % EX_HALF) * 128;
-#pragma unroll
-            for (int c = 0; c < NB; ++c)
-#pragma unroll
-              for (int b = 0; b < 128; b += 16)
-                *reinterpret_cast<uint4*>(v + c * C::VBLK + b) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-        }
         tc_fence_before();
         mbar_arrive(&bars->p_full[X]);
       }
       if (!ok) break;
-      jg += max(u.n, n_other);
 
       // --------------------------------------------------------- epilogue
       if (!u.valid) continue;
       if (u.n > 0) {
-        if (!__all_sync(FULL, mbar_wait(&bars->o_final[X], o_ph, status, abort_flag))) break;
-        o_ph ^= 1;
+        if (!__all_sync(FULL, mbar_wait(&bars->pv_done[X][(cnt - 1) & 1], ((cnt - 1) >> 1) & 1,
+                                        status, abort_flag)))
+          break;
         tc_fence_after();
       }
       const float inv = l_run > 0.f ? 1.f / l_run : l_run == 0.f ? 0.f : NAN;
@@ -839,10 +826,10 @@ extern "C" pattn_status_t pattn_latent_expanded_fwd(const pattn_latent_expanded_
   CUtensorMap m[5];
   if (!encode_rows_map(&m[0], a->q, half, dn, H, a->num_tokens, a->q_head_stride, a->q_stride,
                        BLOCK_M) ||
-      !encode_rows_map(&m[1], a->k_nope, half, dn, H, keys, a->k_head_stride, a->k_stride, BLOCK_N) ||
+      !encode_rows_map(&m[1], a->k_nope, half, dn, H, keys, a->k_head_stride, a->k_stride, EX_KEYS) ||
       !encode_rows_map(&m[2], a->k_rope, half, dr, 1, keys, a->k_rope_stride, a->k_rope_stride,
-                       BLOCK_N) ||
-      !encode_rows_map(&m[3], a->value, half, dn, H, keys, a->v_head_stride, a->v_stride, EX_HALF) ||
+                       EX_KEYS) ||
+      !encode_rows_map(&m[3], a->value, half, dn, H, keys, a->v_head_stride, a->v_stride, EX_KEYS) ||
       !encode_rows_map(&m[4], q_rope, half, dr, H, a->num_tokens, a->q_head_stride, a->q_stride,
                        BLOCK_M))
     return PATTN_ERR_CUDA;
