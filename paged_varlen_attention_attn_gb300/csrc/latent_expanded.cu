@@ -28,8 +28,9 @@
 // Rotary parts shorter than 64 are widened with zeros by TMA (a box that reaches
 // past the row), so S is always a whole number of 64-element column blocks.
 //
-// Twelve warps: 0-3 and 4-7 softmax and epilogue of the two sub-tiles, 8 TMA of Q
-// and K, 9 the MMAs of S, 10 TMA of V, 11 the MMAs of P V.
+// Sixteen warps: 0-3 and 4-7 softmax and epilogue of the two sub-tiles, 8 TMA of Q
+// and K, 9 TMA of V, 10 and 11 the MMAs of S of each sub-tile, 12 and 13 those of P V
+// (14 and 15 leave at once).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -42,9 +43,9 @@
 namespace pattn {
 namespace {
 
-constexpr int EX_THREADS = 384;
-constexpr int EX_SOFTMAX_REGS = 216, EX_OTHER_REGS = 72;  // setmaxnreg split
-constexpr int EX_REGS_TOTAL = 2 * 128 * EX_SOFTMAX_REGS + 128 * EX_OTHER_REGS;
+constexpr int EX_THREADS = 512;
+constexpr int EX_SOFTMAX_REGS = 184, EX_OTHER_REGS = 72;  // setmaxnreg split
+constexpr int EX_REGS_TOTAL = 2 * 128 * (EX_SOFTMAX_REGS + EX_OTHER_REGS);
 constexpr int EX_ROWS = 256;  // query rows of an item
 constexpr int EX_RING = 4;    // item ring
 constexpr int EX_KEYS = 64;   // keys of a tile
@@ -95,9 +96,10 @@ struct ExCfg {
 
 struct ExBars {
   uint64_t q_full[2], q_empty, k_full[4], k_empty[4], v_full[4], v_empty[4];
-  // by sub-tile and score buffer: scores there, P V of the weights in it done
-  uint64_t s_full[2][2], pv_done[2][2];
-  uint64_t p_full[2], drain[2];
+  // by sub-tile and score buffer (a phase of one waits for the last one's reader):
+  // scores there, weights there, P V of the weights done
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];
+  uint64_t drain[4];
   uint64_t ring_full[EX_RING], ring_empty[EX_RING];
   int ring[EX_RING];
   unsigned tmem_base;
@@ -311,24 +313,25 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->q_full[i], 1);
-      mbar_init(&bars->p_full[i], BLOCK_M);
       mbar_init(&bars->drain[i], 1);
+      mbar_init(&bars->drain[2 + i], 1);
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bars->s_full[i][b], 1);
+        mbar_init(&bars->p_full[i][b], BLOCK_M);
         mbar_init(&bars->pv_done[i][b], 1);
       }
     }
     for (int i = 0; i < C::ST; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->k_empty[i], 2);  // one arrival of each sub-tile
       mbar_init(&bars->v_full[i], 1);
-      mbar_init(&bars->v_empty[i], 1);
+      mbar_init(&bars->v_empty[i], 2);
     }
-    mbar_init(&bars->q_empty, 1);
-    // the item ring: posted by warp 8; taken by warps 9 to 11 and each softmax warp
+    mbar_init(&bars->q_empty, 2);
+    // the item ring: posted by warp 8; taken by warps 9 to 13 and each softmax warp
     for (int i = 0; i < EX_RING; ++i) {
       mbar_init(&bars->ring_full[i], 1);
-      mbar_init(&bars->ring_empty[i], 3 + 8);
+      mbar_init(&bars->ring_empty[i], 5 + 8);
     }
     bars->abort_flag = 0;
     fence_mbar_init();
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         if (q_arms0 > 0) mbar_wait(&bars->q_full[0], (q_arms0 - 1) & 1, status, nullptr);
         if (q_arms1 > 0) mbar_wait(&bars->q_full[1], (q_arms1 - 1) & 1, status, nullptr);
       }
-    } else if (warp == 10 && lane == 0) {
+    } else if (warp == 9 && lane == 0) {
       // ------------------------------------------------------------------ V
       int jg = 0, armed_end = 0;
       bool ok = true;
@@ -457,21 +460,23 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         }
       }
       if (!ok || *abort_flag) drain_armed(bars->v_full, C::ST, armed_end, -1, status);
-    } else if (warp == 9 || warp == 11) {
+    } else if (warp >= 10 && warp < 14) {
       // ---------------------------------------------------------------- MMAs
-      // The whole warp walks, with what the descriptors are made of known to be the
-      // same in all lanes, and the elected lane issues.
-      const bool scores = warp == 9;
+      // A warp each for S and for P V of each sub-tile, so that one's waits and commits
+      // pass under the others' MMAs.  The whole warp walks, with what the descriptors
+      // are made of known to be the same in all lanes, and the elected lane issues.
+      const bool scores = warp < 12;
+      const int X = warp & 1;
       const unsigned lead = elect_one();
       constexpr unsigned idesc_s = make_idesc_f16(BLOCK_M, EX_KEYS, !HALF, false);
       constexpr unsigned idesc_pv = make_idesc_f16(BLOCK_M, C::DV, !HALF, true);
       const unsigned t_base = __reduce_max_sync(FULL, tmem);
-      const uint64_t q_d = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t q_d = smem_desc_sw128(smem_u32(sQ + X * C::QTILE), 16, 1024);
       const uint64_t k_d = smem_desc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t v_d = smem_desc_sw128(smem_u32(sV), C::BLK, 1024);
-      int jg = 0;                  // key tiles so far (ring position)
-      int cnt0 = 0, cnt1 = 0;      // of sub-tile X (its score buffer and phase)
-      int q_tot0 = 0, q_tot1 = 0;  // Q tiles of sub-tile X
+      int jg = 0;     // key tiles of the items so far (ring position)
+      int cnt = 0;    // of this sub-tile (its score buffer and phase)
+      int q_tot = 0;  // its Q tiles
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int idx = take(k);
@@ -479,82 +484,74 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         if (lane == 0) release(k);
         const ExItem it = ex_load_item(p, idx, n_items);
         if (!__any_sync(FULL, it.live)) break;
-        const int na = static_cast<int>(__reduce_max_sync(FULL, static_cast<unsigned>(ex_sub(p, it, 0).n)));
-        const int nb = static_cast<int>(__reduce_max_sync(FULL, static_cast<unsigned>(ex_sub(p, it, 1).n)));
-        const int n = max(na, nb);
-        for (int j = 0; ok && j < n; ++j, ++jg) {
-          const int st = jg % C::ST;
-          const unsigned ph = (jg / C::ST) & 1;
-          if (!__all_sync(FULL, mbar_wait(scores ? &bars->k_full[st] : &bars->v_full[st], ph, status,
-                                          abort_flag))) {
+        const int mine = static_cast<int>(
+            __reduce_max_sync(FULL, static_cast<unsigned>(ex_sub(p, it, X).n)));
+        const int n = max(mine, static_cast<int>(__reduce_max_sync(
+                                    FULL, static_cast<unsigned>(ex_sub(p, it, 1 - X).n))));
+        if (n == 0) continue;
+        if (scores && mine > 0) {
+          if (!__all_sync(FULL, mbar_wait(&bars->q_full[X], q_tot & 1, status, abort_flag))) break;
+          ++q_tot;
+        }
+        for (int j = 0; j < n; ++j, ++jg) {
+          const int st = jg % C::ST, b = cnt & 1;
+          const bool active = j < mine;
+          uint64_t* empty = scores ? &bars->k_empty[st] : &bars->v_empty[st];
+          bool there = mbar_wait(scores ? &bars->k_full[st] : &bars->v_full[st], (jg / C::ST) & 1,
+                                 status, abort_flag);
+          if (active && scores && cnt >= 2)  // the buffer's last weights are used
+            there = there &&
+                    mbar_wait(&bars->pv_done[X][b], ((cnt >> 1) - 1) & 1, status, abort_flag);
+          if (active && !scores)
+            there = there && mbar_wait(&bars->p_full[X][b], (cnt >> 1) & 1, status, abort_flag);
+          if (!__all_sync(FULL, there)) {
             ok = false;
             break;
           }
-          // V rows at or past the request's keys become zero: they may hold anything, and
-          // 0 * NaN is NaN.
-          const int rows = it.s - j * EX_KEYS;
-          if (!scores && rows < EX_KEYS) {
-            for (int e = lane; e < (EX_KEYS - rows) * 8 * NB; e += 32) {
-              const int r = rows + e / (8 * NB), x = e % (8 * NB);
-              *reinterpret_cast<uint4*>(sV + st * C::VTILE + (x >> 3) * C::BLK + r * 128 +
-                                        (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+          if (!active) {  // nothing for this sub-tile (released only now that it is full:
+                          // the barrier counts one arrival of each sub-tile per phase)
+            if (lead) mbar_arrive(empty);
+            continue;
           }
+          tc_fence_after();
+          const unsigned s_t = t_base + X * 128u + b * EX_KEYS;
+          if (scores) {
+            const uint64_t kb = k_d + ((st * C::KTILE) >> 4);
 #pragma unroll
-          for (int X = 0; X < 2; ++X) {
-            if (j >= (X ? nb : na)) continue;
-            int& cnt = X ? cnt1 : cnt0;
-            int& q_tot = X ? q_tot1 : q_tot0;
-            const int b = cnt & 1;
-            bool there = true;
-            if (scores) {
-              // the buffer's last weights are used, and Q is there
-              if (cnt >= 2)
-                there = mbar_wait(&bars->pv_done[X][b], ((cnt >> 1) - 1) & 1, status, abort_flag);
-              if (j == 0) {
-                there = there && mbar_wait(&bars->q_full[X], q_tot & 1, status, abort_flag);
-                ++q_tot;
+            for (int kk = 0; kk < 4 * C::KB; ++kk)
+              tc_mma_ss_if(lead, s_t, q_d + (((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4),
+                           kb + (((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4), idesc_s,
+                           kk > 0 ? 1u : 0u);
+            if (lead) tc_commit(&bars->s_full[X][b]);
+          } else {
+            // V rows at or past the request's keys become zero: they may hold anything,
+            // and 0 * NaN is NaN.  (Both sub-tiles' warps do it, each before its MMAs.)
+            const int rows = it.s - j * EX_KEYS;
+            if (rows < EX_KEYS) {
+              for (int e = lane; e < (EX_KEYS - rows) * 8 * NB; e += 32) {
+                const int r = rows + e / (8 * NB), x = e % (8 * NB);
+                *reinterpret_cast<uint4*>(sV + st * C::VTILE + (x >> 3) * C::BLK + r * 128 +
+                                          (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
               }
-            } else {
-              there = mbar_wait(&bars->p_full[X], cnt & 1, status, abort_flag);
+              fence_proxy_async_smem();
+              __syncwarp();
             }
-            if (!__all_sync(FULL, there)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const unsigned s_t = t_base + X * 128u + b * EX_KEYS;
-            if (scores) {
-              const uint64_t qb = q_d + ((X * C::QTILE) >> 4), kb = k_d + ((st * C::KTILE) >> 4);
+            const uint64_t vb = v_d + ((st * C::VTILE) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4 * C::KB; ++kk)
-                tc_mma_ss_if(lead, s_t, qb + (((kk >> 2) * C::QBLK + (kk & 3) * 32) >> 4),
-                             kb + (((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4), idesc_s,
-                             kk > 0 ? 1u : 0u);
-              if (lead) tc_commit(&bars->s_full[X][b]);
-            } else {
-              const uint64_t vb = v_d + ((st * C::VTILE) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < EX_KEYS / 16; ++kk)
-                tc_mma_ts_if(lead, t_base + C::o_col(X), s_t + kk * 8, vb + ((kk * 2048) >> 4),
-                             idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-              if (lead) tc_commit(&bars->pv_done[X][b]);
-            }
-            ++cnt;
+            for (int kk = 0; kk < EX_KEYS / 16; ++kk)
+              tc_mma_ts_if(lead, t_base + C::o_col(0) + X * 128u, s_t + kk * 8,
+                           vb + ((kk * 2048) >> 4), idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+            if (lead) tc_commit(&bars->pv_done[X][b]);
           }
-          if (!ok) break;
-          if (lead) {
-            tc_commit(scores ? &bars->k_empty[st] : &bars->v_empty[st]);
-            if (scores && j == n - 1) tc_commit(&bars->q_empty);
-          }
+          if (lead) tc_commit(empty);
+          ++cnt;
         }
+        if (ok && scores && lead) tc_commit(&bars->q_empty);
       }
       // no MMA may still be running when TMEM is released
       if (lead) {
-        tc_commit(&bars->drain[scores ? 0 : 1]);
-        mbar_wait(&bars->drain[scores ? 0 : 1], 0, status, nullptr);
+        tc_commit(&bars->drain[warp - 10]);
+        mbar_wait(&bars->drain[warp - 10], 0, status, nullptr);
       }
       __syncwarp();
     }
@@ -681,7 +678,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         l_run += ps;
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars->p_full[X]);
+        mbar_arrive(&bars->p_full[X][b]);
       }
       if (!ok) break;
 
