@@ -56,7 +56,7 @@ constexpr int LEAST_SHARE = 3;        // cost of a CTA's share, in key tiles
 constexpr int LA_AHEAD = 1;           // tiles asked for in L2 before their copies
 constexpr float LA_RESCALE_LOG2 = 8.f;
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int MAX_SHARES = 1024;
+constexpr int MAX_SHARES = 160;  // (the merge keeps their weights in shared memory)
 
 // Where a share begins: key tile t of row tile j of request r, with the request as
 // la_request gives it (so that a CTA's first copies wait for one load less).
@@ -333,6 +333,7 @@ struct LaCfg {
   static constexpr int SMEM = BAR_OFF + 1024 + 1024;
   static_assert(SMEM <= 232448, "a CTA's shared memory");
   static_assert(P_OFF % 1024 == 0 && K_OFF % 1024 == 0, "swizzled blocks are 1024-byte aligned");
+  static constexpr int EC = R < 32 ? R : 32;   // columns of O that the epilogue takes at once
   static constexpr unsigned S_COL = 256;       // two score buffers of 64 columns
 };
 
@@ -377,6 +378,9 @@ __device__ __forceinline__ void tc_ld16(unsigned taddr, float (&v)[16]) {
         "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+
+__device__ __forceinline__ void tc_ld_cols(unsigned taddr, float (&v)[16]) { tc_ld16(taddr, v); }
+__device__ __forceinline__ void tc_ld_cols(unsigned taddr, float (&v)[32]) { tc_ld32(taddr, v); }
 
 // Barrier 1 over the softmax threads; whether any of them asked.
 __device__ __forceinline__ bool any_of_128(bool ask) {
@@ -788,13 +792,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         float4* po = reinterpret_cast<float4*>(p.part_o) + part * (R / 4) * p.dc + warp * 32 + lane;
         for (int d = 0; d < nd; ++d, po += 128)
 #pragma unroll
-          for (int c = 0; c < R; c += 16) {
+          for (int c = 0; c < R; c += C::EC) {
             if (c >= g.rows) break;
-            float o[16];
-            tc_ld16(lane_base + d * R + c, o);
+            float o[C::EC];
+            tc_ld_cols(lane_base + d * R + c, o);
             tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
+            for (int e = 0; e < C::EC; e += 4)
               po[static_cast<int64_t>((c + e) / 4) * p.dc] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
       } else {
@@ -803,14 +807,14 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         uint16_t* ob = out + warp * 32 + (lane & ~1) + static_cast<int64_t>(odd) * p.dc;
         for (int d = 0; d < nd; ++d, ob += 128)
 #pragma unroll
-          for (int c = 0; c < R; c += 16) {
+          for (int c = 0; c < R; c += C::EC) {
             if (c >= g.rows) break;
-            float o[16];
-            tc_ld16(lane_base + d * R + c, o);
+            float o[C::EC];
+            tc_ld_cols(lane_base + d * R + c, o);
             tc_wait_ld();
             uint16_t* row = ob + static_cast<int64_t>(c) * p.dc;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2, row += 2 * p.dc) {
+            for (int e = 0; e < C::EC; e += 2, row += 2 * p.dc) {
               const float x = o[e] * bars->l[c + e], y = o[e + 1] * bars->l[c + e + 1];
               const float got = __shfl_xor_sync(FULL, odd ? x : y, 1);
               if (c + e + odd < g.rows)
@@ -833,17 +837,20 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
 
 // --------------------------------------------------------------------- merge
 
-// CTA (x, y): rows 4 G y .. of the row tile that the CTA x of the attention began and
-// left to the next shares, if it did.  A thread merges a dim of the 4 G rows, U parts
-// at a time with their loads in flight together.  Bound by latency: many row tiles in
-// two parts each take G 4, U 2 (64 requests on 128 heads: 22 us with G 1 and a pass
-// for the max, about 7 so), few in many parts G 1, U 8.
-template <bool HALF, int G, int U>
-__global__ void __launch_bounds__(512) latent_merge_kernel(const __grid_constant__ LaProblem p) {
+// CTA (x, y): rows 8 G y .. of the row tile that the CTA x of the attention began and
+// left to the next shares, if it did.  The parts' weights come first (a warp a row, its
+// lanes the parts), under the loads of the sums; a thread then adds up a dim of 4 G
+// rows.  Bound by latency (the parts were written long ago and come from HBM), so a
+// CTA has 128 KB of loads in flight.
+template <bool HALF, int G>
+__global__ void __launch_bounds__(1024) latent_merge_kernel(const __grid_constant__ LaProblem p) {
+  constexpr int U = 8 / G;  // parts in flight
+  constexpr int ROWS = 8 * G;
+  __shared__ float weight[MAX_SHARES][ROWS];
   grid_dep_wait();
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
-  const int lane = threadIdx.x & 31, dim = threadIdx.x;
-  if (blockIdx.x + 1 == gridDim.x && blockIdx.y == 0 && threadIdx.x < 32) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (blockIdx.x + 1 == gridDim.x && blockIdx.y == 0 && tid < 32) {
     unsigned any = 0u;
     for (unsigned i = lane; i < gridDim.x; i += 32) any |= p.cta_status[i];
     any = __reduce_or_sync(FULL, any);
@@ -863,7 +870,7 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const __grid_constant
   const int64_t first = static_cast<int64_t>(p.lanes > 1 ? side : b.y) * p.R;
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.R),
                                         static_cast<int64_t>(q) * p.H - first));
-  const int row0 = blockIdx.y * 4 * G;
+  const int row0 = blockIdx.y * ROWS;
   if (row0 >= rows) return;
   // shares that hold a part of it: the cuts behind this share that lie inside it
   auto inside = [&](int i, const int4& k) {
@@ -876,62 +883,71 @@ __global__ void __launch_bounds__(512) latent_merge_kernel(const __grid_constant
     off = ~__ballot_sync(FULL, share + parts + lane < shares && inside(i, cuts[2 * i]));
     parts += off ? __ffs(off) - 1 : 32;
   }
-  float mx[G][4], l[G][4], acc[G][4];
-#pragma unroll
-  for (int g = 0; g < G; ++g)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      mx[g][e] = -INFINITY;
-      l[g][e] = acc[g][e] = 0.f;
-    }
-  for (int i0 = 0; i0 < parts; i0 += U) {
-    float4 x[G][U], ml[G][U][2];
+  // part i's place: the second partial of the first share, the first of the others
+  auto at = [&](int i) {
+    return static_cast<int64_t>((share + i) * p.lanes + side) * 2 + (i == 0 ? 1 : 0);
+  };
+  const int dim = tid % p.dc, group0 = row0 / 4 + tid / p.dc * G;  // the thread's row groups
+  float4 x[U][G];
+  auto load = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      // part i's place: the second partial of the first share, the first of the others
-      const int i = min(i0 + u, parts - 1);
-      const int64_t at = static_cast<int64_t>((share + i) * p.lanes + side) * 2 + (i == 0 ? 1 : 0);
+      const float4* s = reinterpret_cast<const float4*>(p.part_o) +
+                        (at(min(i0 + u, parts - 1)) * (p.R / 4) + group0) * p.dc + dim;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float4* s = reinterpret_cast<const float4*>(p.part_ml + at * p.R + row0 + 4 * g);
-        ml[g][u][0] = s[0];
-        ml[g][u][1] = s[1];
-        x[g][u] = reinterpret_cast<const float4*>(
-            p.part_o)[(at * (p.R / 4) + blockIdx.y * G + g) * p.dc + dim];
-      }
+      for (int g = 0; g < G; ++g) x[u][g] = s[static_cast<int64_t>(g) * p.dc];
+    }
+  };
+  load(0);
+  for (int row = tid >> 5; row < ROWS; row += blockDim.x >> 5) {
+    const float2* ml = p.part_ml + row0 + row;
+    float top = -INFINITY;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, ml[at(i) * p.R].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+      const float2 v = ml[at(i) * p.R];
+      const float w = fast_exp2(v.x - ref);
+      weight[i][row] = w;
+      l += w * v.y;
     }
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        auto of = [&](const float4& v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; };
-        float top = mx[g][e];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (i0 + u < parts) top = fmaxf(top, of(ml[g][u][e >> 1], 2 * (e & 1)));
-        const float ref = top == -INFINITY ? 0.f : top, was = fast_exp2(mx[g][e] - ref);
-        l[g][e] *= was;
-        acc[g][e] *= was;
-        mx[g][e] = top;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (i0 + u < parts) {
-            const float w = fast_exp2(of(ml[g][u][e >> 1], 2 * (e & 1)) - ref);
-            l[g][e] += w * of(ml[g][u][e >> 1], 2 * (e & 1) + 1);
-            acc[g][e] += w * of(x[g][u], e);
-          }
-      }
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
+    for (int i = lane; i < parts; i += 32) weight[i][row] *= inv;
   }
-  uint16_t* out = p.out + (static_cast<int64_t>(t0) * p.H + first + row0) * p.dc + dim;
+  __syncthreads();
+  float4 acc[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g)
+  for (int g = 0; g < G; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < parts; i0 += U) {
+    if (i0 > 0) load(i0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (row0 + 4 * g + e < rows) {
-        const float s = l[g][e], inv = s > 0.f ? 1.f / s : s == 0.f ? 0.f : NAN;
-        out[static_cast<int64_t>(4 * g + e) * p.dc] =
-            static_cast<uint16_t>(pack2<HALF>(acc[g][e] * inv, 0.f));
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u >= parts) break;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float4 w = *reinterpret_cast<const float4*>(&weight[i0 + u][(group0 + g) * 4 - row0]);
+        acc[g].x += w.x * x[u][g].x;
+        acc[g].y += w.y * x[u][g].y;
+        acc[g].z += w.z * x[u][g].z;
+        acc[g].w += w.w * x[u][g].w;
       }
+    }
+  }
+  uint16_t* out = p.out + (static_cast<int64_t>(t0) * p.H + first) * p.dc + dim;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const float v[4] = {acc[g].x, acc[g].y, acc[g].z, acc[g].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = (group0 + g) * 4 + e;
+      if (row < rows)
+        out[static_cast<int64_t>(row) * p.dc] = static_cast<uint16_t>(pack2<HALF>(v[e], 0.f));
+    }
+  }
 }
 
 // ---------------------------------------------------------------------- host
@@ -978,13 +994,14 @@ cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[4], int gri
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.blockDim = dim3(static_cast<unsigned>(p.dc));
+  cfg.blockDim = dim3(static_cast<unsigned>(2 * p.dc));
   cfg.dynamicSmemBytes = 0;
-  // a quarter as many row tiles as SMs and more: most of them in two parts
+  // a quarter as many row tiles as SMs and more: most of them in two parts, a CTA
+  // each; else finer
   const bool many = static_cast<long long>(p.B) * p.lanes * 4 >= grid;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), many ? R / 16 : R / 4);
-  return many ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, 4, 2>, p)
-              : cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, 1, 8>, p);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), many ? 1 : R / 8);
+  return many ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, R / 8>, p)
+              : cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, 1>, p);
 }
 
 template <int R>
