@@ -840,8 +840,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
 // CTA (x, y): rows 8 G y .. of the row tile that the CTA x of the attention began and
 // left to the next shares, if it did.  The parts' weights come first (a warp a row, its
 // lanes the parts), under the loads of the sums; a thread then adds up a dim of 4 G
-// rows.  Bound by latency (the parts were written long ago and come from HBM), so a
-// CTA has 128 KB of loads in flight.
+// rows.  Bound by latency: the parts were written long ago and come from HBM.
 template <bool HALF, int G>
 __global__ void __launch_bounds__(1024) latent_merge_kernel(const __grid_constant__ LaProblem p) {
   constexpr int U = 8 / G;  // parts in flight
@@ -899,14 +898,17 @@ __global__ void __launch_bounds__(1024) latent_merge_kernel(const __grid_constan
     }
   };
   load(0);
+#pragma unroll 1
   for (int row = tid >> 5; row < ROWS; row += blockDim.x >> 5) {
     const float2* ml = p.part_ml + row0 + row;
     float top = -INFINITY;
+#pragma unroll 1
     for (int i = lane; i < parts; i += 32) top = fmaxf(top, ml[at(i) * p.R].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
     const float ref = top == -INFINITY ? 0.f : top;
     float l = 0.f;
+#pragma unroll 1
     for (int i = lane; i < parts; i += 32) {
       const float2 v = ml[at(i) * p.R];
       const float w = fast_exp2(v.x - ref);
@@ -916,12 +918,14 @@ __global__ void __launch_bounds__(1024) latent_merge_kernel(const __grid_constan
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
     const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN;
+#pragma unroll 1
     for (int i = lane; i < parts; i += 32) weight[i][row] *= inv;
   }
   __syncthreads();
   float4 acc[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
   for (int i0 = 0; i0 < parts; i0 += U) {
     if (i0 > 0) load(i0);
 #pragma unroll
@@ -996,11 +1000,13 @@ cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[4], int gri
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(static_cast<unsigned>(2 * p.dc));
   cfg.dynamicSmemBytes = 0;
-  // a quarter as many row tiles as SMs and more: most of them in two parts, a CTA
-  // each; else finer
+  // a quarter as many row tiles as SMs and more: most of them in two parts, a CTA or
+  // two each; else finer.  (64 requests on 128 heads: 13 us so, 26 with 8 rows a CTA
+  // and 19 with 64, whose code and registers outgrow an SM.)
+  constexpr int G = R >= 32 ? 4 : 2;
   const bool many = static_cast<long long>(p.B) * p.lanes * 4 >= grid;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), many ? 1 : R / 8);
-  return many ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, R / 8>, p)
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), many ? R / (8 * G) : R / 8);
+  return many ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, G>, p)
               : cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, 1>, p);
 }
 
