@@ -48,6 +48,7 @@ constexpr int EX_SOFTMAX_REGS = 184, EX_OTHER_REGS = 72;  // setmaxnreg split
 constexpr int EX_REGS_TOTAL = 2 * 128 * (EX_SOFTMAX_REGS + EX_OTHER_REGS);
 constexpr int EX_ROWS = 256;  // query rows of an item
 constexpr int EX_RING = 4;    // item ring
+constexpr int EX_FEW = 128;   // items that a CTA lists itself
 constexpr int EX_KEYS = 64;   // keys of a tile
 constexpr float EX_RESCALE_LOG2 = 8.f;
 constexpr float EX_SUM_LIMIT = 256.f;  // 2^EX_RESCALE_LOG2
@@ -69,6 +70,7 @@ struct ExProblem {
   ExHeader* hdr;
   int2* tiles;
   int max_tiles;
+  int few;  // an item a CTA at most: the CTAs list the items themselves
   int B, T, K, H, causal;
   float sl2;
 };
@@ -208,13 +210,14 @@ struct ExItem {
   bool live;
 };
 
-__device__ __forceinline__ ExItem ex_load_item(const ExProblem& p, int item, int n_items) {
+__device__ __forceinline__ ExItem ex_load_item(const ExProblem& p, const int2* tiles, int item,
+                                               int n_items) {
   ExItem it;
   it.live = item < n_items;
   it.h = it.i0 = it.t0 = it.q = it.k0 = it.s = 0;
   if (it.live) {
     it.h = item % p.H;
-    const int2 tl = p.tiles[item / p.H];
+    const int2 tl = tiles[item / p.H];
     it.t0 = p.qsl[tl.x];
     it.q = p.qsl[tl.x + 1] - it.t0;
     if (tl.y >= 0) {
@@ -350,14 +353,49 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   tc_fence_after();
   const unsigned tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
-  grid_dep_wait();  // the plan kernel's list
-  const int n_items = p.hdr->tiles * p.H;
+  const int2* tiles = p.tiles;
+  int n_items;
+  if (p.few) {
+    // An item a CTA: their order does not matter, and a call without the plan kernel
+    // is 4 us shorter.  Thread r places the items of request r.
+    __shared__ int2 few_tiles[EX_FEW];
+    __shared__ int warp_tiles[EX_THREADS / 32];
+    const int r = threadIdx.x;
+    int t0 = 0, q = 0, k0, s;
+    bool fine = true;
+    if (r < p.B && !(fine = ex_request(p, r, t0, q, k0, s))) ex_clip(p, t0, q);
+    const int mine = (q + EX_ROWS - 1) / EX_ROWS;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(FULL, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) warp_tiles[warp] = incl;
+    const bool bad = __syncthreads_or(!fine);
+    int at = incl - mine, total = 0;
+    for (int w = 0; w < EX_THREADS / 32; ++w) {
+      if (w < warp) at += warp_tiles[w];
+      total += warp_tiles[w];
+    }
+    for (int t = 0; t < mine && at + t < p.max_tiles; ++t)
+      few_tiles[at + t] = make_int2(r, fine ? t : -1 - t);
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+      *status = bad || total > p.max_tiles ? PATTN_DEV_BAD_METADATA : 0u;
+    n_items = min(total, p.max_tiles) * p.H;
+    tiles = few_tiles;
+    __syncthreads();
+  } else {
+    grid_dep_wait();  // the plan kernel's list
+    n_items = p.hdr->tiles * p.H;
+  }
 
   // The CTA's k-th item: its own block index, then whatever is next in the list,
   // claimed one ahead by warp 8.  An index of n_items or more ends the sequence.
   auto claim = [&](int k) -> int {
-    int idx = k == 0 ? static_cast<int>(blockIdx.x)
-                     : static_cast<int>(gridDim.x + atomicAdd(&p.hdr->next_item, 1u));
+    int idx = k == 0  ? static_cast<int>(blockIdx.x)
+              : p.few ? n_items
+                      : static_cast<int>(gridDim.x + atomicAdd(&p.hdr->next_item, 1u));
     idx = min(idx, n_items);
     const int slot = k % EX_RING;
     if (k >= EX_RING &&
@@ -386,7 +424,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       bool ok = true;
       int idx = claim(0);
       for (int k = 0; idx >= 0; ++k) {
-        const ExItem it = ex_load_item(p, idx, n_items);
+        const ExItem it = ex_load_item(p, tiles, idx, n_items);
         if (!it.live) break;
         idx = claim(k + 1);
         if (idx < 0) {
@@ -444,7 +482,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           break;
         }
         release(k);
-        const ExItem it = ex_load_item(p, idx, n_items);
+        const ExItem it = ex_load_item(p, tiles, idx, n_items);
         if (!it.live) break;
         const int n = max(ex_sub(p, it, 0).n, ex_sub(p, it, 1).n);
         for (int j = 0; j < n; ++j, ++jg) {
@@ -482,7 +520,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         const int idx = take(k);
         if (!__all_sync(FULL, idx >= 0)) break;
         if (lane == 0) release(k);
-        const ExItem it = ex_load_item(p, idx, n_items);
+        const ExItem it = ex_load_item(p, tiles, idx, n_items);
         if (!__any_sync(FULL, it.live)) break;
         const int mine = static_cast<int>(
             __reduce_max_sync(FULL, static_cast<unsigned>(ex_sub(p, it, X).n)));
@@ -568,7 +606,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       const int idx = take(k);
       if (!__all_sync(FULL, idx >= 0)) break;
       if (lane == 0) release(k);
-      const ExItem it = ex_load_item(p, idx, n_items);
+      const ExItem it = ex_load_item(p, tiles, idx, n_items);
       if (!it.live) break;
       const ExSub u = ex_sub(p, it, X);
       const int i = u.i0 + row, s = it.s;
@@ -742,9 +780,12 @@ cudaError_t launch_expanded(const ExProblem& p, const CUtensorMap (&m)[5], cudaS
   using C = ExCfg<NB>;
   auto kern = expanded_kernel<NB, HALF>;
   static std::atomic<unsigned long long> ready{0};  // devices whose limit is set
-  expanded_plan_kernel<<<1, EX_PLAN_THREADS, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (!p.few) {
+    expanded_plan_kernel<<<1, EX_PLAN_THREADS, 0, st>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -755,7 +796,7 @@ cudaError_t launch_expanded(const ExProblem& p, const CUtensorMap (&m)[5], cudaS
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.few ? 0 : 1;
   e = cudaErrorInvalidValue;
   for (int again = 0; again < 2 && e == cudaErrorInvalidValue; ++again) {
     // (with the limit: the register split must fit in what the CTA is launched with)
@@ -813,6 +854,8 @@ extern "C" pattn_status_t pattn_latent_expanded_fwd(const pattn_latent_expanded_
   p.K = a->num_keys;
   p.H = a->num_heads;
   p.causal = a->causal;
+  p.few = l.max_tiles <= EX_FEW &&
+          static_cast<long long>(l.max_tiles) * a->num_heads <= current_sms();
   // strictly positive, so that a masked score (-inf) always maps to weight 0; at
   // scale 0 the weights are 1 exactly
   p.sl2 = fmaxf(a->scale * LOG2E, 1e-30f);
