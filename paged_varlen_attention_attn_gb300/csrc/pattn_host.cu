@@ -39,6 +39,29 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+__global__ void nothing_kernel() {}
+
+// A swizzled map of 16-bit elements.  The driver wants a current context, which a host
+// thread has only after a runtime call that needs one; the maps are the first thing
+// some calls ask for, so the thread gets its context here and asks again.
+bool encode_tiled(CUtensorMap* map, bool half, const void* base, cuuint32_t rank,
+                  const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  for (int again = 0; again < 2; ++again) {
+    const CUresult r =
+        enc(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return true;
+    cudaFuncAttributes attr;
+    if (again == 0 && cudaFuncGetAttributes(&attr, nothing_kernel) != cudaSuccess) return false;
+  }
+  return false;
+}
+
 // The struct grows at its end: a struct_size that reaches the field before
 // `sinks` is a complete older struct.
 bool ext_ok(const pattn_ext_t* ext) {
@@ -383,8 +406,6 @@ bool encode_diffkv_map(CUtensorMap* map, const void* cache, int kv_dtype, int dk
 
 bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int heads, int rows,
                      long long head_stride, long long row_stride, int box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
   const cuuint32_t blocks = static_cast<cuuint32_t>(std::max(1, dim / 64));
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(std::min(dim, 64)),
                               static_cast<cuuint64_t>(rows), blocks,
@@ -392,36 +413,21 @@ bool encode_rows_map(CUtensorMap* map, const void* base, bool half, int dim, int
   const cuuint64_t strides[3] = {2ull * static_cast<cuuint64_t>(row_stride), 128,
                                  2ull * static_cast<cuuint64_t>(head_stride)};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), blocks, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_tiled(map, half, base, 4, dims, strides, box);
 }
 
 bool encode_latent_maps(CUtensorMap* m, const void* q, const void* cache, bool half, int latent,
                         int rope, int q_rows, int q_box, int rows, int box) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const CUtensorMapDataType dt =
-      half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const cuuint64_t row = 2ull * static_cast<cuuint64_t>(latent + rope);
   const cuuint64_t groups = static_cast<cuuint64_t>(rows / 8);
   const cuuint32_t cols = static_cast<cuuint32_t>(latent / 64 + (rope == 64 ? 1 : 0));
   const cuuint32_t qb = static_cast<cuuint32_t>(q_box), gb = static_cast<cuuint32_t>(box / 8);
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  auto encode = [&](CUtensorMap* map, const void* base, cuuint32_t rank, const cuuint64_t* dims,
-                    const cuuint64_t* strides, const cuuint32_t* bx) {
-    return enc(map, dt, rank, const_cast<void*>(base), dims, strides, bx, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  };
   const cuuint64_t qd[3] = {64, static_cast<cuuint64_t>(q_rows), cols}, qs[2] = {row, 128};
   const cuuint32_t qx[3] = {64, qb, cols};
   const cuuint64_t cd[4] = {64, 8, cols, groups}, cs[3] = {row, 128, 8 * row};
   const cuuint32_t cx[4] = {64, 8, cols, gb};
-  if (!encode(&m[0], q, 3, qd, qs, qx) || !encode(&m[1], cache, 4, cd, cs, cx)) return false;
+  if (!encode_tiled(&m[0], half, q, 3, qd, qs, qx) || !encode_tiled(&m[1], half, cache, 4, cd, cs, cx))
+    return false;
   if (rope == 64) {
     m[2] = m[1];
     m[3] = m[0];
@@ -432,8 +438,8 @@ bool encode_latent_maps(CUtensorMap* m, const void* q, const void* cache, bool h
   const cuuint32_t rx[3] = {64, 8, gb};
   const cuuint64_t td[3] = {static_cast<cuuint64_t>(rope), static_cast<cuuint64_t>(q_rows), 1};
   const cuuint32_t tx[3] = {64, qb, 1};
-  return encode(&m[2], tail, 3, rd, rs, rx) &&
-         encode(&m[3], static_cast<const char*>(q) + 2 * latent, 3, td, qs, tx);
+  return encode_tiled(&m[2], half, tail, 3, rd, rs, rx) &&
+         encode_tiled(&m[3], half, static_cast<const char*>(q) + 2 * latent, 3, td, qs, tx);
 }
 
 cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<unsigned long long>& ready,
