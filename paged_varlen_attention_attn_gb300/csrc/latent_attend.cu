@@ -8,19 +8,21 @@
 //
 // Per key and head 2 (2 dc + dr) flops against 2 (dc + dr) bytes per key: at dc =
 // 512 the balance of HBM and tensor cores is near 128 heads.  A CTA holds R = 16,
-// 32 or 64 rows and walks tiles of 64 keys.  One copy of a tile in shared memory
+// 32 or 64 rows and walks tiles of 48 or 64 keys.  One copy of a tile in shared memory
 // feeds both MMAs of tcgen05:
-//   S (64 x 64) = Q K^T, M the rows, K-major; M = 64 leaves S's rows on the first
+//   S (64 x keys) = Q K^T, M the rows, K-major; M = 64 leaves S's rows on the first
 //     16 lanes of each warp;
 //   O^T (128 dims x R, dc / 128 of them) += V^T P^T, M the dims (the same bytes
 //     read MN-major), N the rows.  O transposed keeps all 128 lanes busy for any R
 //     and takes dc / 128 * R <= 256 TMEM columns (O itself would take all 512).
 // P goes through shared memory as the B operand.
 //
-// An MMA costs the thread that issues it about 46 cycles however small it is, so S
-// (36 of them for 576 dims, whatever the keys of a tile) wants the largest tile
-// that leaves two in flight beside Q: with tiles of 32 keys and five in the ring a
-// pass over 8 x 125 k keys took 446 us.
+// An MMA costs its issue 34 to 40 cycles however few keys it has, so S (36 of them
+// for 576 dims) wants large tiles, and the copies want several tiles in flight: a
+// tile's slot is empty from its P V until its next copy, some 2000 cycles of HBM and 1500
+// of softmax later.  Beside up to 32 rows of Q three tiles of 48 keys fit, beside 64
+// rows two of 64.  (8 x 125 k keys, 32 heads: 200 us with two of 64, 208 with five of 32;
+// 64 requests, 128 heads: 90 with two of 64, 92 with four of 32.)
 //
 // A tile lies as [8 keys][64-element column block][8 x 128 bytes], so that the rows
 // of a page land with one copy whatever the block size: a copy holds its warp for
@@ -48,9 +50,8 @@ namespace pattn {
 namespace {
 
 constexpr int LA_THREADS = 256;
-constexpr int LA_KEYS = 64;           // keys of a tile
-constexpr int LA_ROT = LA_KEYS * 128; // bytes of a tile's rotary parts
-constexpr int LA_LAT = 8 * LA_ROT;    // and of its latents (dc = 512)
+// Keys of a tile (above): three tiles of 48 in the ring, or two of 64 beside 64 rows.
+__host__ __device__ constexpr int la_keys(int R) { return R == 64 ? 64 : 48; }
 constexpr int PAD = 2;                // a row tile's fixed cost, in key tiles
 constexpr int LEAST_SHARE = 3;        // cost of a CTA's share, in key tiles
 constexpr int LA_AHEAD = 1;           // tiles asked for in L2 before their copies
@@ -86,6 +87,7 @@ struct LaProblem {
   float sl2;
   int B, T, H, dc, dr, bs, mbps, NB, causal, half;
   int R, r_shift;   // rows of a row tile, a power of two
+  int keys;         // of a key tile
   int lanes;        // CTAs side by side on a share (1, or the row tiles of a token)
   int max_shares;
   int box;          // cache rows of one copy
@@ -122,7 +124,7 @@ __device__ __forceinline__ int la_key_tiles(const LaProblem& p, int q, int s, in
     const unsigned last = (static_cast<unsigned>(j + 1) << p.r_shift) - 1;
     keys = s - q + min(q - 1, static_cast<int>(last / static_cast<unsigned>(p.H))) + 1;
   }
-  return (keys + LA_KEYS - 1) / LA_KEYS;
+  return (keys + p.keys - 1) / p.keys;
 }
 
 // The cost of a request's first x row tiles, a x + b x^2 / 2: the key tiles grow
@@ -324,8 +326,11 @@ __device__ __forceinline__ bool la_next(const LaProblem& p, Walk& w, int lane, S
 template <int R>
 struct LaCfg {
   static constexpr int QBLK = R * 128;         // a 64-element column block of Q
-  static constexpr int NST = 2;                // tiles in the ring
-  static constexpr int STAGE = LA_LAT + LA_ROT;
+  static constexpr int KEYS = la_keys(R);
+  static constexpr int NST = R == 64 ? 2 : 3;  // tiles in the ring
+  static constexpr int ROT = KEYS * 128;       // bytes of a tile's rotary parts
+  static constexpr int LAT = 8 * ROT;          // and of its latents (dc = 512)
+  static constexpr int STAGE = LAT + ROT;
   static constexpr int Q_OFF = 0;
   static constexpr int P_OFF = Q_OFF + 9 * QBLK;
   static constexpr int K_OFF = P_OFF + R * 128;
@@ -338,7 +343,7 @@ struct LaCfg {
 };
 
 struct LaBars {
-  uint64_t k_full[2], k_empty[2];
+  uint64_t k_full[3], k_empty[3];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, drain[2];
   float alpha[64], l[64];
   Cut cuts[2];
@@ -352,7 +357,7 @@ static_assert(sizeof(LaBars) <= 1024, "the barriers fit the space kept for them"
 
 // 16 TMEM lanes x 64 fp32 columns of a warp: lane t gets columns 8 g + 2 (t % 4) + {0,
 // 1} of rows t / 4 (v[4 g], v[4 g + 1]) and t / 4 + 8 (v[4 g + 2], v[4 g + 3]).
-__device__ __forceinline__ void tc_ld_16x64(unsigned taddr, float (&v)[32]) {
+__device__ __forceinline__ void tc_ld_scores(unsigned taddr, float (&v)[32]) {
   unsigned* r = reinterpret_cast<unsigned*>(v);
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
@@ -365,6 +370,23 @@ __device__ __forceinline__ void tc_ld_16x64(unsigned taddr, float (&v)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
         "=r"(r[31])
       : "r"(taddr));
+}
+
+// The same for 48 columns, with the last 16 from a copy of their own.
+__device__ __forceinline__ void tc_ld_scores(unsigned taddr, float (&v)[24]) {
+  unsigned* r = reinterpret_cast<unsigned*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23])
+      : "r"(taddr + 32));
 }
 
 // 16 consecutive fp32 columns of this thread's TMEM lane.
@@ -466,7 +488,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     Walk w = {bars->cuts[0], bars->cuts[1]};
     Seg g;
     int pos = 0, ok = 1;
-    const int ppt = LA_KEYS / p.box;  // pages of a tile
+    const int ppt = C::KEYS / p.box;  // pages of a tile
     const int page = p.fused ? half + 2 * lane : lane;  // this lane's
     const int page_bytes = rot ? p.box * 128 : p.box * 128 * cols;
     while (ok && la_next(p, w, side, g)) {
@@ -474,7 +496,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       const int* bt = p.block_table + static_cast<int64_t>(g.r) * p.mbps;
       // the pool row that the lane's page of key tile kt begins at, -1 for none
       auto page_row = [&](int kt) {
-        const int key = kt * LA_KEYS + page * p.box;
+        const int key = kt * C::KEYS + page * p.box;
         if (page >= ppt || kt >= g.k1 || key >= g.s) return -1;
         int blk = bt[key / p.bs];
         if (blk < 0 || blk >= p.NB) {
@@ -514,7 +536,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         ok = __shfl_sync(FULL, ok, 0);
         if (!ok) break;
         if (row >= 0) {
-          unsigned char* dst = sK + st * C::STAGE + (rot ? LA_LAT : 0) + page * page_bytes;
+          unsigned char* dst = sK + st * C::STAGE + (rot ? C::LAT : 0) + page * page_bytes;
           if (rot)
             tma_load_3d(dst, &rmap, &bars->k_full[st], 0, 0, row >> 3);
           else
@@ -539,14 +561,14 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     // took 54, from a branch for one lane 50 to 71.
     const bool scores = warp == 5;
     const unsigned lead = elect_one();
-    constexpr unsigned idesc_s = make_idesc_f16(64, LA_KEYS, !HALF, false);
+    constexpr unsigned idesc_s = make_idesc_f16(64, C::KEYS, !HALF, false);
     constexpr unsigned idesc_pv = make_idesc_f16(128, R, !HALF, false) | (1u << 15);  // A MN-major
     const unsigned t_base = __reduce_max_sync(FULL, tmem);
     const uint64_t q_d = smem_desc_sw128(smem_u32(sQ), 16, 1024);
     const uint64_t p_d = smem_desc_sw128(smem_u32(sP), 16, 1024);
     // 8 keys are `cols` KB apart; of V, 64 dims are 1 KB apart
     const uint64_t k_d = smem_desc_sw128(smem_u32(sK), 16, cols * 1024);
-    const uint64_t r_d = smem_desc_sw128(smem_u32(sK + (p.fused ? nc * 1024 : LA_LAT)), 16,
+    const uint64_t r_d = smem_desc_sw128(smem_u32(sK + (p.fused ? nc * 1024 : C::LAT)), 16,
                                          p.fused ? cols * 1024 : 1024);
     const uint64_t v_d = smem_desc_sw128(smem_u32(sK), 1024, cols * 1024);
     Walk w = {bars->cuts[0], bars->cuts[1]};
@@ -582,7 +604,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             break;
           }
           tc_fence_after();
-          const unsigned s_t = t_base + C::S_COL + (n & 1) * LA_KEYS;
+          const unsigned s_t = t_base + C::S_COL + (n & 1) * 64;
           uint64_t qb = q_d, kb = k_d + ((st * C::STAGE) >> 4);
           for (int d = 0; d < nd; ++d) {
 #pragma unroll
@@ -609,7 +631,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           }
           tc_fence_after();
           uint64_t vb = v_d + ((st * C::STAGE) >> 4), pb = p_d;
-          for (int kk = 0; kk < LA_KEYS / 16; ++kk) {
+          for (int kk = 0; kk < C::KEYS / 16; ++kk) {
 #pragma unroll
             for (int d = 0; d < 4; ++d)
               if (d < nd)
@@ -638,7 +660,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   } else {
     // ------------------------------------------------------------ softmax
     // Warp w's TMEM lanes 32 w .. + 15 hold rows 16 w .. + 15 of S; a thread has two
-    // of them, ra and ra + 8, and 16 keys of each.
+    // of them, ra and ra + 8, and a quarter of the keys of each.
     const bool has_rows = warp * 16 < R;
     const int ra = warp * 16 + (lane >> 2), c2 = 2 * (lane & 3);
     const unsigned lane_base = tmem + (static_cast<unsigned>(warp * 32) << 16);
@@ -667,28 +689,28 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       const int n_tiles = g.k1 - g.k0;
       for (int i = 0; i < n_tiles; ++i) {
-        const int n = tile + i, key0 = (g.k0 + i) * LA_KEYS;
+        const int n = tile + i, key0 = (g.k0 + i) * C::KEYS;
         if (!__all_sync(FULL, mbar_wait(&bars->s_full[n & 1], (n >> 1) & 1, status, abort_flag)))
           ok = false;
-        float v[32];
+        float v[C::KEYS / 2];
         bool ask = false;
         float alpha[2] = {1.f, 1.f};
         if (ok && has_rows) {
           tc_fence_after();
-          tc_ld_16x64(lane_base + C::S_COL + (n & 1) * LA_KEYS, v);
+          tc_ld_scores(lane_base + C::S_COL + (n & 1) * 64, v);
           tc_wait_ld();
           tc_fence_before();
           if (lane == 0) mbar_arrive(&bars->s_empty[n & 1]);
-          if (key0 + LA_KEYS > first_max) {
+          if (key0 + C::KEYS > first_max) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < C::KEYS / 2; ++e) {
               const int key = key0 + (e >> 2) * 8 + c2 + (e & 1);
               if (key >= kmax[(e >> 1) & 1]) v[e] = -INFINITY;
             }
           }
           float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx[(e >> 1) & 1] = fmaxf(mx[(e >> 1) & 1], v[e]);
+          for (int e = 0; e < C::KEYS / 2; ++e) mx[(e >> 1) & 1] = fmaxf(mx[(e >> 1) & 1], v[e]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(FULL, mx[e], 1));
@@ -705,7 +727,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             }
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
+          for (int e = 0; e < C::KEYS / 2; ++e) {
             const int k = (e >> 1) & 1;
             v[e] = fast_exp2(v[e] * sl2 - (m[k] == -INFINITY ? 0.f : m[k]));
             l[k] += v[e];
@@ -742,7 +764,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         if (!ok) continue;  // (the barriers of the loop stay matched)
         if (has_rows) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
+          for (int c = 0; c < C::KEYS / 8; ++c)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int row = ra + 8 * e;
@@ -753,9 +775,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         // Values of keys at or past seq_len become zero before P V reads them: the
         // slots may hold anything, and 0 * NaN is NaN.
         const int tail = g.s - key0;
-        if (tail < LA_KEYS) {
+        if (tail < C::KEYS) {
           unsigned char* k = sK + (n % C::NST) * C::STAGE;
-          for (int e = threadIdx.x; e < (LA_KEYS - tail) * 8 * nc; e += 128) {
+          for (int e = threadIdx.x; e < (C::KEYS - tail) * 8 * nc; e += 128) {
             const int row = tail + e / (8 * nc), x = e % (8 * nc);
             *reinterpret_cast<uint4*>(k + ((row >> 3) * cols + (x >> 3)) * 1024 + (row & 7) * 128 +
                                       (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -1078,12 +1100,13 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   p.causal = a->causal;
   p.half = a->kv_dtype == PATTN_KV_F16;
   p.R = R;
+  p.keys = la_keys(R);
   p.r_shift = R == 16 ? 4 : R == 32 ? 5 : 6;
   const int tiles = (a->num_heads + R - 1) / R;  // row tiles of a token
   p.lanes = a->max_query_len <= 1 && tiles > 1 && tiles <= 8 ? tiles : 1;
   p.max_shares = std::max(1, l.grid / p.lanes);
   // a copy is a run of rows of one block, and there are two at least for the two warps
-  p.box = a->block_size % 32 == 0 ? 32 : 16;
+  p.box = R == 64 && a->block_size % 32 == 0 ? 32 : 16;
   p.fused = a->rope_size == 64;
   CUtensorMap m[4];
   if (!encode_latent_maps(m, a->q, a->kv_cache, p.half, a->latent_size, a->rope_size,
