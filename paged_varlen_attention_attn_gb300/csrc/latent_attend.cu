@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   const unsigned tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
+  grid_dep_wait();
   la_plan(p, share, bars->sums, bars->cuts, &bars->shares, status);
   const bool works = share < bars->shares;
   unsigned char* sQ = smem + C::Q_OFF;
@@ -868,6 +869,7 @@ __global__ void __launch_bounds__(1024) latent_merge_kernel(const __grid_constan
   constexpr int U = 8 / G;  // parts in flight
   constexpr int ROWS = 8 * G;
   __shared__ float weight[MAX_SHARES][ROWS];
+  grid_dep_trigger();
   grid_dep_wait();
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -1009,27 +1011,19 @@ cudaError_t launch_latent(const LaProblem& p, const CUtensorMap (&m)[4], int gri
   for (int again = 0; again < 2 && e == cudaErrorInvalidValue; ++again) {
     e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::SMEM, ready, again);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(grid), LA_THREADS, C::SMEM, st>>>(p, m[0], m[1], m[2], m[3]);
-    e = cudaGetLastError();
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), LA_THREADS, C::SMEM, st, p, m[0],
+                         m[1], m[2], m[3]);
+    if (e == cudaErrorInvalidValue) cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.blockDim = dim3(static_cast<unsigned>(2 * p.dc));
-  cfg.dynamicSmemBytes = 0;
   // a quarter as many row tiles as SMs and more: most of them in two parts, a CTA or
   // two each; else finer.  (64 requests on 128 heads: 13 us so, 26 with 8 rows a CTA
   // and 19 with 64, whose code and registers outgrow an SM.)
   constexpr int G = R >= 32 ? 4 : 2;
   const bool many = static_cast<long long>(p.B) * p.lanes * 4 >= grid;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), many ? R / (8 * G) : R / 8);
-  return many ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, G>, p)
-              : cudaLaunchKernelEx(&cfg, latent_merge_kernel<HALF, 1>, p);
+  const dim3 ctas(static_cast<unsigned>(grid), many ? R / (8 * G) : R / 8);
+  return many ? launch_dependent(latent_merge_kernel<HALF, G>, ctas, 2u * p.dc, 0, st, p)
+              : launch_dependent(latent_merge_kernel<HALF, 1>, ctas, 2u * p.dc, 0, st, p);
 }
 
 template <int R>

@@ -103,6 +103,8 @@ template <int LPR, int STEPS, bool HALF>
 __global__ void __launch_bounds__(LW_THREADS)
     latent_write_kernel(const __grid_constant__ WriteParams p) {
   constexpr int RPS = 32 / LPR;
+  grid_dep_trigger();
+  grid_dep_wait();
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (LW_THREADS / 32) + (threadIdx.x >> 5);
   const int64_t t = unit / p.units;
   if (t >= p.T) return;
@@ -224,8 +226,8 @@ cudaError_t launch_write(WriteParams& p, cudaStream_t st) {
   const long long ctas =
       (static_cast<long long>(p.T) * p.units + LW_THREADS / 32 - 1) / (LW_THREADS / 32);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  latent_write_kernel<LPR, STEPS, HALF><<<static_cast<unsigned>(ctas), LW_THREADS, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(latent_write_kernel<LPR, STEPS, HALF>, dim3(static_cast<unsigned>(ctas)),
+                          LW_THREADS, 0, st, p);
 }
 
 template <int LPR, bool HALF>
@@ -266,6 +268,8 @@ struct ReadParams {
 // dealt out to the lanes one after the other.
 __global__ void __launch_bounds__(GL_THREADS)
     gather_latent_kernel(const __grid_constant__ ReadParams p) {
+  grid_dep_trigger();
+  grid_dep_wait();
   const int64_t first =
       (static_cast<int64_t>(blockIdx.x) * (GL_THREADS / 32) + (threadIdx.x >> 5)) * GL_ROWS;
   if (first >= p.rows) return;
@@ -450,6 +454,8 @@ extern "C" pattn_status_t pattn_gather_latent(const void* kv_cache, const int32_
   p.bs = block_size;
   constexpr long long PER = GL_ROWS * (GL_THREADS / 32);
   const unsigned grid = static_cast<unsigned>((num_rows + PER - 1) / PER);
-  gather_latent_kernel<<<grid, GL_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PATTN_OK : PATTN_ERR_CUDA;
+  return launch_dependent(gather_latent_kernel, dim3(grid), GL_THREADS, 0,
+                          static_cast<cudaStream_t>(stream), p) == cudaSuccess
+             ? PATTN_OK
+             : PATTN_ERR_CUDA;
 }

@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(EX_PLAN_THREADS)
   __shared__ unsigned bad;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   grid_dep_trigger();
+  grid_dep_wait();
   for (int b = tid; b < EX_BUCKETS; b += EX_PLAN_THREADS) hist[b] = 0;
   if (tid == 0) {
     bad = 0u;
@@ -353,6 +354,8 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   tc_fence_after();
   const unsigned tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
+  grid_dep_trigger();
+  grid_dep_wait();  // the plan kernel's list, or whatever came before
   const int2* tiles = p.tiles;
   int n_items;
   if (p.few) {
@@ -386,7 +389,6 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     tiles = few_tiles;
     __syncthreads();
   } else {
-    grid_dep_wait();  // the plan kernel's list
     n_items = p.hdr->tiles * p.H;
   }
 
@@ -782,28 +784,18 @@ cudaError_t launch_expanded(const ExProblem& p, const CUtensorMap (&m)[5], cudaS
   static std::atomic<unsigned long long> ready{0};  // devices whose limit is set
   cudaError_t e = cudaSuccess;
   if (!p.few) {
-    expanded_plan_kernel<<<1, EX_PLAN_THREADS, 0, st>>>(p);
-    e = cudaGetLastError();
+    e = launch_dependent(expanded_plan_kernel, dim3(1), EX_PLAN_THREADS, 0, st, p);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(
+  const dim3 grid(static_cast<unsigned>(
       std::min<long long>(static_cast<long long>(p.max_tiles) * p.H, current_sms())));
-  cfg.blockDim = dim3(EX_THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.few ? 0 : 1;
   e = cudaErrorInvalidValue;
   for (int again = 0; again < 2 && e == cudaErrorInvalidValue; ++again) {
     // (with the limit: the register split must fit in what the CTA is launched with)
     e = allow_shared_memory(reinterpret_cast<const void*>(kern), C::SMEM, ready, again, EX_THREADS,
                             EX_REGS_TOTAL);
     if (e != cudaSuccess) return e;
-    e = cudaLaunchKernelEx(&cfg, kern, p, m[0], m[1], m[2], m[3], m[4]);
+    e = launch_dependent(kern, grid, EX_THREADS, C::SMEM, st, p, m[0], m[1], m[2], m[3], m[4]);
     if (e == cudaErrorInvalidValue) cudaGetLastError();
   }
   return e;
