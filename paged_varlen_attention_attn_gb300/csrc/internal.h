@@ -230,8 +230,9 @@ bool encode_latent_maps(CUtensorMap* m, const void* q, const void* cache, bool h
 // `ready` holds a bit per device.  (The call costs as much as a launch; the value is
 // the same in every call, so no host thread lowers it between another's set and
 // launch.)  `again`: whatever `ready` says, for a launch that was refused because the
-// limit went with a context that is no longer current.  With threads > 0 also checks that the kernel has at least `regs` registers
-// over them (a setmaxnreg split that asked for more would wait forever).
+// limit went with a context that is no longer current.  With threads > 0 also checks
+// that the kernel has at least `regs` registers over them (a setmaxnreg split that
+// asked for more would wait forever).
 cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<unsigned long long>& ready,
                                 bool again, int threads = 0, int regs = 0);
 

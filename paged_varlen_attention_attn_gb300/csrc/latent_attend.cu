@@ -129,7 +129,9 @@ __device__ __forceinline__ int la_key_tiles(const LaProblem& p, int q, int s, in
 
 // The cost of a request's first x row tiles, a x + b x^2 / 2: the key tiles grow
 // with the position.  (An estimate where rows and tiles do not divide; it only
-// says where the shares are cut.)
+// says where the shares are cut.  Two CTAs compute the cut between them, each for
+// itself, so every product and sum below is rounded as it stands: 0.5 b and the
+// differences of counts are exact, the rest is spelled out.)
 struct Cost {
   float a, b;
   int n;  // row tiles
@@ -148,7 +150,7 @@ __device__ __forceinline__ Cost la_cost(const LaProblem& p, int q, int s) {
 __device__ __forceinline__ unsigned long long la_total(const LaProblem& p, int q, int s) {
   const Cost c = la_cost(p, q, s);
   const float n = static_cast<float>(c.n);
-  return static_cast<unsigned long long>(rintf(n * (c.a + 0.5f * c.b * n)));
+  return static_cast<unsigned long long>(rintf(__fmul_rn(n, __fmaf_rn(0.5f * c.b, n, c.a))));
 }
 
 // ------------------------------------------------------------------- plan
@@ -181,10 +183,11 @@ __device__ __forceinline__ unsigned long long sum_before(unsigned long long x,
 // Where weight w of request r falls, v past the request's begin.
 __device__ __forceinline__ Cut la_place(const LaProblem& p, int r, int t0, int q, int s, float v) {
   const Cost k = la_cost(p, q, s);
-  const float x = 2.f * v / (k.a + sqrtf(fmaxf(0.f, k.a * k.a + 2.f * k.b * v)));
+  const float root = __fsqrt_rn(fmaxf(0.f, __fmaf_rn(k.a, k.a, __fmul_rn(2.f * k.b, v))));
+  const float x = 2.f * v / __fadd_rn(k.a, root);
   Cut cut = {r, min(static_cast<int>(x), k.n - 1), 0, 1, t0, q, s, 0};
   const int nk = la_key_tiles(p, q, s, cut.j);
-  cut.t = static_cast<int>((x - static_cast<float>(cut.j)) * static_cast<float>(nk + PAD));
+  cut.t = static_cast<int>(__fmul_rn(x - static_cast<float>(cut.j), static_cast<float>(nk + PAD)));
   if (cut.t >= nk) {  // behind the row tile's keys: the next one begins
     cut.t = 0;
     if (++cut.j >= k.n) cut = {r + 1, 0, 0, 0, 0, 0, 0, 0};
@@ -194,8 +197,8 @@ __device__ __forceinline__ Cut la_place(const LaProblem& p, int r, int t0, int q
 
 // Cuts the batch into shares: every CTA sums the requests' costs (integers, so that all
 // agree) and finds the two cuts of its share; the first one leaves all of them for the
-// merge.  In the CTAs themselves because a kernel of its own before them, and the load
-// of what it found, put 6 us before the first copy.
+// merge.  (A kernel of its own before them took as long, 50.1 against 50.3 us for 64
+// requests on 16 heads, and is a launch more.)
 __device__ __forceinline__ void la_plan(const LaProblem& p, int share, unsigned long long* warp_sums,
                                         Cut* mine, int* shares_out, unsigned* status) {
   const int tid = threadIdx.x;
@@ -431,7 +434,6 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   LaBars* bars = reinterpret_cast<LaBars*>(smem + C::BAR_OFF);
   unsigned* status = &bars->status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dep_trigger();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
@@ -467,6 +469,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   const unsigned tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort_flag;
   const int share = blockIdx.x / p.lanes, side = blockIdx.x % p.lanes;
+  grid_dep_trigger();  // (with the TMEM in hand, which a later kernel's CTA could take)
   grid_dep_wait();
   la_plan(p, share, bars->sums, bars->cuts, &bars->shares, status);
   const bool works = share < bars->shares;

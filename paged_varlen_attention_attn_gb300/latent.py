@@ -156,7 +156,7 @@ def latent_rope_and_cache(q, latent, k_rope, kv_cache, slot_mapping, positions, 
     pos_at = table_at = max_pos = 0
     if positions is not None:
         pos_at = _index(positions, "positions", torch.int64, (T,), dev)
-        if (cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != dr or
+        if (cos_sin is None or cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != dr or
                 cos_sin.device != dev or not cos_sin.is_contiguous()):
             raise ValueError("cos_sin must be a contiguous fp32 [max_position, rope_size] tensor")
         table_at, max_pos = cos_sin.data_ptr(), cos_sin.shape[0]

@@ -153,7 +153,7 @@ def _write(**kw):
     dict(kv_cache=torch.zeros(2, 32, 160, dtype=torch.bfloat16)),
     dict(kv_cache=torch.zeros(2, 16, 320, dtype=torch.bfloat16)[..., ::2]),
     dict(slot_mapping=torch.zeros(3, dtype=torch.int32)), dict(positions=torch.zeros(4, dtype=torch.int64)),
-    dict(cos_sin=torch.zeros(9, 16)), dict(cos_sin=torch.zeros(9, 32).double()),
+    dict(cos_sin=None), dict(cos_sin=torch.zeros(9, 16)), dict(cos_sin=torch.zeros(9, 32).double()),
     dict(latent_norm=torch.zeros(64, dtype=torch.bfloat16)),
     dict(q_out=torch.zeros(3, 1, 32, dtype=torch.bfloat16)), dict(q=None, q_out=torch.zeros(3, 2, 32)),
     dict(row_out=torch.zeros(3, 128, dtype=torch.bfloat16)),
