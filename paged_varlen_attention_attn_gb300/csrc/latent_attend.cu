@@ -346,7 +346,7 @@ struct LaCfg {
 };
 
 struct LaBars {
-  uint64_t k_full[3], k_empty[3];
+  uint64_t k_full[3], k_empty[3][2];  // (a slot's two copying warps are let in apart)
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, drain[2];
   float alpha[64], l[64];
   Cut cuts[2];
@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&bars->k_full[i], 2);  // the latents' and the rotary parts' bytes
-      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->k_empty[i][0], 1);
+      mbar_init(&bars->k_empty[i][1], 1);
     }
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
@@ -479,12 +480,14 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   const int nc = p.dc / 64;  // column blocks of the latents
   const int cols = nc + p.fused;  // of a copied row
   const int nd = p.dc / 128;
+  const int ppt = C::KEYS / p.box;  // pages of a tile
+  const int first = p.fused ? (ppt + 1) / 2 : ppt;  // of which warp 4 copies these
 
   if (!works) {
   } else if (warp == 4 || warp == 6) {
     // ---------------------------------------------------------------- TMA
     // Rotary parts of 64 elements come with the latents, a copy a page, and warps 4 and
-    // 6 take turns at the pages (a copy holds its warp for some 200 ns); others come
+    // 6 have half of the pages each (a copy holds its warp for some 200 ns); others come
     // through a map that widens them with zeros, copied by warp 6.  Lane 0 waits for
     // a ring slot and posts its warp's bytes, the copies go out from one lane each.
     const int half = warp == 6 ? 1 : 0;
@@ -492,8 +495,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     Walk w = {bars->cuts[0], bars->cuts[1]};
     Seg g;
     int pos = 0, ok = 1;
-    const int ppt = C::KEYS / p.box;  // pages of a tile
-    const int page = p.fused ? half + 2 * lane : lane;  // this lane's
+    const int page = (p.fused && half ? first : 0) + lane;  // this lane's
+    const int last = half ? ppt : first;
     const int page_bytes = rot ? p.box * 128 : p.box * 128 * cols;
     while (ok && la_next(p, w, side, g)) {
       if (g.s == 0) continue;
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       // the pool row that the lane's page of key tile kt begins at, -1 for none
       auto page_row = [&](int kt) {
         const int key = kt * C::KEYS + page * p.box;
-        if (page >= ppt || kt >= g.k1 || key >= g.s) return -1;
+        if (page >= last || kt >= g.k1 || key >= g.s) return -1;
         int blk = bt[key / p.bs];
         if (blk < 0 || blk >= p.NB) {
           flag_status(status, PATTN_DEV_BAD_METADATA);
@@ -530,7 +533,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         const int copies = __popc(__ballot_sync(FULL, row >= 0));
         if (lane == 0) {
           if (pos >= C::NST &&
-              !mbar_wait(&bars->k_empty[st], ((pos / C::NST) - 1) & 1, status, abort_flag))
+              !mbar_wait(&bars->k_empty[st][half], ((pos / C::NST) - 1) & 1, status, abort_flag))
             ok = 0;
           else if (copies > 0)
             mbar_arrive_expect_tx(&bars->k_full[st], static_cast<unsigned>(copies * page_bytes));
@@ -643,9 +646,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
                              (i > 0 || kk > 0) ? 1u : 0u);
             vb += (2 * cols * 1024) >> 4;
             pb += 32 >> 4;
+            if (lead && (kk + 1) * 16 == first * p.box) tc_commit(&bars->k_empty[st][0]);
           }
           if (lead) {
-            tc_commit(&bars->k_empty[st]);
+            tc_commit(&bars->k_empty[st][1]);
             tc_commit(&bars->pv_done);
           }
         }
