@@ -21,8 +21,15 @@
 // for 576 dims) wants large tiles, and the copies want several tiles in flight: a
 // tile's slot is empty from its P V until its next copy, some 2000 cycles of HBM and 1500
 // of softmax later.  Beside up to 32 rows of Q three tiles of 48 keys fit, beside 64
-// rows two of 64.  (8 x 125 k keys, 32 heads: 200 us with two of 64, 208 with five of 32;
-// 64 requests, 128 heads: 90 with two of 64, 92 with four of 32.)
+// rows two of 64.  (8 x 125 k keys, 32 heads: 200 us with two of 64, 208 with five of 32,
+// 192 so; 64 requests, 128 heads: 90 with two of 64, 92 with four of 32.)
+//
+// Measured: 8 x 125 k keys on 32 heads 186 us, 6.2 TB/s; 64 requests of 512 to 4096 keys
+// on 16 heads 44 (25 for the bytes: the start takes some 10 us and the merge 6), on
+// 128 heads 87; 24 chunks beside 40 single tokens on 32 heads 254 us, 501 TFLOP/s.
+// The last two are bound by a slot's life: load, S, softmax and P V one after the
+// other, with two slots, 3300 to 4400 cycles a tile, where the operands' way through
+// shared memory takes 2500.
 //
 // A tile lies as [8 keys][64-element column block][8 x 128 bytes], so that the rows
 // of a page land with one copy whatever the block size: a copy holds its warp for
@@ -33,7 +40,8 @@
 // tiles).  A row tile cut by a share's border leaves unnormalised partials with
 // their max and sum, which a second kernel merges in a fixed order.  In a batch of
 // single tokens with more than 64 heads, the CTAs of a share work side by side
-// on the row tiles of one token, so HBM is read once for all of them.
+// on the row tiles of one token, so HBM is read once for all of them (64 requests
+// on 128 heads 87 us, 94 with a share each; on 256 heads 142 and 156).
 //
 // Eight warps: 0-3 softmax and epilogue, 4 and 6 TMA of the cache, 5 TMA of Q and the
 // MMAs of S, 7 the MMAs of P V.
@@ -54,6 +62,8 @@ constexpr int LA_THREADS = 256;
 __host__ __device__ constexpr int la_keys(int R) { return R == 64 ? 64 : 48; }
 constexpr int PAD = 2;                // a row tile's fixed cost, in key tiles
 constexpr int LEAST_SHARE = 3;        // cost of a CTA's share, in key tiles
+constexpr int LA_BOX = 16;            // cache rows of a copy (runs of 32 took as long: 87 us
+                                      // for 64 requests of 128 heads)
 constexpr int LA_AHEAD = 1;           // tiles asked for in L2 before their copies
 constexpr float LA_RESCALE_LOG2 = 8.f;
 constexpr unsigned FULL = 0xffffffffu;
@@ -90,7 +100,6 @@ struct LaProblem {
   int keys;         // of a key tile
   int lanes;        // CTAs side by side on a share (1, or the row tiles of a token)
   int max_shares;
-  int box;          // cache rows of one copy
   int fused;        // rotary parts of 64 elements: copied with the latents
 };
 
@@ -480,7 +489,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   const int nc = p.dc / 64;  // column blocks of the latents
   const int cols = nc + p.fused;  // of a copied row
   const int nd = p.dc / 128;
-  const int ppt = C::KEYS / p.box;  // pages of a tile
+  constexpr int ppt = C::KEYS / LA_BOX;  // pages of a tile
   const int first = p.fused ? (ppt + 1) / 2 : ppt;  // of which warp 4 copies these
 
   if (!works) {
@@ -497,13 +506,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     int pos = 0, ok = 1;
     const int page = (p.fused && half ? first : 0) + lane;  // this lane's
     const int last = half ? ppt : first;
-    const int page_bytes = rot ? p.box * 128 : p.box * 128 * cols;
+    const int page_bytes = rot ? LA_BOX * 128 : LA_BOX * 128 * cols;
     while (ok && la_next(p, w, side, g)) {
       if (g.s == 0) continue;
       const int* bt = p.block_table + static_cast<int64_t>(g.r) * p.mbps;
       // the pool row that the lane's page of key tile kt begins at, -1 for none
       auto page_row = [&](int kt) {
-        const int key = kt * C::KEYS + page * p.box;
+        const int key = kt * C::KEYS + page * LA_BOX;
         if (page >= last || kt >= g.k1 || key >= g.s) return -1;
         int blk = bt[key / p.bs];
         if (blk < 0 || blk >= p.NB) {
@@ -646,7 +655,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
                              (i > 0 || kk > 0) ? 1u : 0u);
             vb += (2 * cols * 1024) >> 4;
             pb += 32 >> 4;
-            if (lead && (kk + 1) * 16 == first * p.box) tc_commit(&bars->k_empty[st][0]);
+            if (lead && (kk + 1) * 16 == first * LA_BOX) tc_commit(&bars->k_empty[st][0]);
           }
           if (lead) {
             tc_commit(&bars->k_empty[st][1]);
@@ -1106,12 +1115,10 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   const int tiles = (a->num_heads + R - 1) / R;  // row tiles of a token
   p.lanes = a->max_query_len <= 1 && tiles > 1 && tiles <= 8 ? tiles : 1;
   p.max_shares = std::max(1, l.grid / p.lanes);
-  // a copy is a run of rows of one block, and there are two at least for the two warps
-  p.box = R == 64 && a->block_size % 32 == 0 ? 32 : 16;
   p.fused = a->rope_size == 64;
   CUtensorMap m[4];
   if (!encode_latent_maps(m, a->q, a->kv_cache, p.half, a->latent_size, a->rope_size,
-                          a->num_tokens * a->num_heads, R, a->num_blocks * a->block_size, p.box))
+                          a->num_tokens * a->num_heads, R, a->num_blocks * a->block_size, LA_BOX))
     return PATTN_ERR_CUDA;
   const int grid = p.max_shares * p.lanes;
   cudaStream_t st = static_cast<cudaStream_t>(a->stream);

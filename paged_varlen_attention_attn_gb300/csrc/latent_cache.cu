@@ -10,7 +10,10 @@
 // token's cache row (and, if asked, as a dense row, the input of the
 // up-projection).  fp32 throughout with one rounding at the end.
 //
-// Both are bound by HBM: every byte is read once and written once.
+// Both are bound by HBM: every byte is read once and written once.  8384 tokens of 64
+// heads with the dense row: 28.3 us a call, 5.97 TB/s; 64 requests of 512 to 4096 keys read
+// back: 52.6 us, 6.35 TB/s.  A token or a few hundred keys are a chain of latencies,
+// 1.9 and 2.9 us on the GPU.
 #include <algorithm>
 #include <cmath>
 
@@ -232,9 +235,12 @@ cudaError_t launch_write(WriteParams& p, cudaStream_t st) {
 
 template <int LPR, bool HALF>
 cudaError_t launch_write_lpr(WriteParams& p, cudaStream_t st) {
-  // one step a warp until every SM has warps enough to hide the loads' latency
+  // One step a warp until every SM has warps enough to hide the loads' latency, then
+  // fewer warps that read the position and the table row again.  (One against four
+  // steps, heads of 64: 256 tokens of 128 heads 2.8 and 3.7 us, 512 of 64 2.9 and 3.8;
+  // 1024 of 64 4.6 and 4.2, 2048 of 128 12.1 and 8.9.)
   const long long warps = static_cast<long long>(p.T) * ((p.H + 32 / LPR - 1) / (32 / LPR));
-  return warps >= 64LL * current_sms() ? launch_write<LPR, LW_STEPS, HALF>(p, st)
+  return warps >= 48LL * current_sms() ? launch_write<LPR, LW_STEPS, HALF>(p, st)
                                        : launch_write<LPR, 1, HALF>(p, st);
 }
 
@@ -265,7 +271,8 @@ struct ReadParams {
 // Output row i belongs to request r with osl[r] <= i < osl[r + 1] and holds key
 // key_starts[r] + i - osl[r].  A warp takes GL_ROWS rows: that many lanes find
 // their row's request (binary search) and block, then the rows' pieces are
-// dealt out to the lanes one after the other.
+// dealt out to the lanes one after the other.  The kernel alone takes 49.4 us for 145 k
+// rows of 1152 bytes, 6.75 TB/s.
 __global__ void __launch_bounds__(GL_THREADS)
     gather_latent_kernel(const __grid_constant__ ReadParams p) {
   grid_dep_trigger();

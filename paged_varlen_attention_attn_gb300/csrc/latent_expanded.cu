@@ -21,9 +21,10 @@
 // tiles are 64 keys, each sub-tile has two score buffers in TMEM (4 x 64 columns beside
 // the 2 x dv of O), and both sub-tiles' MMAs on a tile follow each other at once: S_A,
 // S_B of tile j + 1, then P V_A, P V_B of tile j, from a warp each.  K and V then have
-// three stages, and the softmax of a tile runs under the MMAs of its neighbours.  The
-// price is S at N 64, which reads operands for 48 cycles an MMA against 32 of the
-// tensor core.
+// three stages, and the softmax of a tile runs under the MMAs of its neighbours: 1806
+// us, 1.25 PFLOP/s.  The price is S at N 64, which reads operands for 48 cycles an MMA
+// against 32 of the tensor core, and bounds it now.  (4 chunks of 2048 behind 6144, 16
+// heads: 476 us, 1.26 PFLOP/s; 6 short requests 7.6 us on the GPU.)
 //
 // Rotary parts shorter than 64 are widened with zeros by TMA (a box that reaches
 // past the row), so S is always a whole number of 64-element column blocks.
