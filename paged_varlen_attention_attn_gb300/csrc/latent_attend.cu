@@ -794,11 +794,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         const int tail = g.s - key0;
         if (tail < C::KEYS) {
           unsigned char* k = sK + (n % C::NST) * C::STAGE;
-          for (int e = threadIdx.x; e < (C::KEYS - tail) * 8 * nc; e += 128) {
-            const int row = tail + e / (8 * nc), x = e % (8 * nc);
-            *reinterpret_cast<uint4*>(k + ((row >> 3) * cols + (x >> 3)) * 1024 + (row & 7) * 128 +
-                                      (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
+          const int x = threadIdx.x & 63;  // 16-byte piece of a row
+          if (x < 8 * nc)
+            for (int row = tail + (threadIdx.x >> 6); row < C::KEYS; row += 2)
+              *reinterpret_cast<uint4*>(k + ((row >> 3) * cols + (x >> 3)) * 1024 + (row & 7) * 128 +
+                                        (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -851,14 +851,19 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             float o[C::EC];
             tc_ld_cols(lane_base + d * R + c, o);
             tc_wait_ld();
+            // (the stores last: behind one, the next weight's load and exchange would wait)
+            unsigned w[C::EC / 2];
+#pragma unroll
+            for (int e = 0; e < C::EC; ++e) o[e] *= bars->l[c + e];
+#pragma unroll
+            for (int e = 0; e < C::EC; e += 2) {
+              const float got = __shfl_xor_sync(FULL, odd ? o[e] : o[e + 1], 1);
+              w[e / 2] = odd ? pack2<HALF>(got, o[e + 1]) : pack2<HALF>(o[e], got);
+            }
             uint16_t* row = ob + static_cast<int64_t>(c) * p.dc;
 #pragma unroll
-            for (int e = 0; e < C::EC; e += 2, row += 2 * p.dc) {
-              const float x = o[e] * bars->l[c + e], y = o[e + 1] * bars->l[c + e + 1];
-              const float got = __shfl_xor_sync(FULL, odd ? x : y, 1);
-              if (c + e + odd < g.rows)
-                *reinterpret_cast<unsigned*>(row) = odd ? pack2<HALF>(got, y) : pack2<HALF>(x, got);
-            }
+            for (int e = 0; e < C::EC; e += 2, row += 2 * p.dc)
+              if (c + e + odd < g.rows) *reinterpret_cast<unsigned*>(row) = w[e / 2];
           }
       }
       tc_fence_before();
