@@ -24,12 +24,12 @@
 // rows two of 64.  (8 x 125 k keys, 32 heads: 200 us with two of 64, 208 with five of 32,
 // 192 so; 64 requests, 128 heads: 90 with two of 64, 92 with four of 32.)
 //
-// Measured: 8 x 125 k keys on 32 heads 186 us, 6.2 TB/s; 64 requests of 512 to 4096 keys
+// Measured: 8 x 125 k keys on 32 heads 187 us, 6.2 TB/s; 64 requests of 512 to 4096 keys
 // on 16 heads 44 (25 for the bytes: the start takes some 10 us and the merge 6), on
-// 128 heads 87; 24 chunks beside 40 single tokens on 32 heads 254 us, 501 TFLOP/s.
-// The last two are bound by a slot's life: load, S, softmax and P V one after the
-// other, with two slots, 3300 to 4400 cycles a tile, where the operands' way through
-// shared memory takes 2500.
+// 128 heads 84; 24 chunks beside 40 single tokens on 32 heads 227 us, 561 TFLOP/s.  The
+// last two are bound by a slot's life, with two of them: copy 1550 to 2000 cycles, S
+// 1310 (2100 beside a P V), softmax 1100 and P into shared memory 640 with the waits,
+// P V 690 to 1200.  (Eight softmax warps on half of the keys each: 85 and 229 us.)
 //
 // A tile lies as [8 keys][64-element column block][8 x 128 bytes], so that the rows
 // of a page land with one copy whatever the block size: a copy holds its warp for
