@@ -67,6 +67,32 @@ def test_keys_cut_over_the_gpu(lens, H):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("H", [16, 40])
+def test_lengths_around_the_tiles_of_48_keys(H):
+    lens = [(1, s) for s in (47, 48, 49, 95, 96, 97, 143, 144, 145, 191, 193)]
+    c = Paged(H, lens, H=H, dc=256, dr=64, bs=16, device=DEV, poison=True)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("H", [100, 512, 513, 1000])
+def test_single_tokens_of_many_heads(H):
+    c = Paged(H, [(1, 5), (0, 3), (1, 900), (1, 64)], H=H, dc=128, dr=16, bs=16, device=DEV, poison=True)
+    c.check(c.run())
+    assert status() == 0
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_longest_row_given_too_long_or_too_short(H):
+    c = Paged(8, [(1, 90), (3, 200), (1, 30)], H=H, dc=128, dr=64, bs=16, device=DEV)
+    c.check(c.run(max_query_len=77))
+    assert status() == 0
+    out = torch.full((5, H, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    c.run(out=out, max_query_len=1)  # with single tokens' layout the chunk is refused
+    if H == 128:
+        assert status() == 5 and (out[1:4] == 0).all()
+    c.check(out, requests=[0, 2])
+
+
 def test_many_requests():
     lens = [(1, 1 + (37 * i) % 400) for i in range(1500)]
     c = Paged(5, lens, H=16, dc=128, dr=64, bs=16, device=DEV)

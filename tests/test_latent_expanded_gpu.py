@@ -47,6 +47,13 @@ def test_many_items():
     c.check(c.run(), requests=range(0, 40, 3))
 
 
+def test_many_requests():
+    lens = [(1 + 5 * (i % 7 == 3), 6 + 11 * i % 90) for i in range(700)]
+    c = Dense(7, lens, H=2, dn=64, dr=16, device=DEV)
+    c.check(c.run(), requests=range(0, 700, 41))
+    assert status() == 0
+
+
 def test_requests_without_keys():
     c = Dense(2, [(3, 0), (4, 9), (2, 0)], H=3, dn=64, dr=32, device=DEV)
     c.check(c.run(causal=0), causal=0)

@@ -192,6 +192,39 @@ def test_replay_after_a_larger_call_took_another_workspace(make):
     pa.release_workspaces()
 
 
+def test_calls_back_to_back_wait_for_each_other():
+    """Each call reads what the call before wrote, or writes what it read, with nothing
+    between them; the kernels may be launched while the one before still runs."""
+    T, H, dc, dr, bs = 2048, 16, 512, 64, 16
+    c = Paged(8, [(1, 2048)] * 4, H=H, dc=dc, dr=dr, bs=bs, device=DEV)
+    slots = (c.table[:, :128].long().repeat_interleave(bs, 1) * bs + torch.arange(2048, device=DEV) % bs).flatten()
+    starts = torch.arange(0, 4 * T + 1, T, dtype=torch.int32, device=DEV)
+    size = dict(latent_size=dc, block_size=bs)
+    g = torch.Generator().manual_seed(2)
+    rows = [torch.randn(4 * T, dc + dr, generator=g).bfloat16().to(DEV) for _ in range(2)]
+
+    def steps(wait):
+        got = []
+        for i in range(12):
+            latent, key = rows[i % 2].split([dc, dr], 1)
+            pa.latent_rope_and_cache(None, latent, key, c.cache, slots, None, None, block_size=bs)
+            wait()
+            out = c.run()
+            wait()
+            back = pa.gather_latent(c.cache, c.table, starts, num_rows=4 * T, **size)
+            wait()
+            # the rows read back, turned over, overwrite the cache that both have read
+            pa.latent_rope_and_cache(None, back[0], back[1], c.cache, slots.flip(0), None, None, block_size=bs)
+            wait()
+            got += [out, c.run(), *back]
+            wait()
+        torch.cuda.synchronize()
+        return got
+
+    for x, y in zip(steps(torch.cuda.synchronize), steps(lambda: None)):
+        assert torch.equal(x, y)
+
+
 def test_calls_from_two_threads():
     calls = [make()[1] for make in CALLS]
     want = [call() for call in calls]
