@@ -59,11 +59,19 @@ _ROPE_PACK, _ATTEND_PACK, _EXPANDED_PACK = (_packer(c) for c in (LatentRopeArgs,
                                                                  LatentExpandedArgs))
 
 
+_types = {}  # kv_dtype -> torch dtype; the index tensors' types by their C names
+
+
 def _type_of(kv_dtype):
-    import torch
-    if kv_dtype not in (KV_BF16, KV_F16):
-        raise PattnError(2, "a cache of latent rows is KV_BF16 or KV_F16")
-    return torch.float16 if kv_dtype == KV_F16 else torch.bfloat16
+    dt = _types.get(kv_dtype)
+    if dt is None:
+        if kv_dtype not in (KV_BF16, KV_F16):
+            raise PattnError(2, "a cache of latent rows is KV_BF16 or KV_F16")
+        import torch
+        _types.update({KV_BF16: torch.bfloat16, KV_F16: torch.float16, "int32": torch.int32,
+                       "int64": torch.int64, "float": torch.float32})
+        dt = _types[kv_dtype]
+    return dt
 
 
 def _heads(x, name, dtype, dev):
@@ -106,6 +114,14 @@ def _index(x, name, dtype, shape, dev):
     return x.data_ptr()
 
 
+def _out(x, name, dtype, shape, dev, stream):
+    """(tensor, address) of a contiguous output: x if it is one, or a new one."""
+    if x is None:
+        x = _empty(shape, dtype, dev, stream)
+        return x, x.data_ptr()
+    return x, _index(x, name, dtype, shape, dev)
+
+
 def latent_rope_and_cache(q, latent, k_rope, kv_cache, slot_mapping, positions, cos_sin, *,
                           block_size, kv_dtype=KV_BF16, interleaved=False, latent_norm=None,
                           norm_eps=1e-6, q_out=None, row_out=None, device_status=None,
@@ -124,7 +140,6 @@ def latent_rope_and_cache(q, latent, k_rope, kv_cache, slot_mapping, positions, 
     ``device_status``: optional int32/uint32 tensor of one element that collects
     bit 1 for slots past the pool and positions outside the table.  Returns
     ``q_out``; raises PattnError or ValueError."""
-    import torch
     dt = _type_of(kv_dtype)
     dev = kv_cache.device
     NB, row = _cache(kv_cache, dt, block_size)
@@ -143,20 +158,22 @@ def latent_rope_and_cache(q, latent, k_rope, kv_cache, slot_mapping, positions, 
             raise ValueError("q must be [num_tokens, heads, rope_size]")
         if q_out is None:
             q_out = _empty(q.shape, dt, dev, stream)
-        o_at, o_st, o_sh = _heads(q_out, "q_out", dt, dev)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
+            o_at, o_st, o_sh = q_out.data_ptr(), H * dr, dr
+        else:
+            o_at, o_st, o_sh = _heads(q_out, "q_out", dt, dev)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
     elif q_out is not None:
         raise ValueError("q_out goes with q")
     if row_out is not None:
         row_at, row_st = _rows(row_out, "row_out", dt, dev)
         if row_out.shape != (T, row):
             raise ValueError("row_out must be [num_tokens, latent_size + rope_size]")
-    slots_at = _index(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
+    slots_at = _index(slot_mapping, "slot_mapping", _types["int64"], (T,), dev)
     pos_at = table_at = max_pos = 0
     if positions is not None:
-        pos_at = _index(positions, "positions", torch.int64, (T,), dev)
-        if (cos_sin is None or cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != dr or
+        pos_at = _index(positions, "positions", _types["int64"], (T,), dev)
+        if (cos_sin is None or cos_sin.dtype != _types["float"] or cos_sin.dim() != 2 or cos_sin.shape[1] != dr or
                 cos_sin.device != dev or not cos_sin.is_contiguous()):
             raise ValueError("cos_sin must be a contiguous fp32 [max_position, rope_size] tensor")
         table_at, max_pos = cos_sin.data_ptr(), cos_sin.shape[0]
@@ -185,23 +202,19 @@ def gather_latent(kv_cache, block_table, out_start_loc, *, num_rows, latent_size
     of ``latent_out`` [num_rows, latent_size] and ``rope_out`` [num_rows, rope_size]
     (default: new tensors).  Returns (latent_out, rope_out); raises PattnError or
     ValueError."""
-    import torch
     dt = _type_of(kv_dtype)
     dev = kv_cache.device
     NB, row = _cache(kv_cache, dt, block_size)
     dr = row - latent_size
     B, mbps = block_table.shape
-    bt_at = _index(block_table, "block_table", torch.int32, (B, mbps), dev)
-    osl_at = _index(out_start_loc, "out_start_loc", torch.int32, (B + 1,), dev)
-    ks_at = 0 if key_starts is None else _index(key_starts, "key_starts", torch.int32, (B,), dev)
+    i32 = _types["int32"]
+    bt_at = _index(block_table, "block_table", i32, (B, mbps), dev)
+    osl_at = _index(out_start_loc, "out_start_loc", i32, (B + 1,), dev)
+    ks_at = 0 if key_starts is None else _index(key_starts, "key_starts", i32, (B,), dev)
     if latent_size <= 0 or dr <= 0 or num_rows < 0:
         raise PattnError(1, "pattn_gather_latent")
-    if latent_out is None:
-        latent_out = _empty((num_rows, latent_size), dt, dev, stream)
-    if rope_out is None:
-        rope_out = _empty((num_rows, dr), dt, dev, stream)
-    lat_at = _index(latent_out, "latent_out", dt, (num_rows, latent_size), dev)
-    rope_at = _index(rope_out, "rope_out", dt, (num_rows, dr), dev)
+    latent_out, lat_at = _out(latent_out, "latent_out", dt, (num_rows, latent_size), dev, stream)
+    rope_out, rope_at = _out(rope_out, "rope_out", dt, (num_rows, dr), dev, stream)
     status_at = _status_at(device_status, dev)
     if num_rows == 0 or B == 0:  # (an empty tensor has no address)
         return latent_out, rope_out
@@ -234,17 +247,18 @@ def _scratch(workspace, need, dev, stream):
     workspace of at least ``need`` bytes."""
     raw = _raw_stream(stream, dev)
     ws = _workspace(workspace, dev, raw)
-    buf = ws.current(dev)
-    if buf is None or buf.numel() < need:
-        buf = ws.get(need, dev, stream)
-    ws.used_on(raw)
-    at, size = buf.data_ptr(), buf.numel()
     ext = getattr(ws, "_ext", None)
-    if ext is None or ext.workspace != at or (ext.stream or 0) != raw:
-        ext = ws._ext = Ext.from_buffer_copy(_pack(_EXT_PACK, "workspace", _EXT_PACK.size, 0, 0, 0, 0,
-                                                   0, 0, 0, at, size, raw, 0, 0, 0))
+    if (ext is None or ext._workspace_keepalive is not ws.buf or ext._bytes < need or
+            ext._raw != raw or ext._device != dev):
+        buf = ws.get(need, dev, stream)
+        at, size = buf.data_ptr(), buf.numel()
+        ext = Ext.from_buffer_copy(_pack(_EXT_PACK, "workspace", _EXT_PACK.size, 0, 0, 0, 0, 0, 0, 0,
+                                         at, size, raw, 0, 0, 0))
+        ext._at, ext._bytes, ext._raw, ext._device = at, size, raw, dev
         ext._workspace_keepalive = buf  # (its status word may be read after a larger call)
-    return at, size, raw, ext
+        ws._ext = ext
+    ws.used_on(raw)
+    return ext._at, ext._bytes, raw, ext
 
 
 def latent_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale, latent_size,
@@ -260,7 +274,6 @@ def latent_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale
     with ``forward`` and not needed.  ``workspace``: a Workspace (default: one per
     stream and host thread).  ``latent_forward.last_ext`` serves
     pattn_read_device_status.  Raises PattnError or ValueError."""
-    import torch
     dt = _type_of(kv_dtype)
     dev = q.device
     NB, row = _cache(kv_cache, dt, block_size)
@@ -270,12 +283,11 @@ def latent_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale
                          "tensor on the cache's device")
     T, H, _ = q.shape
     B, mbps = block_table.shape
-    bt_at = _index(block_table, "block_table", torch.int32, (B, mbps), dev)
-    sl_at = _index(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    qsl_at = _index(query_start_loc, "query_start_loc", torch.int32, (B + 1,), dev)
-    if out is None:
-        out = _empty((T, H, latent_size), dt, dev, stream)
-    out_at = _index(out, "out", dt, (T, H, latent_size), dev)
+    i32 = _types["int32"]
+    bt_at = _index(block_table, "block_table", i32, (B, mbps), dev)
+    sl_at = _index(seq_lens, "seq_lens", i32, (B,), dev)
+    qsl_at = _index(query_start_loc, "query_start_loc", i32, (B + 1,), dev)
+    out, out_at = _out(out, "out", dt, (T, H, latent_size), dev, stream)
     if T == 0 or B == 0:  # (an empty tensor has no address)
         return out
     latent_size = int(latent_size)
@@ -304,7 +316,6 @@ def latent_expanded_forward(q, k_nope, k_rope, value, query_start_loc, key_start
     ``max_key_len`` are taken for the likeness with ``forward`` and not needed.
     ``latent_expanded_forward.last_ext`` serves pattn_read_device_status.  Raises
     PattnError or ValueError."""
-    import torch
     dt = _type_of(kv_dtype)
     dev = q.device
     q_at, q_st, q_sh = _heads(q, "q", dt, dev)
@@ -319,11 +330,9 @@ def latent_expanded_forward(q, k_nope, k_rope, value, query_start_loc, key_start
         raise ValueError("q, k_nope, k_rope and value must be [num_tokens, heads, nope + rope], "
                          "[num_keys, heads, nope], [num_keys, rope] and [num_keys, heads, value]")
     B = query_start_loc.shape[0] - 1
-    qsl_at = _index(query_start_loc, "query_start_loc", torch.int32, (B + 1,), dev)
-    ksl_at = _index(key_start_loc, "key_start_loc", torch.int32, (B + 1,), dev)
-    if out is None:
-        out = _empty((T, H, dv), dt, dev, stream)
-    out_at = _index(out, "out", dt, (T, H, dv), dev)
+    qsl_at = _index(query_start_loc, "query_start_loc", _types["int32"], (B + 1,), dev)
+    ksl_at = _index(key_start_loc, "key_start_loc", _types["int32"], (B + 1,), dev)
+    out, out_at = _out(out, "out", dt, (T, H, dv), dev, stream)
     if T == 0 or B <= 0:  # (an empty tensor has no address)
         return out
     if K == 0:  # (likewise: no key is read)
