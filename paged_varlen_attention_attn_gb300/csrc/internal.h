@@ -101,7 +101,8 @@ struct Problem {
 
 #ifdef PATTN_WAIT_TEST
 // Wait-test build only: sets Problem::test_skip for the calls that follow
-// (0 turns it off).  Exported as pattn_test_set_wait_skip.
+// (0 turns it off; 3 and 4 are the first key tile of the latent attentions, absorbed
+// and expanded).  Exported as pattn_test_set_wait_skip.
 extern "C" void pattn_test_set_wait_skip(int mode);
 int test_wait_skip();
 #endif

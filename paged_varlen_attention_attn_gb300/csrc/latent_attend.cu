@@ -101,6 +101,7 @@ struct LaProblem {
   int lanes;        // CTAs side by side on a share (1, or the row tiles of a token)
   int max_shares;
   int fused;        // rotary parts of 64 elements: copied with the latents
+  int test_skip;    // wait-test build only
 };
 
 // A request's rows and keys; false (and the rows clipped to out) if they are bad.
@@ -504,6 +505,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     Walk w = {bars->cuts[0], bars->cuts[1]};
     Seg g;
     int pos = 0, ok = 1;
+#ifdef PATTN_WAIT_TEST
+    // wait-test build: this tile's first half posts no bytes and issues no copy
+    const int skip_pos = (p.test_skip == 3 && half == 0 && blockIdx.x == 0) ? 0 : -1;
+#else
+    constexpr int skip_pos = -1;
+#endif
     const int page = (p.fused && half ? first : 0) + lane;  // this lane's
     const int last = half ? ppt : first;
     const int page_bytes = rot ? LA_BOX * 128 : LA_BOX * 128 * cols;
@@ -539,6 +546,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
 #pragma unroll
         for (int e = 0; e < LA_AHEAD; ++e) rows[e] = rows[e + 1];
         rows[LA_AHEAD] = page_row(kt + 1 + LA_AHEAD);
+        if (pos == skip_pos) continue;
         const int copies = __popc(__ballot_sync(FULL, row >= 0));
         if (lane == 0) {
           if (pos >= C::NST &&
@@ -565,7 +573,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     // CTA exits.  (A slot's phase also needs the other producer's bytes; if that one
     // gave up first, this wait runs out instead.)
     if ((!ok || *abort_flag) && lane == 0) {
-      drain_armed(bars->k_full, C::NST, pos, -1, status);
+      drain_armed(bars->k_full, C::NST, pos, skip_pos, status);
     }
     __syncwarp();
   } else if (warp == 5 || warp == 7) {
@@ -1121,6 +1129,9 @@ extern "C" pattn_status_t pattn_latent_fwd(const pattn_latent_t* a) {
   p.lanes = a->max_query_len <= 1 && tiles > 1 && tiles <= 8 ? tiles : 1;
   p.max_shares = std::max(1, l.grid / p.lanes);
   p.fused = a->rope_size == 64;
+#ifdef PATTN_WAIT_TEST
+  p.test_skip = test_wait_skip();
+#endif
   CUtensorMap m[4];
   if (!encode_latent_maps(m, a->q, a->kv_cache, p.half, a->latent_size, a->rope_size,
                           a->num_tokens * a->num_heads, R, a->num_blocks * a->block_size, LA_BOX))

@@ -74,6 +74,7 @@ struct ExProblem {
   int few;  // an item a CTA at most: the CTAs list the items themselves
   int B, T, K, H, causal;
   float sl2;
+  int test_skip;  // wait-test build only
 };
 
 // NB: 64-element column blocks of the part without rotation (dn = dv = 64 NB).
@@ -423,6 +424,12 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(EX_OTHER_REGS));
     if (warp == 8 && lane == 0) {
       // ------------------------------------------------------------ Q and K
+#ifdef PATTN_WAIT_TEST
+      // wait-test build: this tile posts no bytes and issues no copy
+      const int skip_pos = (p.test_skip == 4 && blockIdx.x == 0) ? 0 : -1;
+#else
+      constexpr int skip_pos = -1;
+#endif
       int jg = 0, n_worked = 0, armed_end = 0, q_arms0 = 0, q_arms1 = 0;
       bool ok = true;
       int idx = claim(0);
@@ -458,8 +465,9 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&bars->k_full[st], C::KTILE);
           armed_end = jg + 1;
+          if (jg == skip_pos) continue;
+          mbar_arrive_expect_tx(&bars->k_full[st], C::KTILE);
           const int row = it.k0 + j * EX_KEYS;
           tma_load_4d(sK + st * C::KTILE, &kmap, &bars->k_full[st], 0, row, 0, it.h);
           tma_load_4d(sK + st * C::KTILE + NB * C::BLK, &rmap, &bars->k_full[st], 0, row, 0, 0);
@@ -470,7 +478,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       // A role gave up on a wait: no copy may still be writing shared memory when
       // the CTA exits.
       if (!ok || idx < 0 || *abort_flag) {
-        drain_armed(bars->k_full, C::ST, armed_end, -1, status);
+        drain_armed(bars->k_full, C::ST, armed_end, skip_pos, status);
         if (q_arms0 > 0) mbar_wait(&bars->q_full[0], (q_arms0 - 1) & 1, status, nullptr);
         if (q_arms1 > 0) mbar_wait(&bars->q_full[1], (q_arms1 - 1) & 1, status, nullptr);
       }
@@ -849,6 +857,9 @@ extern "C" pattn_status_t pattn_latent_expanded_fwd(const pattn_latent_expanded_
   p.causal = a->causal;
   p.few = l.max_tiles <= EX_FEW &&
           static_cast<long long>(l.max_tiles) * a->num_heads <= current_sms();
+#ifdef PATTN_WAIT_TEST
+  p.test_skip = test_wait_skip();
+#endif
   // strictly positive, so that a masked score (-inf) always maps to weight 0; at
   // scale 0 the weights are 1 exactly
   p.sl2 = fmaxf(a->scale * LOG2E, 1e-30f);
