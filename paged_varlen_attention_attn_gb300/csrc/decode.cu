@@ -220,6 +220,18 @@ __device__ __forceinline__ void merge_partitions(const Problem& p, int r, int h,
   }
 }
 
+// Behind the prefill of a mixed batch this grid starts without waiting for it, but it
+// must not end before it: what follows in the stream (in a captured graph, or as a
+// programmatic dependent) waits for this grid alone.  One thread of the last CTA waits
+// on its way out; every way out of the kernel passes here.  (All CTAs waiting would
+// keep later ones off the SMs.  The CTA holds nothing that the prefill still needs: all
+// of the prefill's CTAs are running, or gone, when this grid starts.)
+__device__ __forceinline__ void end_behind_prefill(const Problem& p) {
+  if (p.pdl_launch && !p.pdl_wait && blockIdx.x + 1 == gridDim.x &&
+      threadIdx.x + 1 == blockDim.x)
+    grid_dep_wait();
+}
+
 // HALF: q, a 16-bit cache and out are f16 (else bf16; an e4m3 cache goes with
 // bf16 q and out).
 //
@@ -281,6 +293,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH, ROWS>::THREADS,
         for (int64_t e = a + threadIdx.x; e < b; e += blockDim.x) out[e] = __float2bfloat16_rn(0.f);
       }
     }
+    end_behind_prefill(p);
     return;
   }
   int s = p.seq_lens[r];
@@ -288,7 +301,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH, ROWS>::THREADS,
   unsigned* status = &p.hdr->status;
   if (bad) {
     if (threadIdx.x == 0 && sp == 0) flag_status(status, PATTN_DEV_BAD_METADATA);
-    if (t0 < 0 || t0 >= p.T) return;
+    if (t0 < 0 || t0 >= p.T) {
+      end_behind_prefill(p);
+      return;
+    }
     s = 0;  // treat as empty: the rows become zero
   }
 
@@ -387,6 +403,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, FP8, NT, HG, WPH, ROWS>::THREADS,
     // stage's phase also needs the other producer's bytes; if that warp gave
     // up first, this wait runs out (bounded) instead.
     if (!ok && lane == 0) drain_armed(full, NST, armed_end, skip_pos, status);
+    end_behind_prefill(p);  // (the CTA's last thread is a producer's)
     return;  // nothing after this needs the producers
   }
 

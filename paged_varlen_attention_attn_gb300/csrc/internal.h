@@ -76,7 +76,7 @@ struct Problem {
                     // the stream has finished
   int pdl_wait;     // ...and waits for it (griddepcontrol.wait) before it touches
                     // the status word or the partition counters, which that
-                    // kernel clears
+                    // kernel clears; without, only its last CTA waits, at its end
   int pdl_trigger;  // the prefill kernel lets its dependent start once all of
                     // its CTAs are running (decode CTAs then take the SMs that
                     // finished prefill CTAs leave)
@@ -239,7 +239,12 @@ cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<unsig
 
 // A launch whose CTAs may take their places before the kernel before it has finished;
 // the kernel waits for it (grid_dep_wait) before it touches anything a kernel before
-// could have written or read, so it is ordered like any other.  (Back to back: a
+// could have written or read.  The wait is for that one kernel.  It orders the launch
+// behind the whole stream because no kernel ends before those in front of it: an
+// ordinary launch waits for all of them, and every dependent launch of this library
+// waits in all of its CTAs, or in its last one where it means to overlap the kernel
+// before it (the decodes of a mixed batch).  A kernel that ended without a wait would
+// break that for whatever follows it.  (Back to back: a
 // latent cache write of 8384 tokens 30.7 -> 28.4 us, a read-back of 64 requests 55.3 ->
 // 52.6, a decode of 64 requests on 16 heads 47.1 -> 44.8; calls of a few tokens, which
 // the host bounds, the same.)

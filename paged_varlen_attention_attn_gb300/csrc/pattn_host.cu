@@ -736,8 +736,9 @@ pattn_status_t pattn_varlen_fwd(const void* q, const void* kv_cache, const int32
   // unless per-phase events sit between them.  After the prep kernel it
   // waits for it before it starts (it reads the order that kernel writes);
   // after the prefill kernel (which starts only once the plan kernel's writes
-  // are done) it has nothing to wait for, and it may take the SMs of finished
-  // prefill CTAs.
+  // are done) it has nothing to wait for before its work, and it may take the
+  // SMs of finished prefill CTAs; its last CTA waits at its end, so that the
+  // call is over when this kernel is.
   const bool timed = ext->timing_events != nullptr;
   p.pdl_launch = timed ? 0 : 1;
   p.pdl_wait = tc_prefill ? 0 : 1;
