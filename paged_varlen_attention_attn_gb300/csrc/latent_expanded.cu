@@ -103,6 +103,7 @@ struct ExBars {
   // by sub-tile and score buffer (a phase of one waits for the last one's reader):
   // scores there, weights there, P V of the weights done
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];
+  uint64_t v_clean[4];  // a V stage's rows behind the request's keys are zero
   uint64_t drain[4];
   uint64_t ring_full[EX_RING], ring_empty[EX_RING];
   int ring[EX_RING];
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       mbar_init(&bars->k_empty[i], 2);  // one arrival of each sub-tile
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_empty[i], 2);
+      mbar_init(&bars->v_clean[i], 1);
     }
     mbar_init(&bars->q_empty, 2);
     // the item ring: posted by warp 8; taken by warps 9 to 13 and each softmax warp
@@ -526,6 +528,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       int jg = 0;     // key tiles of the items so far (ring position)
       int cnt = 0;    // of this sub-tile (its score buffer and phase)
       int q_tot = 0;  // its Q tiles
+      unsigned clean = 0u;  // sub-tile 0: the phase of each V stage's next clearing, a bit each
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int idx = take(k);
@@ -535,8 +538,10 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
         if (!__any_sync(FULL, it.live)) break;
         const int mine = static_cast<int>(
             __reduce_max_sync(FULL, static_cast<unsigned>(ex_sub(p, it, X).n)));
-        const int n = max(mine, static_cast<int>(__reduce_max_sync(
-                                    FULL, static_cast<unsigned>(ex_sub(p, it, 1 - X).n))));
+        const int other = static_cast<int>(
+            __reduce_max_sync(FULL, static_cast<unsigned>(ex_sub(p, it, 1 - X).n)));
+        const int n = max(mine, other);
+        const bool two = other > 0;
         if (n == 0) continue;
         if (scores && mine > 0) {
           if (!__all_sync(FULL, mbar_wait(&bars->q_full[X], q_tot & 1, status, abort_flag))) break;
@@ -560,6 +565,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
           if (!active) {  // nothing for this sub-tile (released only now that it is full:
                           // the barrier counts one arrival of each sub-tile per phase)
             if (lead) mbar_arrive(empty);
+            if (it.s - j * EX_KEYS < EX_KEYS) clean ^= 1u << st;
             continue;
           }
           tc_fence_after();
@@ -574,16 +580,27 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
             if (lead) tc_commit(&bars->s_full[X][b]);
           } else {
             // V rows at or past the request's keys become zero: they may hold anything,
-            // and 0 * NaN is NaN.  (Both sub-tiles' warps do it, each before its MMAs.)
+            // and 0 * NaN is NaN.  They are in the item's last tile, where sub-tile 1, if
+            // it has rows, is active: its warp clears them, and sub-tile 0's waits for it.
             const int rows = it.s - j * EX_KEYS;
             if (rows < EX_KEYS) {
-              for (int e = lane; e < (EX_KEYS - rows) * 8 * NB; e += 32) {
-                const int r = rows + e / (8 * NB), x = e % (8 * NB);
-                *reinterpret_cast<uint4*>(sV + st * C::VTILE + (x >> 3) * C::BLK + r * 128 +
-                                          (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              if (X == 0 && two) {
+                if (!__all_sync(FULL, mbar_wait(&bars->v_clean[st], (clean >> st) & 1u, status,
+                                                abort_flag))) {
+                  ok = false;
+                  break;
+                }
+                clean ^= 1u << st;
+              } else {
+                for (int e = lane; e < (EX_KEYS - rows) * 8 * NB; e += 32) {
+                  const int r = rows + e / (8 * NB), x = e % (8 * NB);
+                  *reinterpret_cast<uint4*>(sV + st * C::VTILE + (x >> 3) * C::BLK + r * 128 +
+                                            (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (X == 1 && lane == 0) mbar_arrive(&bars->v_clean[st]);
               }
-              fence_proxy_async_smem();
-              __syncwarp();
             }
             const uint64_t vb = v_d + ((st * C::VTILE) >> 4);
 #pragma unroll
