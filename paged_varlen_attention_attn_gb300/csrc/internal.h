@@ -28,6 +28,13 @@ struct WsHeader {
   int pad[60];
 };
 
+// The status word of a call whose kernel clears it itself: no CTA may OR into a word
+// that another may clear later, so each stores its own word behind the header, and the
+// header's holds their number above the PATTN_DEV_* bits (0: there are none).
+// pattn_read_device_status puts them together.
+constexpr int STATUS_WORDS_SHIFT = 8;
+constexpr int MAX_STATUS_WORDS = 256;
+
 struct Problem {
   const void* q;
   const void* kv;
@@ -102,7 +109,8 @@ struct Problem {
 #ifdef PATTN_WAIT_TEST
 // Wait-test build only: sets Problem::test_skip for the calls that follow
 // (0 turns it off; 3 and 4 are the first key tile of the latent attentions, absorbed
-// and expanded).  Exported as pattn_test_set_wait_skip.
+// and expanded; 5 that of the expanded one's last CTA, beside a late first CTA).
+// Exported as pattn_test_set_wait_skip.
 extern "C" void pattn_test_set_wait_skip(int mode);
 int test_wait_skip();
 #endif

@@ -56,7 +56,7 @@ constexpr float EX_SUM_LIMIT = 256.f;  // 2^EX_RESCALE_LOG2
 constexpr unsigned FULL = 0xffffffffu;
 
 struct ExHeader {
-  unsigned status;
+  unsigned status;      // (see STATUS_WORDS_SHIFT)
   int tiles;            // written by the plan kernel
   unsigned next_item;   // zeroed by the plan kernel
   int pad[61];
@@ -69,6 +69,7 @@ struct ExProblem {
   const int* ksl;
   void* out;
   ExHeader* hdr;
+  unsigned* words;  // behind the header: the CTAs' own status, where few
   int2* tiles;
   int max_tiles;
   int few;  // an item a CTA at most: the CTAs list the items themselves
@@ -107,6 +108,7 @@ struct ExBars {
   uint64_t drain[4];
   uint64_t ring_full[EX_RING], ring_empty[EX_RING];
   int ring[EX_RING];
+  unsigned status;  // of this CTA
   unsigned tmem_base;
   int abort_flag;
 };
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   ExBars* bars = reinterpret_cast<ExBars*>(smem + C::BAR_OFF);
-  unsigned* status = &p.hdr->status;
+  unsigned* status = &bars->status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -342,6 +344,7 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       mbar_init(&bars->ring_empty[i], 5 + 8);
     }
     bars->abort_flag = 0;
+    bars->status = 0u;
     fence_mbar_init();
     tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&kmap);
@@ -360,6 +363,11 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
   volatile int* abort_flag = &bars->abort_flag;
   grid_dep_trigger();
   grid_dep_wait();  // the plan kernel's list, or whatever came before
+#ifdef PATTN_WAIT_TEST
+  // wait-test build: a first CTA that starts late, some 40 ms behind the others
+  if (p.test_skip == 5 && blockIdx.x == 0)
+    for (int i = 0; i < 40; ++i) __nanosleep(1000000u);
+#endif
   const int2* tiles = p.tiles;
   int n_items;
   if (p.few) {
@@ -388,7 +396,8 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
     for (int t = 0; t < mine && at + t < p.max_tiles; ++t)
       few_tiles[at + t] = make_int2(r, fine ? t : -1 - t);
     if (blockIdx.x == 0 && threadIdx.x == 0)
-      *status = bad || total > p.max_tiles ? PATTN_DEV_BAD_METADATA : 0u;
+      p.hdr->status = (gridDim.x << STATUS_WORDS_SHIFT) |
+                      (bad || total > p.max_tiles ? PATTN_DEV_BAD_METADATA : 0u);
     n_items = min(total, p.max_tiles) * p.H;
     tiles = few_tiles;
     __syncthreads();
@@ -428,7 +437,10 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
       // ------------------------------------------------------------ Q and K
 #ifdef PATTN_WAIT_TEST
       // wait-test build: this tile posts no bytes and issues no copy
-      const int skip_pos = (p.test_skip == 4 && blockIdx.x == 0) ? 0 : -1;
+      const int skip_pos = (p.test_skip == 4 && blockIdx.x == 0) ||
+                                   (p.test_skip == 5 && blockIdx.x + 1 == gridDim.x)
+                               ? 0
+                               : -1;
 #else
       constexpr int skip_pos = -1;
 #endif
@@ -784,6 +796,12 @@ __global__ void __launch_bounds__(EX_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) {
+    // (the plan kernel has cleared the call's word; in a call without one, the first CTA
+    // may do so after this one has ended)
+    if (p.few) p.words[blockIdx.x] = bars->status;
+    else if (bars->status) flag_status(&p.hdr->status, bars->status);
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -798,7 +816,7 @@ struct ExLayout {
 ExLayout ex_layout(int B, int T) {
   ExLayout l;
   l.max_tiles = T / EX_ROWS + B;  // a request's last item may be short
-  l.tiles_off = sizeof(ExHeader);
+  l.tiles_off = sizeof(ExHeader) + MAX_STATUS_WORDS * sizeof(unsigned);
   l.total = l.tiles_off + (static_cast<size_t>(l.max_tiles) * sizeof(int2) + 255) / 256 * 256;
   return l;
 }
@@ -865,6 +883,7 @@ extern "C" pattn_status_t pattn_latent_expanded_fwd(const pattn_latent_expanded_
   p.ksl = a->key_start_loc;
   p.out = a->out;
   p.hdr = static_cast<ExHeader*>(a->workspace);
+  p.words = reinterpret_cast<unsigned*>(p.hdr + 1);
   p.tiles = reinterpret_cast<int2*>(static_cast<unsigned char*>(a->workspace) + l.tiles_off);
   p.max_tiles = l.max_tiles;
   p.B = a->num_seqs;
@@ -873,7 +892,8 @@ extern "C" pattn_status_t pattn_latent_expanded_fwd(const pattn_latent_expanded_
   p.H = a->num_heads;
   p.causal = a->causal;
   p.few = l.max_tiles <= EX_FEW &&
-          static_cast<long long>(l.max_tiles) * a->num_heads <= current_sms();
+          static_cast<long long>(l.max_tiles) * a->num_heads <=
+              std::min(current_sms(), MAX_STATUS_WORDS);
 #ifdef PATTN_WAIT_TEST
   p.test_skip = test_wait_skip();
 #endif

@@ -632,6 +632,16 @@ pattn_status_t pattn_read_device_status(const pattn_ext_t* ext) {
       cudaSuccess)
     return PATTN_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return PATTN_ERR_CUDA;
+  const unsigned words = host >> STATUS_WORDS_SHIFT;
+  if (words > 0 && words <= MAX_STATUS_WORDS &&
+      ext->workspace_bytes >= sizeof(WsHeader) + words * sizeof(unsigned)) {
+    unsigned more[MAX_STATUS_WORDS];
+    if (cudaMemcpyAsync(more, hdr + 1, words * sizeof(unsigned), cudaMemcpyDeviceToHost, st) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+      return PATTN_ERR_CUDA;
+    for (unsigned i = 0; i < words; ++i) host |= more[i];
+  }
   if (cudaMemsetAsync(&hdr->status, 0, sizeof(unsigned), st) != cudaSuccess) return PATTN_ERR_CUDA;
   if (host & PATTN_DEV_TIMEOUT) return PATTN_ERR_DEVICE_TIMEOUT;
   if (host & PATTN_DEV_BAD_METADATA) return PATTN_ERR_BAD_METADATA;
