@@ -666,6 +666,7 @@ class Workspace:
         self._stream = None  # whose pool the buffer is from (cudaStream_t)
         self._held = False   # not to be given back when it is replaced
         self._replaced = []
+        self._ext = None     # of calls that take the buffer as it is (latent.py's)
 
     def current(self, device):
         """The buffer it has on ``device``, or None."""
@@ -683,7 +684,7 @@ class Workspace:
             buf = _empty(nbytes, torch.uint8, device, stream)
             if self._held:
                 self._replaced.append(self.buf)
-            self.buf, self._held = buf, False
+            self.buf, self._held, self._ext = buf, False, None
             self._stream = _raw_stream(stream, device) if device.type == "cuda" else 0
         return self.buf
 

@@ -244,12 +244,12 @@ def _workspace_bytes(name, dev, *sizes):
 
 def _scratch(workspace, need, dev, stream):
     """(address, bytes, raw stream, Ext for pattn_read_device_status) of a call's
-    workspace of at least ``need`` bytes."""
+    workspace of at least ``need`` bytes.  (The Ext lasts as long as the buffer: a
+    Workspace drops it with the buffer that it replaces.)"""
     raw = _raw_stream(stream, dev)
     ws = _workspace(workspace, dev, raw)
-    ext = getattr(ws, "_ext", None)
-    if (ext is None or ext._workspace_keepalive is not ws.buf or ext._bytes < need or
-            ext._raw != raw or ext._device != dev):
+    ext = ws._ext
+    if ext is None or ext._bytes < need or ext._raw != raw or ext._device != dev:
         buf = ws.get(need, dev, stream)
         at, size = buf.data_ptr(), buf.numel()
         ext = Ext.from_buffer_copy(_pack(_EXT_PACK, "workspace", _EXT_PACK.size, 0, 0, 0, 0, 0, 0, 0,
@@ -273,7 +273,8 @@ def latent_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale
     selects the layout for single tokens).  ``max_seq_len`` is taken for the likeness
     with ``forward`` and not needed.  ``workspace``: a Workspace (default: one per
     stream and host thread).  ``latent_forward.last_ext`` serves
-    pattn_read_device_status.  Raises PattnError or ValueError."""
+    pattn_read_device_status, which tells (and clears) the status of the latest call
+    on that workspace, of whichever operator.  Raises PattnError or ValueError."""
     dt = _type_of(kv_dtype)
     dev = q.device
     NB, row = _cache(kv_cache, dt, block_size)
@@ -314,8 +315,8 @@ def latent_expanded_forward(q, k_nope, k_rope, value, query_start_loc, key_start
     that are multiples of 8 elements (k_nope and value may be views of one
     up-projection).  Returns ``out`` [T, H, nope].  ``max_query_len`` and
     ``max_key_len`` are taken for the likeness with ``forward`` and not needed.
-    ``latent_expanded_forward.last_ext`` serves pattn_read_device_status.  Raises
-    PattnError or ValueError."""
+    ``latent_expanded_forward.last_ext`` serves pattn_read_device_status, as for
+    ``latent_forward``.  Raises PattnError or ValueError."""
     dt = _type_of(kv_dtype)
     dev = q.device
     q_at, q_st, q_sh = _heads(q, "q", dt, dev)
