@@ -592,7 +592,8 @@ pattn_status_t pattn_gather_latent(const void* kv_cache, const int32_t* block_ta
  *
  * with the requests, block table, lengths, causal mask, metadata checks and
  * status word of pattn_varlen_fwd (row i of request r at position seq_len -
- * q_len + i).  A request's cached rows are read once for all its rows' heads up
+ * q_len + i); a seq_len above 2^31 - 256 is bad metadata too, however wide the
+ * block table.  A request's cached rows are read once for all its rows' heads up
  * to 64 (row, head) pairs; the keys are cut into equal shares over the GPU, and
  * requests that several shares touch are merged by log-sum-exp in a fixed order.
  */

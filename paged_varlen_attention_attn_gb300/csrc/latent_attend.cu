@@ -66,6 +66,7 @@ constexpr int LA_BOX = 16;            // cache rows of a copy (runs of 32 took a
                                       // for 64 requests of 128 heads)
 constexpr int LA_AHEAD = 1;           // tiles asked for in L2 before their copies
 constexpr float LA_RESCALE_LOG2 = 8.f;
+constexpr int LA_MOST_KEYS = 0x7fffff00;  // of a request: 32 bits hold a few tiles more
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_SHARES = 160;  // (the merge keeps their weights in shared memory)
 
@@ -110,8 +111,8 @@ __device__ __forceinline__ bool la_request(const LaProblem& p, int r, int& t0, i
   q = p.qsl[r + 1] - t0;
   s = p.seq_lens[r];
   if (q == 0) return true;
-  if (q > 0 && s >= q && s <= static_cast<int64_t>(p.mbps) * p.bs && t0 >= 0 && q <= p.T - t0 &&
-      (p.lanes == 1 || q == 1))
+  if (q > 0 && s >= q && s <= static_cast<int64_t>(p.mbps) * p.bs && s <= LA_MOST_KEYS && t0 >= 0 &&
+      q <= p.T - t0 && (p.lanes == 1 || q == 1))
     return true;
   const int64_t end = static_cast<int64_t>(t0) + q;
   t0 = min(max(t0, 0), p.T);
