@@ -288,10 +288,12 @@ def latent_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale
     bt_at = _index(block_table, "block_table", i32, (B, mbps), dev)
     sl_at = _index(seq_lens, "seq_lens", i32, (B,), dev)
     qsl_at = _index(query_start_loc, "query_start_loc", i32, (B + 1,), dev)
+    latent_size = int(latent_size)
+    if not 0 < latent_size < row:
+        raise PattnError(1, "pattn_latent_fwd")
     out, out_at = _out(out, "out", dt, (T, H, latent_size), dev, stream)
     if T == 0 or B == 0:  # (an empty tensor has no address)
         return out
-    latent_size = int(latent_size)
     need = _workspace_bytes("pattn_latent_workspace_bytes", dev, B, H, latent_size)
     at, size, raw, ext = _scratch(workspace, need, dev, stream)
     args = _pack(_ATTEND_PACK, "pattn_latent_fwd", _ATTEND_PACK.size, q.data_ptr(),
@@ -330,11 +332,13 @@ def latent_expanded_forward(q, k_nope, k_rope, value, query_start_loc, key_start
             D != dn + dr):
         raise ValueError("q, k_nope, k_rope and value must be [num_tokens, heads, nope + rope], "
                          "[num_keys, heads, nope], [num_keys, rope] and [num_keys, heads, value]")
-    B = query_start_loc.shape[0] - 1
+    B = query_start_loc.numel() - 1
+    if B < 0:
+        raise ValueError("query_start_loc must hold num_seqs + 1 numbers")
     qsl_at = _index(query_start_loc, "query_start_loc", _types["int32"], (B + 1,), dev)
     ksl_at = _index(key_start_loc, "key_start_loc", _types["int32"], (B + 1,), dev)
     out, out_at = _out(out, "out", dt, (T, H, dv), dev, stream)
-    if T == 0 or B <= 0:  # (an empty tensor has no address)
+    if T == 0 or B == 0:  # (an empty tensor has no address)
         return out
     if K == 0:  # (likewise: no key is read)
         k_at = v_at = r_at = q_at
