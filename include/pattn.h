@@ -621,7 +621,8 @@ typedef struct {
 
 pattn_status_t pattn_latent_fwd(const pattn_latent_t* args);
 
-/* Workspace bytes pattn_latent_fwd needs (0 if the arguments are invalid). */
+/* Workspace bytes pattn_latent_fwd needs on the current device (0 if the arguments are
+ * invalid).  They follow from latent_size; num_seqs and num_heads are only checked. */
 size_t pattn_latent_workspace_bytes(int num_seqs, int num_heads, int latent_size);
 
 /*

@@ -122,6 +122,12 @@ def _out(x, name, dtype, shape, dev, stream):
     return x, _index(x, name, dtype, shape, dev)
 
 
+def _length(x, what):
+    """Refuses a length that no batch has (None: not given)."""
+    if x is not None and not int(x) >= 0:
+        raise PattnError(1, what)
+
+
 def latent_rope_and_cache(q, latent, k_rope, kv_cache, slot_mapping, positions, cos_sin, *,
                           block_size, kv_dtype=KV_BF16, interleaved=False, latent_norm=None,
                           norm_eps=1e-6, q_out=None, row_out=None, device_status=None,
@@ -270,8 +276,8 @@ def latent_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale
 
     block_table int32 [B, blocks], seq_lens int32 [B], query_start_loc int32 [B + 1]
     as for ``forward``; ``max_query_len``: host int, at least every query length (1
-    selects the layout for single tokens).  ``max_seq_len`` is taken for the likeness
-    with ``forward`` and not needed.  ``workspace``: a Workspace (default: one per
+    selects the layout for single tokens).  ``max_seq_len``: as for ``forward``, whose
+    callers have it; it chooses nothing here and is checked for its sign only.  ``workspace``: a Workspace (default: one per
     stream and host thread).  ``latent_forward.last_ext`` serves
     pattn_read_device_status, which tells (and clears) the status of the latest call
     on that workspace, of whichever operator.  Raises PattnError or ValueError."""
@@ -291,6 +297,8 @@ def latent_forward(q, kv_cache, block_table, seq_lens, query_start_loc, *, scale
     latent_size = int(latent_size)
     if not 0 < latent_size < row:
         raise PattnError(1, "pattn_latent_fwd")
+    _length(max_query_len, "pattn_latent_fwd")
+    _length(max_seq_len, "pattn_latent_fwd")
     out, out_at = _out(out, "out", dt, (T, H, latent_size), dev, stream)
     if T == 0 or B == 0:  # (an empty tensor has no address)
         return out
@@ -316,7 +324,8 @@ def latent_expanded_forward(q, k_nope, k_rope, value, query_start_loc, key_start
     query_start_loc[r] ... and keys key_start_loc[r] ....  Any token and head strides
     that are multiples of 8 elements (k_nope and value may be views of one
     up-projection).  Returns ``out`` [T, H, nope].  ``max_query_len`` and
-    ``max_key_len`` are taken for the likeness with ``forward`` and not needed.
+    ``max_key_len`` choose nothing (the kernel plans from the device's own lengths) and
+    are checked for their signs only.
     ``latent_expanded_forward.last_ext`` serves pattn_read_device_status, as for
     ``latent_forward``.  Raises PattnError or ValueError."""
     dt = _type_of(kv_dtype)
@@ -332,6 +341,8 @@ def latent_expanded_forward(q, k_nope, k_rope, value, query_start_loc, key_start
             D != dn + dr):
         raise ValueError("q, k_nope, k_rope and value must be [num_tokens, heads, nope + rope], "
                          "[num_keys, heads, nope], [num_keys, rope] and [num_keys, heads, value]")
+    _length(max_query_len, "pattn_latent_expanded_fwd")
+    _length(max_key_len, "pattn_latent_expanded_fwd")
     B = query_start_loc.numel() - 1
     if B < 0:
         raise ValueError("query_start_loc must hold num_seqs + 1 numbers")

@@ -30,6 +30,13 @@ def test_a_latent_size_without_a_part_of_the_row(latent_size):
         absorbed(latent_size=latent_size)
 
 
+@pytest.mark.parametrize("call,name", [(absorbed, "max_query_len"), (absorbed, "max_seq_len"),
+                                       (expanded, "max_query_len"), (expanded, "max_key_len")])
+def test_lengths_that_no_batch_has(call, name):
+    with pytest.raises(pa.PattnError):
+        call(**{name: -1})
+
+
 def test_starts_without_a_number():
     with pytest.raises(ValueError):
         expanded(starts=0)
