@@ -251,31 +251,6 @@ __device__ __forceinline__ ExSub ex_sub(const ExProblem& p, const ExItem& it, in
   return u;
 }
 
-__device__ __forceinline__ void ffma2(float& a0, float& a1, float b, float c) {
-  asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
-      "mov.b64 ra, {%0, %1};\n\t"
-      "mov.b64 rb, {%2, %2};\n\t"
-      "mov.b64 rc, {%3, %3};\n\t"
-      "fma.rn.f32x2 ra, ra, rb, rc;\n\t"
-      "mov.b64 {%0, %1}, ra;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b), "f"(c));
-}
-__device__ __forceinline__ void fadd2(float& s0, float& s1, float a0, float a1) {
-  asm("{\n\t.reg .b64 ra, rb;\n\t"
-      "mov.b64 ra, {%0, %1};\n\t"
-      "mov.b64 rb, {%2, %3};\n\t"
-      "add.f32x2 ra, ra, rb;\n\t"
-      "mov.b64 {%0, %1}, ra;\n\t}"
-      : "+f"(s0), "+f"(s1)
-      : "f"(a0), "f"(a1));
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // The weights 2^(x sl2 - ref) of 32 scores, packed in pairs as P; returns their sum.
 template <bool HALF>
 __device__ __forceinline__ float ex_weights(const float (&x)[32], float sl2, float ref,

@@ -192,24 +192,6 @@ struct Sub {
   __device__ bool active(int kt) const { return valid && kt >= x0 && kt < x1; }
 };
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// (a0, a1) * (b, b) + (c, c) on the paired fp32 pipe.
-__device__ __forceinline__ void ffma2(float& a0, float& a1, float b, float c) {
-  asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
-      "mov.b64 ra, {%0, %1};\n\t"
-      "mov.b64 rb, {%2, %2};\n\t"
-      "mov.b64 rc, {%3, %3};\n\t"
-      "fma.rn.f32x2 ra, ra, rb, rc;\n\t"
-      "mov.b64 {%0, %1}, ra;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b), "f"(c));
-}
-
 // Widens rows [row0, row1) of an e4m3 tile, stored as rows of D bytes
 // in the last BLOCK_N x D bytes of a K or V stage, in place into the stage's
 // f16 tile in the 128-byte-swizzled layout: code c of row r goes to d half
@@ -406,17 +388,6 @@ __device__ __forceinline__ bool split_q_tile(unsigned char* q, uint64_t* q_full,
   __syncwarp();
   if ((t & 31) == 0) mbar_arrive(q_conv);
   return true;
-}
-
-// (s0, s1) += (a0, a1)
-__device__ __forceinline__ void fadd2(float& s0, float& s1, float a0, float a1) {
-  asm("{\n\t.reg .b64 ra, rb;\n\t"
-      "mov.b64 ra, {%0, %1};\n\t"
-      "mov.b64 rb, {%2, %3};\n\t"
-      "add.f32x2 ra, ra, rb;\n\t"
-      "mov.b64 {%0, %1}, ra;\n\t}"
-      : "+f"(s0), "+f"(s1)
-      : "f"(a0), "f"(a1));
 }
 
 // (a0, a1) *= (b0, b1)

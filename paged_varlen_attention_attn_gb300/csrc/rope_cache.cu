@@ -58,28 +58,6 @@ struct RopeParams {
   unsigned char axis[128];  // axis of each rotary pair (axes > 1)
 };
 
-template <bool HALF>
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const unsigned u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (HALF) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    } else {
-      x[2 * i] = __uint_as_float(u[i] << 16);
-      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  }
-}
-
-template <bool HALF>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack2<HALF>(x[0], x[1]), pack2<HALF>(x[2], x[3]), pack2<HALF>(x[4], x[5]),
-                    pack2<HALF>(x[6], x[7]));
-}
-
 // Eight values over their scale as e4m3 codes: the fp32 quotient, as in
 // pattn_reshape_and_cache, rounded to nearest even, saturated at +-448, NaN
 // kept.
