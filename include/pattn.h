@@ -509,8 +509,14 @@ pattn_status_t pattn_gather_cache(const void* kv_cache, const int32_t* block_tab
  * they give no layout, this is the reading taken.)
  *
  * Sizes of every entry point below: latent_size a multiple of 128 up to 512,
- * rope_size a multiple of 16 up to 64, block_size a multiple of 16.  As the
- * product p . V defines it, a weight of 0 times an infinity or a NaN is NaN: a
+ * rope_size a multiple of 16 up to 64, block_size a multiple of 16.
+ *
+ * Both attentions hold scores, maxima, sums and outputs in fp32 and round twice: a
+ * weight to the cache's type, half a step of it (2^-8 or 2^-11 relative; an f16
+ * weight below 2^-14 of the largest by 2^-25 of that one), as the tensor cores take
+ * their operands, and the result.  The normaliser sums the weights unrounded.
+ *
+ * As the product p . V defines it, a weight of 0 times an infinity or a NaN is NaN: a
  * non-finite value of a key that the causal mask hides can reach rows of its
  * request.  Keys at or past seq_len and other requests' keys never do.
  */

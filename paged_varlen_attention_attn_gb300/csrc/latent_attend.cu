@@ -15,7 +15,10 @@
 //   O^T (128 dims x R, dc / 128 of them) += V^T P^T, M the dims (the same bytes
 //     read MN-major), N the rows.  O transposed keeps all 128 lanes busy for any R
 //     and takes dc / 128 * R <= 256 TMEM columns (O itself would take all 512).
-// P goes through shared memory as the B operand.
+// P goes through shared memory as the B operand, in the cache's type, which is all
+// that the MMA takes beside 16-bit values; the normaliser sums it in fp32 before that.
+// (bf16: 2.0e-3 from the result in 64 bits in root mean square, relative; 1.7e-3 with P
+// in fp32, which is the rounding of the result alone.  f16, long contexts: 2.1e-4 both.)
 //
 // An MMA costs its issue 34 to 40 cycles however few keys it has, so S (36 of them
 // for 576 dims) wants large tiles, and the copies want several tiles in flight: a
@@ -24,12 +27,13 @@
 // rows two of 64.  (8 x 125 k keys, 32 heads: 200 us with two of 64, 208 with five of 32,
 // 192 so; 64 requests, 128 heads: 90 with two of 64, 92 with four of 32.)
 //
-// Measured: 8 x 125 k keys on 32 heads 187 us, 6.2 TB/s; 64 requests of 512 to 4096 keys
+// Measured: 8 x 125 k keys on 32 heads 188 us, 6.1 TB/s; 64 requests of 512 to 4096 keys
 // on 16 heads 44 (25 for the bytes: the start takes some 10 us and the merge 6), on
-// 128 heads 84; 24 chunks beside 40 single tokens on 32 heads 227 us, 561 TFLOP/s.  The
+// 128 heads 83; 24 chunks beside 40 single tokens on 32 heads 225 us, 565 TFLOP/s.  The
 // last two are bound by a slot's life, with two of them: copy 1550 to 2000 cycles, S
 // 1310 (2100 beside a P V), softmax 1100 and P into shared memory 640 with the waits,
-// P V 690 to 1200.  (Eight softmax warps on half of the keys each: 85 and 229 us.)
+// P V 690 to 1200.  (Eight softmax warps on half of the keys each were no faster: 85 and
+// 229 us beside 84 and 227.)
 //
 // A tile lies as [8 keys][64-element column block][8 x 128 bytes], so that the rows
 // of a page land with one copy whatever the block size: a copy holds its warp for
@@ -40,8 +44,8 @@
 // tiles).  A row tile cut by a share's border leaves unnormalised partials with
 // their max and sum, which a second kernel merges in a fixed order.  In a batch of
 // single tokens with more than 64 heads, the CTAs of a share work side by side
-// on the row tiles of one token, so HBM is read once for all of them (64 requests
-// on 128 heads 87 us, 94 with a share each; on 256 heads 142 and 156).
+// on the row tiles of one token, so HBM is read once for all of them (when this was
+// chosen: 64 requests on 128 heads 87 us, 94 with a share each; on 256 heads 142 and 156).
 //
 // Eight warps: 0-3 softmax and epilogue, 4 and 6 TMA of the cache, 5 TMA of Q and the
 // MMAs of S, 7 the MMAs of P V.
@@ -62,8 +66,7 @@ constexpr int LA_THREADS = 256;
 __host__ __device__ constexpr int la_keys(int R) { return R == 64 ? 64 : 48; }
 constexpr int PAD = 2;                // a row tile's fixed cost, in key tiles
 constexpr int LEAST_SHARE = 3;        // cost of a CTA's share, in key tiles
-constexpr int LA_BOX = 16;            // cache rows of a copy (runs of 32 took as long: 87 us
-                                      // for 64 requests of 128 heads)
+constexpr int LA_BOX = 16;            // cache rows of a copy (runs of 32 took as long)
 constexpr int LA_AHEAD = 1;           // tiles asked for in L2 before their copies
 constexpr float LA_RESCALE_LOG2 = 8.f;
 constexpr int LA_MOST_KEYS = 0x7fffff00;  // of a request: 32 bits hold a few tiles more
@@ -208,8 +211,8 @@ __device__ __forceinline__ Cut la_place(const LaProblem& p, int r, int t0, int q
 
 // Cuts the batch into shares: every CTA sums the requests' costs (integers, so that all
 // agree) and finds the two cuts of its share; the first one leaves all of them for the
-// merge.  (A kernel of its own before them took as long, 50.1 against 50.3 us for 64
-// requests on 16 heads, and is a launch more.)
+// merge.  (When this was chosen a kernel of its own before them took as long, 50.1 us for
+// 64 requests on 16 heads against 50.3 without it, and it is a launch more.)
 __device__ __forceinline__ void la_plan(const LaProblem& p, int share, unsigned long long* warp_sums,
                                         Cut* mine, int* shares_out, unsigned* status) {
   const int tid = threadIdx.x;
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     // descriptors are made of the same in all lanes and known to be (reductions over
     // the warp), and the elected lane issues: an MMA of S then takes 34 cycles (M 64, N
     // 64; its operands take 32 to read).  With lane 0 in place of the elected one it
-    // took 54, from a branch for one lane 50 to 71.
+    // took 54, from a branch for one lane 46 to 71.
     const bool scores = warp == 5;
     const unsigned lead = elect_one();
     constexpr unsigned idesc_s = make_idesc_f16(64, C::KEYS, !HALF, false);

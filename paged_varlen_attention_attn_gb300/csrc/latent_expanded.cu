@@ -21,10 +21,15 @@
 // tiles are 64 keys, each sub-tile has two score buffers in TMEM (4 x 64 columns beside
 // the 2 x dv of O), and both sub-tiles' MMAs on a tile follow each other at once: S_A,
 // S_B of tile j + 1, then P V_A, P V_B of tile j, from a warp each.  K and V then have
-// three stages, and the softmax of a tile runs under the MMAs of its neighbours: 1806
-// us, 1.25 PFLOP/s.  The price is S at N 64, which reads operands for 48 cycles an MMA
-// against 32 of the tensor core, and bounds it now.  (4 chunks of 2048 behind 6144, 16
-// heads: 476 us, 1.26 PFLOP/s; 6 short requests 7.6 us on the GPU.)
+// three stages, and the softmax of a tile runs under the MMAs of its neighbours: 1780
+// to 1810 us, 1.25 PFLOP/s.  The price is S at N 64, which reads operands for 48 cycles
+// an MMA against 32 of the tensor core, and bounds it now.  (4 chunks of 2048 behind
+// 6144, 16 heads: 469 to 477 us, 1.27 PFLOP/s; 6 short requests 7.7 us on the GPU.  Heads
+// of 64, rotary 64, the same prompts: 1175 us, 1.15 PFLOP/s.)
+//
+// P is rounded to the operands' type, as the tensor core takes it; its sum is not.  (bf16:
+// 2.1e-3 from the result in 64 bits in root mean square, relative, where the rounding of
+// the result alone is 1.6e-3; f16 2.9e-4 and 2.1e-4.)
 //
 // Rotary parts shorter than 64 are widened with zeros by TMA (a box that reaches
 // past the row), so S is always a whole number of 64-element column blocks.
