@@ -216,7 +216,8 @@ int pattn_decode_splits(const pattn_ext_t* ext, int num_heads, int num_kv_heads,
                         int block_size, int window);
 
 /*
- * Reads and clears the device status word of ext->workspace.  Synchronises
+ * Reads and clears the device status word of ext->workspace (workspace_bytes as
+ * for the call: calls of few CTAs leave more words behind it).  Synchronises
  * ext->stream.  Returns PATTN_OK, PATTN_ERR_BAD_METADATA or
  * PATTN_ERR_DEVICE_TIMEOUT for the calls since the last read (each
  * pattn_varlen_fwd call first clears the word on its stream), or

@@ -633,8 +633,10 @@ pattn_status_t pattn_read_device_status(const pattn_ext_t* ext) {
     return PATTN_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return PATTN_ERR_CUDA;
   const unsigned words = host >> STATUS_WORDS_SHIFT;
-  if (words > 0 && words <= MAX_STATUS_WORDS &&
-      ext->workspace_bytes >= sizeof(WsHeader) + words * sizeof(unsigned)) {
+  if (words > 0 && words <= MAX_STATUS_WORDS) {
+    // (no answer rather than half of one)
+    if (ext->workspace_bytes < sizeof(WsHeader) + words * sizeof(unsigned))
+      return PATTN_ERR_INVALID_ARGUMENT;
     unsigned more[MAX_STATUS_WORDS];
     if (cudaMemcpyAsync(more, hdr + 1, words * sizeof(unsigned), cudaMemcpyDeviceToHost, st) !=
             cudaSuccess ||

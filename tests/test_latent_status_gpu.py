@@ -66,6 +66,16 @@ def test_a_timeout_does_not_stay_behind_for_other_calls(wlib):
         assert _status(wlib, op) == 0
 
 
+def test_the_status_of_part_of_a_workspace_is_refused():
+    c = Dense(6, dn=128, dr=64, device=DEV, **FEW)
+    c.run()
+    whole = pa.latent_expanded_forward.last_ext
+    part = pa.Ext.from_buffer_copy(whole)
+    part.workspace_bytes = 256
+    assert pa.pattn_read_device_status(part) == 1
+    assert pa.pattn_read_device_status(whole) == 0
+
+
 def test_bad_metadata_of_few_items():
     c = Dense(5, dn=128, dr=64, device=DEV, **FEW)
     c.key_starts[2] += 1
